@@ -239,6 +239,94 @@ mla_status mla_prefill_attention(const void *q_nope, const void *q_rope, const v
 mla_status mla_decode_plan_host(const int32_t *seq_lens, int B, int H, int topk, mla_kv_dtype kv_dtype,
                                 int num_sms, void *workspace_host, size_t ws_bytes);
 
+/* ------------------------------------------------------------------------------------------
+ * Several tokens per request: the calls of one speculative decoding step.  T drafted tokens
+ * per request form a tree (each token's parent is an earlier drafted token or the request's
+ * last committed token).  Their queries and keys are rotated (mla_rope), their entries join
+ * the cache (mla_cache_write), every drafted token attends to the request's cache and to the
+ * drafted tokens it descends from, and mla_verify_draft decides which of them stand.  The
+ * entries of those that stand are then written again at their final positions
+ * (mla_cache_write with positions taken from mla_verify_draft's depths).  mla_cache_read
+ * brings a cached prefix back as the [L][576] entries mla_prefill_decompress takes.
+ * A call over zero tokens (N = 0) is valid and enqueues nothing.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Which values of a rotated part form the pairs (a, b): neighbours (2j, 2j + 1), or values j
+ * and j + d_rot / 2. */
+typedef enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 } mla_rope_layout;
+
+/* Rotary positions of part of every head (the decoupled-RoPE query and key of "MLA 在极长上下文
+ * 下的显存带宽突围": only the last d_rot values of a head carry positions).  Row (n, h) of x
+ * holds d_pass values that pass unchanged, then d_rot values in d_rot / 2 pairs; pair j of
+ * token n turns by theta = positions[n] * freqs[j]:
+ *   (a, b) -> mscale * (a cos theta - b sin theta,  a sin theta + b cos theta),
+ * computed in fp32 and rounded once to bf16.  The angle is reduced exactly (64-bit fixed
+ * point), so positions up to 2^31 keep fp32 accuracy; freqs is fp64 (radians per position),
+ * which is where a long context's scaling goes; a negative position turns backwards.
+ * x, out_pass, out_rot: bf16, values of a row adjacent, rows placed by the given token and
+ * head strides (in elements).  out_pass may be NULL (the passing part is not copied), and
+ * out_rot may be x's own rotated part (rotation in place; any other overlap is undefined).
+ * d_rot even and >= 2, d_pass >= 0; positions int32 [N], freqs fp64 [d_rot / 2].  16-byte
+ * aligned rows with d_pass a multiple of 8 and d_rot of 16 take the vector path. */
+mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t N, int H, int d_pass,
+                    int d_rot, mla_rope_layout layout, const int32_t *positions, const double *freqs, float mscale,
+                    void *out_pass, int64_t pass_token_stride, int64_t pass_head_stride, void *out_rot,
+                    int64_t rot_token_stride, int64_t rot_head_stride, void *stream);
+
+/* Cache write of many tokens (a ragged batch's prompts, or drafted tokens): token n of
+ * request requests[n] (NULL: request n) goes to that request's logical position positions[n],
+ * page block_table[request][position / 64], row position % 64.  kv bf16 [N][576] with row
+ * stride kv_stride elements: latent (512) | key (64), as a down-projection leaves them.
+ *   latent: with norm_weight (bf16 [512]) first y = x / sqrt(mean(x^2) + norm_eps) * weight
+ *           in fp32, otherwise y = x;
+ *   key:    with freqs (fp64 [32]) rotated as by mla_rope at rope_positions[n] (NULL:
+ *           positions[n]; a drafted token's place in its tree differs from its slot).
+ * A bf16 cache receives y and the key rounded once to bf16.  An FP8 record receives, per 128
+ * latent channels, scale = max|y| / 448 (1 for a zero block) and the e4m3 codes nearest to
+ * y / scale (fp32 division, clamped to +-448), and the key in bf16, as mla_cache_append does.
+ * positions[n] < 0 skips token n.  A request outside [0, num_requests), a position beyond the
+ * block table or a page id outside [0, num_pages) skips the token and records MLA_ERR_INDEX
+ * in *device_status (optional).  cache and kv rows 16-byte aligned (kv_stride a multiple of
+ * 8); values finite; two tokens of one call must not share a row. */
+mla_status mla_cache_write(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages, const int32_t *block_table,
+                           int num_requests, int max_pages, const int32_t *requests, const int32_t *positions,
+                           const void *kv, int64_t kv_stride, int64_t N, const void *norm_weight, float norm_eps,
+                           const double *freqs, const int32_t *rope_positions, mla_rope_layout layout, float mscale,
+                           int32_t *device_status, void *stream);
+
+/* Cache read, the way back: entries[n][0..576) = the entry at logical position positions[n]
+ * of request requests[n] (NULL: request n), bf16; an FP8 record is dequantised as
+ * bf16(code * scale) (fp32 product).  entries has row stride entries_stride elements (a
+ * multiple of 8, rows 16-byte aligned).  Skipped tokens (negative or unmapped positions, as
+ * above) leave their row of entries as it was. */
+mla_status mla_cache_read(const void *cache, mla_kv_dtype kv_dtype, int64_t num_pages, const int32_t *block_table,
+                          int num_requests, int max_pages, const int32_t *requests, const int32_t *positions,
+                          int64_t N, void *entries, int64_t entries_stride, int32_t *device_status, void *stream);
+
+/* Verification of a drafted tree against the target's probabilities.  Token i of request b
+ * is tokens[b][i], drawn after its parent parents[b][i] (an earlier token, or -1: the last
+ * committed token; NULL: a chain, parent i - 1).  target [B][T + 1][V]: row 0 the target's
+ * distribution after the last committed token, row i + 1 after drafted token i.  draft
+ * [B][T][V]: the distribution token i was drawn from, or NULL where the draft is certain of
+ * its token (the residual then only loses that token).  uniforms [B][T + 1] in [0, 1).
+ * The walk starts at the last committed token with P = its target row and mass M = 1, and
+ * takes the tokens in order.  A token x whose parent is where the walk stands is accepted if
+ *   u_i q(x) M < P(x):  the walk moves there (P = its target row, M = 1);
+ * otherwise P = max(P - M q, 0) and M = sum P, the residual distribution.  At the end
+ * next_token is the first v with sum_{w <= v} P(w) > u_T sum P.  Where nothing of P is left
+ * (draft and target agree), P is the target row where the walk stands; -1 if that is empty.
+ * Sums are exact 58-bit fixed point, so nothing depends on an order of additions.
+ * num_accepted [B]; depths [B][T]: 0, 1, ... for the accepted tokens in order, -1 for the
+ * others; next_token [B].  tree_lens [B] (NULL: T): drafted tokens that count, the others
+ * are never accepted.  A token id outside [0, V) is rejected with its residual unchanged, a
+ * tree_lens outside [0, T] is clamped; both record MLA_ERR_INDEX in *device_status
+ * (optional).  1 <= T <= 64, 1 <= V <= 2^20.  Probabilities fp32, rows adding up to about 1;
+ * values that are negative or NaN count as 0, above 1 as 1. */
+mla_status mla_verify_draft(const float *target, const float *draft, const int32_t *tokens, const int32_t *parents,
+                            const int32_t *tree_lens, const float *uniforms, int B, int T, int V,
+                            int32_t *num_accepted, int32_t *depths, int32_t *next_token, int32_t *device_status,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,7 @@ STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
                 3: "MLA_ERR_WORKSPACE", 4: "MLA_ERR_CUDA", 5: "MLA_ERR_INDEX",
                 6: "MLA_ERR_TIMEOUT", 7: "MLA_ERR_RANGE"}
 KV_BF16, KV_FP8 = 0, 1
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 
 _lock = threading.Lock()
 _lib = None
@@ -67,6 +68,14 @@ def lib():
             L.mla_absorb_query.restype = I
             L.mla_project_output.argtypes = [P, P, I, I, P, P, P]
             L.mla_project_output.restype = I
+            L.mla_rope.argtypes = [P, I64, I64, I64, I, I, I, I, P, P, F, P, I64, I64, P, I64, I64, P]
+            L.mla_rope.restype = I
+            L.mla_cache_write.argtypes = [P, I, I64, P, I, I, P, P, P, I64, I64, P, F, P, P, I, F, P, P]
+            L.mla_cache_write.restype = I
+            L.mla_cache_read.argtypes = [P, I, I64, P, I, I, P, P, I64, P, I64, P, P]
+            L.mla_cache_read.restype = I
+            L.mla_verify_draft.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P, P]
+            L.mla_verify_draft.restype = I
             L.mla_decode_status.argtypes = [P, SZ, P]
             L.mla_decode_status.restype = I
             L.mla_decode_inject_stall.argtypes = [I]
@@ -388,6 +397,265 @@ def inject_stall(enable: bool) -> None:
 def status(ws: Workspace, stream=None) -> int:
     """Synchronise and return (and clear) the device-side status code of the workspace."""
     return int(lib().mla_decode_status(ws.ptr(), ws.nbytes, _stream(stream)))
+
+
+# ---- several tokens per request: rotary positions, cache write and read, verification ----
+# These take tensors of any one CUDA device (the launch goes to that device's current stream,
+# or to `stream`) and allocate the outputs they are not given.
+
+def _device_of(*named):
+    """The CUDA device that all given tensors (name, tensor or None) live on."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    return dev
+
+
+class _Same:
+    """Stands for torch.cuda.device(d) where d is the current device already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _Same()
+
+
+def _on(dev):
+    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _new(shape, dtype, dev, stream):
+    """An output tensor; memory that a stream other than the current one writes is recorded on it."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _ints(t, shape, name):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
+
+
+def _status_word(t):
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1 or not t.is_contiguous()):
+        raise ValueError("device_status must be a contiguous int32 tensor")
+
+
+def _layout(layout) -> int:
+    try:
+        return ROPE_LAYOUTS[layout]
+    except (KeyError, TypeError):
+        raise ValueError(f"layout must be 'interleaved' or 'half', not {layout!r}") from None
+
+
+def _freqs(freqs, d_rot):
+    if freqs.dtype != torch.float64 or tuple(freqs.shape) != (d_rot // 2,) or not freqs.is_contiguous():
+        raise ValueError(f"freqs must be contiguous float64 [{d_rot // 2}]")
+
+
+def rope_frequencies(d_rot: int = 64, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(freqs float64 [d_rot/2] in radians per position, mscale) for rope() and cache_write().
+
+    f_j = base^(-2j/d_rot), stretched for contexts beyond the trained length by `factor`:
+    'none'; 'linear' (f / factor: positions interpolated); 'ntk' (base * factor^(d/(d-2)): the
+    highest frequency kept, the lowest divided by factor); 'yarn' (frequencies that turn more
+    than beta_fast times over the trained length kept, those below beta_slow turns divided by
+    factor, a linear ramp over j between; mscale = 0.1 ln factor + 1 on the rotated values).
+    """
+    import math
+    if d_rot < 2 or d_rot % 2 or not base > 1.0 or not (math.isfinite(factor) and factor >= 1.0):
+        raise ValueError("d_rot must be even and >= 2, base > 1, factor finite and >= 1")
+    j = torch.arange(d_rot // 2, dtype=torch.float64)
+    f = base ** (-2.0 * j / d_rot)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ntk":
+        if d_rot < 4:
+            raise ValueError("'ntk' needs d_rot >= 4")
+        f = (base * factor ** (d_rot / (d_rot - 2.0))) ** (-2.0 * j / d_rot)
+    elif scaling == "yarn":
+        if trained_length < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("'yarn' needs trained_length >= 1 and beta_fast > beta_slow > 0")
+
+        def place(turns):  # the j whose frequency makes that many turns over the trained length
+            return d_rot * math.log(trained_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo, hi = max(math.floor(place(beta_fast)), 0), min(math.ceil(place(beta_slow)), d_rot - 1)
+        divided = ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f / factor * divided + f * (1.0 - divided)
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling != "none":
+        raise ValueError(f"scaling must be 'none', 'linear', 'ntk' or 'yarn', not {scaling!r}")
+    return f.to(device if device is not None else "cuda"), mscale
+
+
+def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pass=None, out_rot=None,
+         copy_pass: bool = True, stream=None):
+    """Rotary positions of the last 2 len(freqs) values of every head: x bf16 [N,H,D] (rows of any
+    stride, values adjacent), positions int32 [N], freqs float64 -> (x[..., :D-d] copied or None,
+    the rotated part), bf16 [N,H,D-d] and [N,H,d].  copy_pass=False leaves the first part out;
+    out_rot may be x[..., D-d:] itself (rotation in place)."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3:
+        raise ValueError("x must be bf16 [N,H,D]")
+    N, H, D = x.shape
+    d_rot = 2 * freqs.numel()
+    d_pass = D - d_rot
+    if d_rot < 2 or d_pass < 0:
+        raise ValueError(f"x has {D} values per head, freqs turns {d_rot}")
+    dev = _device_of(("x", x), ("positions", positions), ("freqs", freqs), ("out_pass", out_pass), ("out_rot", out_rot))
+    _ints(positions, (N,), "positions")
+    _freqs(freqs, d_rot)
+    with _on(dev):
+        if out_pass is None and copy_pass and d_pass > 0:
+            out_pass = _new((N, H, d_pass), torch.bfloat16, dev, stream)
+        elif not copy_pass:
+            out_pass = None
+        if out_rot is None:
+            out_rot = _new((N, H, d_rot), torch.bfloat16, dev, stream)
+        for t, n, d in ((out_pass, "out_pass", d_pass), (out_rot, "out_rot", d_rot)):
+            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (N, H, d)):
+                raise ValueError(f"{n} must be bf16 [{N},{H},{d}]")
+        for t, n in ((x, "x"), (out_pass, "out_pass"), (out_rot, "out_rot")):
+            if t is not None and t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+                raise ValueError(f"{n} must have unit stride within a row")
+        ps = out_pass.stride() if out_pass is not None else (0, 0)
+        rs, xs = out_rot.stride(), x.stride()
+        if N and H:
+            _check("mla_rope", lib().mla_rope(
+                _ptr(x), xs[0], xs[1], N, H, d_pass, d_rot, _layout(layout), _ptr(positions), _ptr(freqs),
+                float(mscale), _ptr(out_pass), ps[0], ps[1], _ptr(out_rot), rs[0], rs[1], _stream(stream)))
+    return out_pass, out_rot
+
+
+def _cache_kind(cache) -> int:
+    if cache.dtype == torch.bfloat16 and tuple(cache.shape[1:]) == (64, 576):
+        kv = KV_BF16
+    elif cache.dtype == torch.uint8 and tuple(cache.shape[1:]) == (64, 656):
+        kv = KV_FP8
+    else:
+        raise ValueError("cache must be bf16 [P,64,576] or uint8 [P,64,656]")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    return kv
+
+
+def _tokens(block_table, requests, positions):
+    """N after checks of the block table and the tokens' places."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous int32 [B,max_pages]")
+    if positions.dim() != 1:
+        raise ValueError("positions must be int32 [N]")
+    N = positions.shape[0]
+    _ints(positions, (N,), "positions")
+    if requests is not None:
+        _ints(requests, (N,), "requests")
+    return N
+
+
+def _entry_rows(t, N, name):
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (N, 576) or (N and t.stride(1) != 1):
+        raise ValueError(f"{name} must be bf16 [{N},576] with unit stride within a row")
+    return t.stride(0) if N > 1 else 576
+
+
+def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_positions=None,
+                layout="interleaved", mscale: float = 1.0, norm_weight=None, norm_eps: float = 1e-6,
+                device_status=None, stream=None):
+    """Writes many tokens' entries: token n (kv bf16 [N,576]: latent | key) goes to position
+    positions[n] (< 0 skips) of request requests[n] (None: request n) of the paged cache, bf16
+    [P,64,576] or uint8 FP8 records [P,64,656] (quantised on the way in).  With norm_weight
+    (bf16 [512]) the latent is RMS-normalised first; with freqs (float64 [32]) the key is rotated
+    at rope_positions (None: positions).  device_status: optional int32 [1] for MLA_ERR_INDEX."""
+    dev = _device_of(("cache", cache), ("block_table", block_table), ("requests", requests),
+                     ("positions", positions), ("kv", kv), ("freqs", freqs), ("rope_positions", rope_positions),
+                     ("norm_weight", norm_weight), ("device_status", device_status))
+    kind = _cache_kind(cache)
+    N = _tokens(block_table, requests, positions)
+    stride = _entry_rows(kv, N, "kv")
+    if freqs is not None:
+        _freqs(freqs, 64)
+    if rope_positions is not None:
+        if freqs is None:
+            raise ValueError("rope_positions without freqs")
+        _ints(rope_positions, (N,), "rope_positions")
+    if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or tuple(norm_weight.shape) != (512,)
+                                    or not norm_weight.is_contiguous()):
+        raise ValueError("norm_weight must be contiguous bf16 [512]")
+    _status_word(device_status)
+    with _on(dev):
+        _check("mla_cache_write", lib().mla_cache_write(
+            _ptr(cache), kind, cache.shape[0], _ptr(block_table), block_table.shape[0], block_table.shape[1],
+            _ptr(requests), _ptr(positions), _ptr(kv), stride, N, _ptr(norm_weight), float(norm_eps), _ptr(freqs),
+            _ptr(rope_positions), _layout(layout), float(mscale), _ptr(device_status), _stream(stream)))
+    return cache
+
+
+def cache_read(cache, block_table, requests, positions, entries=None, device_status=None, stream=None):
+    """Reads many tokens' entries back: bf16 [N,576], row n = position positions[n] of request
+    requests[n] (None: request n); FP8 records are dequantised.  Rows of skipped tokens (negative
+    or unmapped positions) stay as they were in `entries` (undefined where it is allocated here)."""
+    dev = _device_of(("cache", cache), ("block_table", block_table), ("requests", requests),
+                     ("positions", positions), ("entries", entries), ("device_status", device_status))
+    kind = _cache_kind(cache)
+    N = _tokens(block_table, requests, positions)
+    _status_word(device_status)
+    with _on(dev):
+        if entries is None:
+            entries = _new((N, 576), torch.bfloat16, dev, stream)
+        stride = _entry_rows(entries, N, "entries")
+        _check("mla_cache_read", lib().mla_cache_read(
+            _ptr(cache), kind, cache.shape[0], _ptr(block_table), block_table.shape[0], block_table.shape[1],
+            _ptr(requests), _ptr(positions), N, _ptr(entries), stride, _ptr(device_status), _stream(stream)))
+    return entries
+
+
+def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None, tree_lens=None,
+                 device_status=None, stream=None):
+    """Which drafted tokens stand, and the next token: target_probs fp32 [B,T+1,V] (row 0 after
+    the last committed token, row i+1 after drafted token i), draft_probs fp32 [B,T,V] (or None:
+    the draft is certain of its tokens), draft_tokens int32 [B,T], uniforms fp32 [B,T+1] in
+    [0,1), parents int32 [B,T] (-1: the last committed token; None: a chain), tree_lens int32 [B]
+    -> (num_accepted int32 [B], depths int32 [B,T]: place among the accepted tokens or -1,
+    next_token int32 [B])."""
+    dev = _device_of(("target_probs", target_probs), ("draft_probs", draft_probs), ("draft_tokens", draft_tokens),
+                     ("uniforms", uniforms), ("parents", parents), ("tree_lens", tree_lens),
+                     ("device_status", device_status))
+    if draft_tokens.dim() != 2 or target_probs.dim() != 3:
+        raise ValueError("draft_tokens must be int32 [B,T], target_probs fp32 [B,T+1,V]")
+    B, T = draft_tokens.shape
+    V = target_probs.shape[2]
+    _ints(draft_tokens, (B, T), "draft_tokens")
+    for t, shape, name in ((target_probs, (B, T + 1, V), "target_probs"), (draft_probs, (B, T, V), "draft_probs"),
+                           (uniforms, (B, T + 1), "uniforms")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous fp32 {list(shape)}")
+    if parents is not None:
+        _ints(parents, (B, T), "parents")
+    if tree_lens is not None:
+        _ints(tree_lens, (B,), "tree_lens")
+    _status_word(device_status)
+    with _on(dev):
+        num = _new((B,), torch.int32, dev, stream)
+        depths = _new((B, T), torch.int32, dev, stream)
+        nxt = _new((B,), torch.int32, dev, stream)
+        _check("mla_verify_draft", lib().mla_verify_draft(
+            _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(parents), _ptr(tree_lens),
+            _ptr(uniforms), B, T, V, _ptr(num), _ptr(depths), _ptr(nxt), _ptr(device_status), _stream(stream)))
+    return num, depths, nxt
 
 
 def plan_host(seq_lens, B: int, H: int, topk: int = 0, num_sms: int = 148, kv_dtype="bf16"):
