@@ -303,6 +303,41 @@ mla_status mla_cache_read(const void *cache, mla_kv_dtype kv_dtype, int64_t num_
                           int num_requests, int max_pages, const int32_t *requests, const int32_t *positions,
                           int64_t N, void *entries, int64_t entries_stride, int32_t *device_status, void *stream);
 
+/* Tree attention: T drafted tokens per request attend to the cache at once.  The request's
+ * entries, seq_lens[b] of them, end with those of its n = tree_lens[b] drafted tokens (n <= T;
+ * NULL: T): drafted token j sits at position seq_lens[b] - n + j.  Token i attends to every
+ * position before the drafted ones, and to drafted token j if bit j of tree_mask[b][i] is set
+ * (its ancestors and, normally, itself); bits at or beyond n mean nothing.  Per head, as
+ * mla_decode:
+ *     s = softmax_scale (q~ . c + q_R . k_R),  out[b][i][h] = softmax(s) c,  lse = ln sum e^s.
+ * q_nope bf16 [B][T][H][512], q_rope bf16 [B][T][H][64], tree_mask uint64 [B][T], out fp32 or
+ * bf16 (rounded once; the operand type mla_project_output rounds to in any case)
+ * [B][T][H][512], lse fp32 [B][T][H] or NULL.  Tokens i >= n and tokens that attend to nothing
+ * get out = 0 and lse = -inf.  A drafted token's entry may hold anything, NaN included, where
+ * no row attends to it; entries before the drafted ones must be finite.
+ * The rows of a request's T x H queries are taken 128 at a time, so a cache page is read once
+ * per 128 rows: with 16 heads, eight drafted tokens cost about what one does.
+ * tree_lens outside [0, T] or above seq_lens[b] are clamped and recorded as MLA_ERR_INDEX;
+ * other device-side errors as mla_decode.  1 <= T <= 64, 1 <= H <= 128.
+ * Workspace and plan are as mla_decode's (a plan serves any number of calls until seq_lens or
+ * tree_lens change; one workspace serves one call at a time). */
+typedef enum { MLA_OUT_FP32 = 0, MLA_OUT_BF16 = 1 } mla_out_dtype;
+
+size_t mla_decode_tree_workspace_size(int B, int T, int H, int num_sms);
+
+mla_status mla_decode_tree_plan(const int32_t *seq_lens, const int32_t *tree_lens, int B, int T, int H,
+                                mla_kv_dtype kv_dtype, int num_sms, void *workspace, size_t ws_bytes, void *stream);
+
+mla_status mla_decode_tree(const void *workspace, size_t ws_bytes, const void *q_nope, const void *q_rope,
+                           const void *cache, mla_kv_dtype kv_dtype, int64_t num_pages, const int32_t *block_table,
+                           int max_pages, const int32_t *seq_lens, const int32_t *tree_lens, const uint64_t *tree_mask,
+                           int B, int T, int H, float softmax_scale, void *out, mla_out_dtype out_dtype, float *lse,
+                           void *stream);
+
+/* Host twin of mla_decode_tree_plan (as mla_decode_plan_host); num_sms must be > 0. */
+mla_status mla_decode_tree_plan_host(const int32_t *seq_lens, const int32_t *tree_lens, int B, int T, int H,
+                                     mla_kv_dtype kv_dtype, int num_sms, void *workspace_host, size_t ws_bytes);
+
 /* Verification of a drafted tree against the target's probabilities.  Token i of request b
  * is tokens[b][i], drawn after its parent parents[b][i] (an earlier token, or -1: the last
  * committed token; NULL: a chain, parent i - 1).  target [B][T + 1][V]: row 0 the target's

@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "mla_decode.h"
+#include "tc_util.cuh"
 
 namespace mla {
 namespace {
@@ -87,14 +88,16 @@ __device__ Sum3 block_exclusive_scan3(Sum3 v, Sum3 *total, Sum3 *sh) {
     return r;
 }
 
+// B: entries (requests; a tree plan: row tiles of requests), H: rows of an entry.
+template <typename Src>
 __global__ void __launch_bounds__(kPlanThreads)
-plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh, unsigned char *ws, int iu_in_smem) {
+plan_kernel(const Src src, int B, int H, int units, int ovh, unsigned char *ws, int iu_in_smem) {
     __shared__ int64_t sh[kPlanWarps];
     __shared__ Sum3 sh3[kPlanWarps];
     extern __shared__ int32_t s_iu[];  // items' units (when max_items of them fit)
     grid_dep_wait();    // seq_lens may come from the kernel before this one on the stream
     grid_dep_launch();  // the decode kernel may launch now; it waits for this plan to complete
-    const WsLayout L = ws_layout(B, H, units);
+    const WsLayout L = ws_layout(B, H, units, Src::kTree);
     int64_t *req_start = reinterpret_cast<int64_t *>(ws + L.req_start);
     int32_t *num_splits = reinterpret_cast<int32_t *>(ws + L.num_splits);
     int32_t *split_base = reinterpret_cast<int32_t *>(ws + L.split_base);
@@ -105,10 +108,10 @@ plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
 
     // budget positions: the running position stays in a register (req_start is only written)
     int64_t local = 0;
-    for (int b = b0; b < b1; ++b) local += req_cost(req_tiles(seq_lens, topk, b), ovh);
+    for (int b = b0; b < b1; ++b) local += req_cost(req_tiles(src, b), ovh);
     int64_t total;
     const int64_t pos0 = block_exclusive_scan(local, &total, sh);
-    const int64_t per = plan_budget(total, units, topk > 0 ? req_cost(req_tiles(seq_lens, topk, 0), ovh) : 0, B, ovh);
+    const int64_t per = plan_budget(total, units, src.topk > 0 ? req_cost(req_tiles(src, 0), ovh) : 0, B, ovh);
 
     // With at most one request per thread, its cut stays in a register and every thread then
     // emits one work item at a time (a request cut into many pieces is not left to one thread);
@@ -121,7 +124,7 @@ plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
     {
         int64_t pos = pos0;
         for (int b = b0; b < b1; ++b) {
-            const int32_t tiles = req_tiles(seq_lens, topk, b);
+            const int32_t tiles = req_tiles(src, b);
             const ReqSplit r = req_split(pos, tiles, per, units, ovh);
             r_one = r;
             req_start[b] = pos;
@@ -142,7 +145,7 @@ plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
     {
         int64_t pos = pos0;
         for (int b = b0; b < b1; ++b) {
-            const int32_t tiles = req_tiles(seq_lens, topk, b);
+            const int32_t tiles = req_tiles(src, b);
             const ReqSplit r = one_each ? r_one : req_split(pos, tiles, per, units, ovh);
             const int32_t sb = r.n > 1 ? (int32_t)slot : -1;
             num_splits[b] = r.n;
@@ -150,10 +153,10 @@ plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
             if (one_each) {
                 s_off[b] = (int32_t)off;
                 s_rs[b] = r;
-                s_len[b] = req_len(seq_lens, topk, b);
+                s_len[b] = req_len(src, b);
                 s_slot[b] = sb;
             } else {
-                emit_request(ws, L, seq_lens, topk, b, pos, per, units, ovh, (int32_t)off, sb, iu_copy);
+                emit_request(ws, L, src, b, pos, per, units, ovh, (int32_t)off, sb, iu_copy);
             }
             off += r.n;
             if (r.n > 1) {
@@ -173,7 +176,7 @@ plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
                 if (s_off[mid] <= i) lo = mid;
                 else hi = mid - 1;
             }
-            emit_piece(ws, L, lo, s_len[lo], s_rs[lo], i - s_off[lo], per, units, i, s_slot[lo], iu_copy);
+            emit_piece(ws, L, item_entry(src, lo), s_len[lo], s_rs[lo], i - s_off[lo], per, units, i, s_slot[lo], iu_copy);
         }
     }
     __syncthreads();  // item_unit is complete (shared, or global writes of this block)
@@ -188,7 +191,7 @@ plan_kernel(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
     for (int u = threadIdx.x; u <= units; u += kPlanThreads)
         if (u > last) unit_begin[u] = n;
     if (threadIdx.x == 0) {
-        write_header(ws, L, B, H, topk, units, n, per, (int32_t)s_total, (int32_t)r_total, ovh);
+        write_source_header(ws, L, src, B, H, units, n, per, (int32_t)s_total, (int32_t)r_total, ovh);
         *reinterpret_cast<int *>(ws + L.status) = 0;
     }
 }
@@ -208,6 +211,8 @@ constexpr int kCombineThreads = 256;
 constexpr int kCombineCtasPerSm = 2;
 constexpr int kCombineSmemReqs = 1024;  // split requests whose (b, n, s0) are staged in shared memory
 
+// kTree: the entries are row tiles of requests, and the output may be bf16 (rounded once, here).
+template <bool kTree>
 __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm)
 combine_kernel(DecodeArgs a) {
     __shared__ int32_t s_b[kCombineSmemReqs], s_n[kCombineSmemReqs], s_s0[kCombineSmemReqs];
@@ -217,7 +222,7 @@ combine_kernel(DecodeArgs a) {
     const unsigned char *ws = a.ws;
     const int H = a.H;
     const PlanHeader *hd = reinterpret_cast<const PlanHeader *>(ws);
-    const WsLayout L = ws_layout(hd->B, hd->H, hd->num_units);
+    const WsLayout L = ws_layout(hd->B, hd->H, hd->num_units, kTree);
     const int nsr = hd->num_split_reqs;
     if (nsr <= 0) return;
     const int32_t *split_list = reinterpret_cast<const int32_t *>(ws + L.split_list);
@@ -248,6 +253,12 @@ combine_kernel(DecodeArgs a) {
             n = num_splits[b];
             s0 = split_base[b];
         }
+        int64_t orow = (int64_t)b * H + h;  // the output row
+        if constexpr (kTree) {
+            const int rq = b % a.reqs, y = b / a.reqs * kRowTile + h;
+            if (y >= a.T * a.heads) continue;
+            orow = (int64_t)rq * a.T * a.heads + y;
+        }
         const float *plse = part_lse + (int64_t)s0 * H + h;
         const float4 *po = part_o + ((int64_t)s0 * H + h) * (kDLatent / 4);
         float M = -INFINITY, Z = 0.f;
@@ -268,7 +279,10 @@ combine_kernel(DecodeArgs a) {
             float mn = M;
 #pragma unroll
             for (int j = 0; j < 4; ++j) mn = fmaxf(mn, li[j]);
-            if (mn == -INFINITY) continue;  // every piece so far is empty
+            if (mn == -INFINITY) {  // every piece so far is empty
+                if constexpr (kTree) Z += li[0] != li[0] || li[1] != li[1] || li[2] != li[2] || li[3] != li[3] ? NAN : 0.f;
+                continue;
+            }
             const float r = exp2f((M - mn) * kLog2e);  // 0 while M is -inf
             Z *= r;
 #pragma unroll
@@ -292,12 +306,21 @@ combine_kernel(DecodeArgs a) {
             }
             M = mn;
         }
-        const float inv = Z > 0.f ? 1.f / Z : 0.f;
-        float4 *dst = reinterpret_cast<float4 *>(a.out + ((int64_t)b * H + h) * kDLatent);
+        float inv = Z > 0.f ? 1.f / Z : 0.f;
+        if constexpr (kTree) inv = Z != Z ? Z : inv;  // a row whose scores are NaN
+        if (kTree && a.out16) {
+            uint2 *dst = reinterpret_cast<uint2 *>(a.out16 + orow * kDLatent);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            dst[lane + 32 * q] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
-        if (lane == 0) a.lse[(int64_t)b * H + h] = M == -INFINITY ? -INFINITY : M + logf(Z);
+            for (int q = 0; q < 4; ++q)
+                dst[lane + 32 * q] = make_uint2(bf16x2_bits(acc[q].x * inv, acc[q].y * inv),
+                                                bf16x2_bits(acc[q].z * inv, acc[q].w * inv));
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(a.out + orow * kDLatent);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                dst[lane + 32 * q] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+        }
+        if (lane == 0 && (!kTree || a.lse)) a.lse[orow] = M == -INFINITY ? (kTree && Z != Z ? Z : -INFINITY) : M + logf(Z);
     }
 }
 
@@ -308,7 +331,10 @@ int device_sm_count() {
     return sms;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Requests x row tiles fit the work items' words and the tensor maps.
+bool tree_shape_ok(int B, int T, int H) {
+    return B >= 1 && T >= 1 && H >= 1 && T <= kMaxDrafted && H <= kMaxHeads && B <= (1 << 20) / row_tiles(T, H);
+}
 
 // Limit of one pipeline wait in the decode kernel (SM clock cycles), for calls made from now on.
 std::atomic<long long> g_wait_cycles{kDefaultWaitCycles};
@@ -339,6 +365,28 @@ int units_for(int num_sms) {
     return u;
 }
 
+template <typename Src>
+mla_status launch_plan(const Src &src, int B, int H, int units, int ovh, void *workspace, void *stream) {
+    // a programmatic dependent of whatever ran before on the stream (it waits for it before
+    // reading seq_lens); the items' units stay in shared memory when they fit
+    const size_t iu_bytes = sizeof(int32_t) * (size_t)ws_layout(B, H, units, Src::kTree).max_items;
+    const int iu_in_smem = iu_bytes <= 32 * 1024 ? 1 : 0;  // beside the kernel's ~12 KB of static shared memory
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(kPlanThreads, 1, 1);
+    cfg.dynamicSmemBytes = iu_in_smem ? iu_bytes : 0;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan_kernel<Src>, src, B, H, units, ovh, (unsigned char *)workspace, iu_in_smem) ==
+                   cudaSuccess
+               ? MLA_OK
+               : MLA_ERR_CUDA;
+}
+
 mla_status run_decode(const DecodeArgs &a, cudaStream_t stream) {
     int sms = device_sm_count();
     if (sms <= 0) return MLA_ERR_CUDA;
@@ -357,7 +405,8 @@ mla_status run_decode(const DecodeArgs &a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, a.T > 0 ? combine_kernel<true> : combine_kernel<false>, a) != cudaSuccess)
+        return MLA_ERR_CUDA;
     return MLA_OK;
 }
 
@@ -386,25 +435,8 @@ mla_status mla_decode_plan(const int32_t *seq_lens, int B, int H, int topk, mla_
     if (num_sms <= 0) return MLA_ERR_CUDA;
     const int units = units_for(num_sms);
     if (ws_bytes < ws_layout(B, H, units).total) return MLA_ERR_WORKSPACE;
-    // a programmatic dependent of whatever ran before on the stream (it waits for it before
-    // reading seq_lens); the items' units stay in shared memory when they fit
-    const size_t iu_bytes = sizeof(int32_t) * (size_t)ws_layout(B, H, units).max_items;
-    const int iu_in_smem = iu_bytes <= 32 * 1024 ? 1 : 0;  // beside the kernel's ~12 KB of static shared memory
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1, 1, 1);
-    cfg.blockDim = dim3(kPlanThreads, 1, 1);
-    cfg.dynamicSmemBytes = iu_in_smem ? iu_bytes : 0;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const int ovh = piece_overhead(kv_dtype == MLA_KV_FP8_E4M3);
-    return cudaLaunchKernelEx(&cfg, plan_kernel, seq_lens, B, H, topk, units, ovh, (unsigned char *)workspace,
-                              iu_in_smem) == cudaSuccess
-               ? MLA_OK
-               : MLA_ERR_CUDA;
+    return launch_plan(ReqSource{seq_lens, topk}, B, H, units, piece_overhead(kv_dtype == MLA_KV_FP8_E4M3), workspace,
+                       stream);
 }
 
 mla_status mla_decode_plan_host(const int32_t *seq_lens, int B, int H, int topk, mla_kv_dtype kv_dtype,
@@ -417,7 +449,7 @@ mla_status mla_decode_plan_host(const int32_t *seq_lens, int B, int H, int topk,
     const int units = num_units_for(num_sms);
     const WsLayout L = ws_layout(B, H, units);
     if (ws_bytes < L.plan_end) return MLA_ERR_WORKSPACE;
-    build_plan_serial(seq_lens, B, H, topk, units, piece_overhead(kv_dtype == MLA_KV_FP8_E4M3),
+    build_plan_serial(ReqSource{seq_lens, topk}, B, H, units, piece_overhead(kv_dtype == MLA_KV_FP8_E4M3),
                       (unsigned char *)workspace_host);
     *reinterpret_cast<int *>((unsigned char *)workspace_host + L.status) = 0;
     return MLA_OK;
@@ -489,6 +521,85 @@ mla_status mla_decode_sparse(const void *workspace, size_t ws_bytes, const void 
     a.ws_bytes = ws_bytes;
     a.wait_cycles = g_wait_cycles.load();
     a.stall_test = g_stall_test.load();
+    return run_decode(a, (cudaStream_t)stream);
+}
+
+size_t mla_decode_tree_workspace_size(int B, int T, int H, int num_sms) {
+    if (!tree_shape_ok(B, T, H) || num_sms < 0) return 0;
+    if (num_sms == 0) num_sms = device_sm_count();
+    if (num_sms <= 0) return 0;
+    return ws_layout(B * row_tiles(T, H), kRowTile, units_for(num_sms), true).total;
+}
+
+mla_status mla_decode_tree_plan(const int32_t *seq_lens, const int32_t *tree_lens, int B, int T, int H,
+                                mla_kv_dtype kv_dtype, int num_sms, void *workspace, size_t ws_bytes, void *stream) {
+    if (!workspace || !seq_lens || B < 1 || T < 1 || H < 1 || num_sms < 0) return MLA_ERR_INVALID_ARG;
+    if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+    if (!tree_shape_ok(B, T, H)) return MLA_ERR_UNSUPPORTED;
+    if (num_sms == 0) num_sms = device_sm_count();
+    if (num_sms <= 0) return MLA_ERR_CUDA;
+    const int units = units_for(num_sms), entries = B * row_tiles(T, H);
+    if (ws_bytes < ws_layout(entries, kRowTile, units, true).total) return MLA_ERR_WORKSPACE;
+    return launch_plan(TreeSource{seq_lens, tree_lens, B, T, H}, entries, kRowTile, units,
+                       piece_overhead(kv_dtype == MLA_KV_FP8_E4M3), workspace, stream);
+}
+
+mla_status mla_decode_tree_plan_host(const int32_t *seq_lens, const int32_t *tree_lens, int B, int T, int H,
+                                     mla_kv_dtype kv_dtype, int num_sms, void *workspace_host, size_t ws_bytes) {
+    if (!workspace_host || !seq_lens || B < 1 || T < 1 || H < 1 || num_sms < 1) return MLA_ERR_INVALID_ARG;
+    if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+    if (!tree_shape_ok(B, T, H)) return MLA_ERR_UNSUPPORTED;
+    const int units = num_units_for(num_sms), entries = B * row_tiles(T, H);
+    const WsLayout L = ws_layout(entries, kRowTile, units, true);
+    if (ws_bytes < L.plan_end) return MLA_ERR_WORKSPACE;
+    build_plan_serial(TreeSource{seq_lens, tree_lens, B, T, H}, entries, kRowTile, units,
+                      piece_overhead(kv_dtype == MLA_KV_FP8_E4M3), (unsigned char *)workspace_host);
+    *reinterpret_cast<int *>((unsigned char *)workspace_host + L.status) = 0;
+    return MLA_OK;
+}
+
+mla_status mla_decode_tree(const void *workspace, size_t ws_bytes, const void *q_nope, const void *q_rope,
+                           const void *cache, mla_kv_dtype kv_dtype, int64_t num_pages, const int32_t *block_table,
+                           int max_pages, const int32_t *seq_lens, const int32_t *tree_lens, const uint64_t *tree_mask,
+                           int B, int T, int H, float softmax_scale, void *out, mla_out_dtype out_dtype, float *lse,
+                           void *stream) {
+    if (!workspace || !q_nope || !q_rope || !cache || !block_table || !seq_lens || !tree_mask || !out)
+        return MLA_ERR_INVALID_ARG;
+    if (B < 1 || T < 1 || H < 1 || max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+    if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+    if (out_dtype != MLA_OUT_FP32 && out_dtype != MLA_OUT_BF16) return MLA_ERR_INVALID_ARG;
+    if (!tree_shape_ok(B, T, H) || num_pages > (int64_t)(INT32_MAX / kPageRows)) return MLA_ERR_UNSUPPORTED;
+    if (!isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(cache) || !aligned16(out)) return MLA_ERR_INVALID_ARG;
+    const int entries = B * row_tiles(T, H);
+    if (ws_bytes < ws_layout(entries, kRowTile, 1, true).plan_end) return MLA_ERR_WORKSPACE;
+    DecodeArgs a;
+    memset(&a, 0, sizeof a);
+    a.ws = (const unsigned char *)workspace;
+    a.status = (int *)((unsigned char *)workspace + ws_layout(1, 1, 1).status);
+    a.q_nope = (const uint16_t *)q_nope;
+    a.q_rope = (const uint16_t *)q_rope;
+    a.cache = (const unsigned char *)cache;
+    a.num_pages = num_pages;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.topk = kTreePlan;
+    a.B = entries;
+    a.H = kRowTile;
+    a.scale_log2 = softmax_scale * kLog2e;
+    a.out = out_dtype == MLA_OUT_FP32 ? (float *)out : nullptr;
+    a.out16 = out_dtype == MLA_OUT_BF16 ? (uint16_t *)out : nullptr;
+    a.lse = lse;
+    a.kv_fp8 = kv_dtype == MLA_KV_FP8_E4M3;
+    a.ws_bytes = ws_bytes;
+    a.wait_cycles = g_wait_cycles.load();
+    a.stall_test = g_stall_test.load();
+    a.T = T;
+    a.reqs = B;
+    a.heads = H;
+    a.tree_mask = (const unsigned long long *)tree_mask;
+    a.tree_lens = tree_lens;
     return run_decode(a, (cudaStream_t)stream);
 }
 

@@ -32,6 +32,12 @@ struct DecodeArgs {
     size_t ws_bytes;
     long long wait_cycles;        // iteration limit of every pipeline wait, in SM clock cycles
     int stall_test;               // nonzero: the MMA issuer first waits on a barrier nothing completes
+    // tree decode (T > 0): B above counts (request, row tile) entries and H is kRowTile; the
+    // queries are [reqs][T][heads][...], the outputs [reqs][T][heads][512] and [reqs][T][heads]
+    int T, reqs, heads;
+    const unsigned long long *tree_mask;  // [reqs][T]: bit j set: token i attends drafted token j
+    const int32_t *tree_lens;     // [reqs] or null (T)
+    uint16_t *out16;              // bf16 output instead of `out`
 };
 
 // Default limit of a pipeline wait: about two seconds of SM clock.  Nothing in a healthy run
@@ -44,9 +50,9 @@ constexpr long long kDefaultWaitCycles = 4000000000LL;
 __device__ __forceinline__ bool plan_matches(const DecodeArgs &a) {
     const PlanHeader *hd = reinterpret_cast<const PlanHeader *>(a.ws);
     if (hd->magic != kPlanMagic || hd->B != a.B || hd->H != a.H || hd->topk != a.topk ||
-        hd->num_units < 1 || ws_layout(hd->B, hd->H, hd->num_units).total > a.ws_bytes)
+        hd->num_units < 1 || ws_layout(hd->B, hd->H, hd->num_units, a.T > 0).total > a.ws_bytes)
         return false;
-    return true;
+    return a.T == 0 || (hd->reserved[0] == a.T && hd->reserved[1] == a.heads);
 }
 
 // Programmatic dependent launch: a kernel launched with programmatic stream serialization

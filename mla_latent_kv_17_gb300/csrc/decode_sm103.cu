@@ -207,6 +207,13 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float *amax) {
 // Largest magnitude an fp16 operand holds (beyond it the conversion gives infinity).
 constexpr float kF16Max = 65504.0f;
 
+// The request of a work item.  A tree item's word also names its row tile (plan.h); dense and
+// top-k items hold the request itself.
+template <bool kTree>
+__device__ __forceinline__ int item_request(int32_t entry) {
+    return kTree ? entry_request(entry) : entry;
+}
+
 // Page p (0 or 1) of the tile starting at token t of item w: its valid rows (0 when the page
 // lies past the item's end) and its physical id (-1 when that id is out of range).
 struct PageRef {
@@ -220,13 +227,14 @@ __device__ __forceinline__ int32_t ld_early(const int32_t *p) {
     asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
+template <bool kTree>
 __device__ __forceinline__ PageRef page_of(const DecodeArgs &a, const WorkItem &w, int t, int p) {
     const int t_p = t + kPageRows * p;
     PageRef r{0, -1};
     if (t_p >= w.t1) return r;
     r.rows = min(kPageRows, w.t1 - t_p);
     const int lp = t_p / kPageRows;
-    const int64_t id = lp < a.max_pages ? (int64_t)ld_early(a.block_table + (int64_t)w.b * a.max_pages + lp) : -1;
+    const int64_t id = lp < a.max_pages ? (int64_t)ld_early(a.block_table + (int64_t)item_request<kTree>(w.b) * a.max_pages + lp) : -1;
     r.id = (id >= 0 && id < a.num_pages) ? id : -1;
     return r;
 }
@@ -363,7 +371,7 @@ struct PageMask {
     uint64_t valid;
     int cnt;
 };
-template <bool kSparse>
+template <bool kSparse, bool kTree>
 __device__ __forceinline__ PageMask page_mask(const DecodeArgs &a, const WorkItem &w, int t, int p, int lane) {
     PageMask m;
     m.cnt = max(0, min(kPageRows, w.t1 - (t + kPageRows * p)));
@@ -371,7 +379,7 @@ __device__ __forceinline__ PageMask page_mask(const DecodeArgs &a, const WorkIte
         const SparseRows r = sparse_rows(a, w, t, p, lane, false);
         m.valid = (uint64_t)r.lo | ((uint64_t)r.hi << 32);
     } else {
-        const PageRef pg = page_of(a, w, t, p);
+        const PageRef pg = page_of<kTree>(a, w, t, p);
         m.valid = pg.id >= 0 && pg.rows > 0 ? (pg.rows >= 64 ? ~0ull : ((1ull << pg.rows) - 1ull)) : 0ull;
     }
     return m;
@@ -464,6 +472,99 @@ __device__ __noinline__ void store_rows(uint32_t tcol, uint8_t *stg, float *obas
     }
 }
 
+// The same for a tree item: rows of 128-row tile `tile` of the request's T x heads query rows.
+// A row that attends nothing is written as zeros whatever its accumulator holds.  kF32: fp32
+// rows (the output, or a partial result); otherwise bf16, two 32-column slices per 128-B line,
+// each value rounded once.
+template <bool kF32>
+__device__ __noinline__ void store_tree_rows(uint32_t tcol, uint8_t *stg, void *obase, float inv, int h, int warp,
+                                             int lane, int rows) {
+    const bool none = inv == 0.f;
+#pragma unroll 1
+    for (int cb = 0; cb < 256; cb += kF32 ? 32 : 64) {
+        if constexpr (kF32) {
+            uint32_t o[32];
+            tmem_ld32(tcol + cb, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = none ? 0.f : __uint_as_float(o[4 * q + i]) * inv;
+                *reinterpret_cast<float4 *>(stg + h * 128 + ((q ^ (h & 7)) * 16)) =
+                    make_float4(f[0], f[1], f[2], f[3]);
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t o[32];
+                tmem_ld32(tcol + cb + 32 * half, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = none ? 0u
+                                    : pack_bf16(__uint_as_float(o[8 * q + 2 * i]) * inv,
+                                                __uint_as_float(o[8 * q + 2 * i + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(stg + h * 128 + (((4 * half + q) ^ (h & 7)) * 16)) =
+                        make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = warp * 32 + 4 * i + (lane >> 3), q = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4 *>(stg + row * 128 + ((q ^ (row & 7)) * 16));
+            if (row < rows)
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(obase) +
+                                           ((int64_t)row * kDLatent + cb) * (kF32 ? 4 : 2) + 16 * q) = v;
+        }
+        __syncwarp();
+    }
+}
+
+// Tree decode: a drafted token's latent is attended by some rows of a tile and masked for
+// others, so a NaN or infinity in it (a branch gone wrong) must not reach the rows that mask
+// it through 0 x NaN.  Rows lo .. hi - 1 of a 64-row latent-half page (4 boxes) lose their
+// non-finite values before PV reads them; the rows that do attend the token still get a NaN,
+// from its score.
+template <bool kF16>
+__device__ __noinline__ void clean_rows(uint8_t *dh, int lo, int hi, int h) {
+    constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
+    for (int i = lo * 32 + h; i < hi * 32; i += 128) {
+        const int row = i / 32, ch = i % 32;
+        uint4 *p = reinterpret_cast<uint4 *>(dh + (ch / 8) * kBox + row * 128 + (ch % 8) * 16);
+        uint4 v = *p;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((w[k] & kExp) == kExp) {
+                w[k] &= 0xFFFF0000u;
+                bad = true;
+            }
+            if ((w[k] & (kExp << 16)) == kExp << 16) {
+                w[k] &= 0xFFFFu;
+                bad = true;
+            }
+        }
+        if (bad) *p = v;
+    }
+}
+
+// Which tokens of the 64 that start at `t` a query row attends: everything before the drafted
+// tokens (which start at `first`), then what its ancestor bits say.
+__device__ __forceinline__ uint64_t tree_row_mask(int t, int first, uint64_t bits) {
+    const int d = first - t;  // tokens of the page before the first drafted one
+    if (d >= 64) return ~0ull;
+    if (d <= -64) return 0ull;
+    if (d <= 0) return bits >> -d;
+    return ((1ull << d) - 1ull) | bits << d;
+}
+
 // Walks the tiles of this cluster's work in order: units cl, cl + ncl, ..., their items
 // (those with tokens), and each item's 128-token tiles.
 struct TileCursor {
@@ -519,6 +620,20 @@ __device__ int next_request(const int32_t *ub, const WorkItem *items, int units,
         if (u < units) nit = ub[u];
     }
     return -1;
+}
+
+// Brings the query rows of a work item's entry into L2.
+template <bool kTree>
+__device__ __forceinline__ void prefetch_query(const DecodeArgs &a, int32_t entry) {
+    int64_t row = (int64_t)entry * a.H;
+    int rows = a.H;
+    if constexpr (kTree) {
+        const int y0 = entry_tile(entry) * kRowTile;
+        row = (int64_t)entry_request(entry) * a.T * a.heads + y0;
+        rows = min(kRowTile, a.T * a.heads - y0);
+    }
+    prefetch_l2(a.q_nope + row * kDLatent, (uint32_t)(rows * kDLatent * 2));
+    prefetch_l2(a.q_rope + row * kDRope, (uint32_t)(rows * kDRope * 2));
 }
 
 // Two e4m3 codes (low byte first) times their block scale, as a packed fp16 pair: the code
@@ -587,7 +702,9 @@ __device__ bool fp8_jobs(const TileCursor &start, int which, F &&f) {
 // tmap_sc: FP8 scales (16-B boxes) or, for kMode 1, the cache in 64-row boxes; tmap_rope:
 // FP8 RoPE (bf16, 128-B swizzle); tmap_qn / tmap_qr:
 // the queries (64 columns x 128 heads of one request, 128-B swizzle).
-template <int kMode>
+// kTree: the rows are 128 of a request's T x heads query rows instead of its heads, each with its
+// own mask over the drafted tokens (modes 0 and 2).
+template <int kMode, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMode == 2 ? kThreadsFp8 : kMode == 1 ? kThreadsSparse : kThreads, 1)
 decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tmap_sc,
                     const __grid_constant__ CUtensorMap tmap_rope, const __grid_constant__ CUtensorMap tmap_qn,
@@ -653,7 +770,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
     }
 
     const PlanHeader *hd = reinterpret_cast<const PlanHeader *>(a.ws);
-    const WsLayout L = ws_layout(hd->B, hd->H, hd->num_units);
+    const WsLayout L = ws_layout(hd->B, hd->H, hd->num_units, kTree);
     const int32_t *unit_begin = reinterpret_cast<const int32_t *>(a.ws + L.unit_begin);
     const WorkItem *items = reinterpret_cast<const WorkItem *>(a.ws + L.items);
     float *part_lse = reinterpret_cast<float *>(const_cast<unsigned char *>(a.ws) + L.part_lse);
@@ -676,7 +793,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         const bool ok = fp8_jobs(start, 2, [&](int kind, uint32_t g, const TileCursor &t) -> bool {
             // a page that was not loaded (past the item's end, or an id out of range) is not
             // expanded; its stage only completes
-            const PageRef pg = page_of(a, t.w, t.t, kind == 1 ? (int)peer : (int)rank);
+            const PageRef pg = page_of<kTree>(a, t.w, t.t, kind == 1 ? (int)peer : (int)rank);
             int raw_bar, half;
             uint32_t raw_phase, region, scale_off, full_bar;
             if (kind == 2) {
@@ -732,7 +849,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
             start.begin(unit_begin, items, units, cl, ncl);
             const bool ok = fp8_jobs(start, warp == 8 ? 0 : 1, [&](int kind, uint32_t g, const TileCursor &t) -> bool {
                 if (kind == 2) {
-                    const PageRef pg = page_of(a, t.w, t.t, (int)rank);  // read before the wait
+                    const PageRef pg = page_of<kTree>(a, t.w, t.t, (int)rank);  // read before the wait
                     if (!wait_bar(c, bar(base, B_OTH_EMPTY), (g & 1u) ^ 1u, false)) return false;
                     const uint32_t rb = bar(base, B_RAW + 3), dst = base + kOffOth;
                     if (pg.rows > 0 && pg.id >= 0) {
@@ -747,7 +864,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     }
                     return true;
                 }
-                const PageRef pg = page_of(a, t.w, t.t, kind == 0 ? (int)rank : (int)peer);
+                const PageRef pg = page_of<kTree>(a, t.w, t.t, kind == 0 ? (int)rank : (int)peer);
                 const DhSlot d = dh_slot<kSparse>(g, kind);
                 if (d.fill > 0 && !wait_bar(c, bar(base, B_DH_EMPTY + d.slot), (d.fill - 1u) & 1u, false))
                     return false;
@@ -796,7 +913,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         mbar_arrive(fb);
                     }
                 } else {
-                    const PageRef pg = page_of(a, t.w, t.t, p);  // read before the wait
+                    const PageRef pg = page_of<kTree>(a, t.w, t.t, p);  // read before the wait
                     if (d.fill > 0 && !warp_wait(c, bar(base, B_DH_EMPTY + d.slot), (d.fill - 1u) & 1u, false))
                         return false;
                     if (lane == 0) {
@@ -889,7 +1006,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         mbar_arrive(fb);
                     }
                 } else {
-                    const PageRef pg = page_of(a, cur.w, cur.t, (int)rank);  // before the wait
+                    const PageRef pg = page_of<kTree>(a, cur.w, cur.t, (int)rank);  // before the wait
                     if (!warp_wait(c, bar(base, B_OTH_EMPTY), (g & 1u) ^ 1u, false)) {
                         ok = false;
                         break;
@@ -935,7 +1052,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
             // wait for any of it.  FP8 records convert the query to fp16 on the way in, which
             // the softmax warps do (B_Q_READY).
             uint32_t qld_phase = 0, qcp_phase = 0;
-            auto load_query = [&](int bq) -> bool {
+            auto load_query = [&](int entry) -> bool {
+                const int bq = item_request<kTree>(entry), y0 = kTree ? entry_tile(entry) * kRowTile : 0;
                 const uint32_t qb = bar(base, B_QLD);
                 for (int round = 0; round < 3; ++round) {
                     if (lane == 0) {
@@ -944,10 +1062,10 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                             const int blk = 3 * round + i;  // 0-3 own half, 4 RoPE, 5-8 other half
                             const uint32_t dst = base + kOffQs + i * kQsBox;
                             if (blk == 4)
-                                tma_load_3d(dst, &tmap_qr, 0, 0, bq, qb);
+                                tma_load_3d(dst, &tmap_qr, 0, y0, bq, qb);
                             else
                                 tma_load_3d(dst, &tmap_qn,
-                                            blk < 4 ? 256 * (int)rank + 64 * blk : 256 * (int)peer + 64 * (blk - 5), 0,
+                                            blk < 4 ? 256 * (int)rank + 64 * blk : 256 * (int)peer + 64 * (blk - 5), y0,
                                             bq, qb);
                         }
                     }
@@ -985,10 +1103,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         }
                         // the next item's query is loaded after this one: bring it into L2 now
                         const int bnext = next_request(unit_begin, items, units, ncl, u, it);
-                        if (bnext >= 0 && lane == 0) {
-                            prefetch_l2(a.q_nope + (int64_t)bnext * a.H * kDLatent, (uint32_t)(a.H * kDLatent * 2));
-                            prefetch_l2(a.q_rope + (int64_t)bnext * a.H * kDRope, (uint32_t)(a.H * kDRope * 2));
-                        }
+                        if (bnext >= 0 && lane == 0) prefetch_query<kTree>(a, bnext);
                     }
                     ++nitem;
                     tc_fence_after();
@@ -1110,7 +1225,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         uint32_t qphase = 0;
         float qmax = 0.f;  // FP8 records: largest query magnitude converted to fp16
         // issues round `round` of request bq's query boxes (thread 0)
-        auto q_round = [&](int bq, int round) {
+        auto q_round = [&](int entry, int round) {
+            const int bq = item_request<kTree>(entry), y0 = kTree ? entry_tile(entry) * kRowTile : 0;
             const uint32_t qb = bar(base, B_QLD);
             mbar_arrive_expect_tx(qb, 3 * kQsBox);
             for (int i = 0; i < 3; ++i) {
@@ -1118,9 +1234,9 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 const int blk = 3 * round + i;
                 const uint32_t dst = base + kOffQs + i * kQsBox;
                 if (blk == 4)
-                    tma_load_3d(dst, &tmap_qr, 0, 0, bq, qb);
+                    tma_load_3d(dst, &tmap_qr, 0, y0, bq, qb);
                 else
-                    tma_load_3d(dst, &tmap_qn, blk < 4 ? 256 * (int)rank + 64 * blk : 256 * (int)peer + 64 * (blk - 5), 0,
+                    tma_load_3d(dst, &tmap_qn, blk < 4 ? 256 * (int)rank + 64 * blk : 256 * (int)peer + 64 * (blk - 5), y0,
                                 bq, qb);
             }
         };
@@ -1194,12 +1310,45 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 const int b = w.b;
                 float *orow;
                 float *lrow;
-                if (w.slot < 0) {
+                // tree: the item's rows, this thread's drafted token, its mask and where the
+                // drafted tokens begin
+                int rows = a.H, first = 0, total = 0;
+                bool live = true;
+                uint64_t tbits = 0;
+                int64_t row0 = 0;  // the item's first output row
+                if constexpr (kTree) {
+                    const int rq = entry_request(b), y0 = entry_tile(b) * kRowTile, token = (y0 + h) / a.heads;
+                    total = max(0, a.seq_lens[rq]);
+                    const int n = tree_len(a.tree_lens, a.seq_lens, a.T, rq);
+                    if (h == 0 && rank == 0 && (n != (a.tree_lens ? a.tree_lens[rq] : a.T) || a.seq_lens[rq] < 0))
+                        record_error(a.status, MLA_ERR_INDEX);  // clamped
+                    rows = min(kRowTile, a.T * a.heads - y0);
+                    live = token < n;
+                    first = total - n;
+                    tbits = live ? a.tree_mask[(int64_t)rq * a.T + token] : 0ull;
+                    row0 = (int64_t)rq * a.T * a.heads + y0;
+                    orow = w.slot < 0 ? a.out : part_o;  // (row 0 of the item is found at its end)
+                    lrow = w.slot >= 0 ? part_lse + (int64_t)w.slot * kRowTile + h : a.lse ? a.lse + row0 + h : nullptr;
+                } else if (w.slot < 0) {
                     orow = a.out + ((int64_t)b * a.H + h) * kDLatent + rank * 256;
                     lrow = a.lse + (int64_t)b * a.H + h;
                 } else {
                     orow = part_o + ((int64_t)w.slot * a.H + h) * kDLatent + rank * 256;
                     lrow = part_lse + (int64_t)w.slot * a.H + h;
+                }
+                if (kTree && w.t1 <= w.t0) {
+                    if (h < rows) {
+                        const int64_t at = (row0 + h) * kDLatent + rank * 256;
+                        for (int q = 0; q < 64; ++q) {
+                            if (a.out16) {
+                                if (q < 32) reinterpret_cast<uint4 *>(a.out16 + at)[q] = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                reinterpret_cast<float4 *>(a.out + at)[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+                        }
+                        if (rank == 0 && lrow) *lrow = -INFINITY;
+                    }
+                    continue;
                 }
                 if (w.t1 <= w.t0) {
                     if (h < a.H) {
@@ -1220,23 +1369,21 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     q_ready = false;
                     // the next item's query is loaded at the end of this one: bring it into L2 now
                     bnext = next_request(unit_begin, items, units, ncl, u, it);
-                    if (bnext >= 0 && threadIdx.x == 0) {
-                        prefetch_l2(a.q_nope + (int64_t)bnext * a.H * kDLatent, (uint32_t)(a.H * kDLatent * 2));
-                        prefetch_l2(a.q_rope + (int64_t)bnext * a.H * kDRope, (uint32_t)(a.H * kDRope * 2));
-                    }
+                    if (bnext >= 0 && threadIdx.x == 0) prefetch_query<kTree>(a, bnext);
                 }
                 float m = -INFINITY, l = 0.f;
                 // which rows of each page attend (warp-collective), read one tile ahead
-                PageMask nm0 = page_mask<kSparse>(a, w, w.t0, 0, lane), nm1 = page_mask<kSparse>(a, w, w.t0, 1, lane);
+                PageMask nm0 = page_mask<kSparse, kTree>(a, w, w.t0, 0, lane), nm1 = page_mask<kSparse, kTree>(a, w, w.t0, 1, lane);
                 for (int t = w.t0, j = 0; t < w.t1; t += kTile, ++j, ++g) {
                     // ================= part A: own page's scores -> weights -> message
                     const int nvalid = min(kTile, w.t1 - t);
                     const PageMask pm0 = nm0, pm1 = nm1;
                     if (t + kTile < w.t1) {
-                        nm0 = page_mask<kSparse>(a, w, t + kTile, 0, lane);
-                        nm1 = page_mask<kSparse>(a, w, t + kTile, 1, lane);
+                        nm0 = page_mask<kSparse, kTree>(a, w, t + kTile, 0, lane);
+                        nm1 = page_mask<kSparse, kTree>(a, w, t + kTile, 1, lane);
                     }
-                    const uint64_t vown = rank == 0 ? pm0.valid : pm1.valid;
+                    uint64_t vown = rank == 0 ? pm0.valid : pm1.valid;
+                    if constexpr (kTree) vown &= tree_row_mask(t + kPageRows * (int)rank, first, tbits);
                     if (!warp_wait(c, bar(base, B_S_FULL), g & 1u, false)) {
                         ok = false;
                         break;
@@ -1334,6 +1481,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         f1 = ex2_approx(r1 - mn);
                         alpha = ex2_approx(m - mn);
                         l = l * alpha + l0 * f0 + l1 * f1;
+                    } else if constexpr (kTree) {
+                        l += l0 + l1;  // 0, or NaN where every token the row attends scores NaN
                     }
                     const bool resc_o = j > 0 && mn > m;
                     m = mn;
@@ -1366,6 +1515,21 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         wrote = true;
                     }
                     if (!ok) break;
+                    if constexpr (kTree) {
+                        // drafted tokens in this tile (the same in every thread of the item)
+                        for (int p = 0; p < 2 && t + kTile > first; ++p) {
+                            const int lo = max(0, first - (t + kPageRows * p)), hi = p == 0 ? pm0.cnt : pm1.cnt;
+                            if (lo >= hi || (p == 0 ? pm0.valid : pm1.valid) == 0ull) continue;
+                            const DhSlot d = dh_slot<kSparse>(g, p == (int)rank ? 0 : 1);
+                            if (!warp_wait(c, bar(base, d.full), d.phase & 1u, false)) {
+                                ok = false;
+                                break;
+                            }
+                            clean_rows<kFp8>(gbase + kOffDh + d.slot * kDhBytes, lo, hi, h);
+                            wrote = true;
+                        }
+                        if (!ok) break;
+                    }
                     if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_smem();
                     // O rescale: the previous tile's PV is done (waited above before the
                     // probability tile was rewritten)
@@ -1394,19 +1558,31 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     break;
                 }
                 tc_fence_after();
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                float inv = l > 0.f ? 1.f / l : 0.f;
+                if constexpr (kTree) inv = !live ? 0.f : l != l ? l : inv;  // NaN: so is the row
                 // Each 32-column slice goes through this CTA's own probability rows (free
                 // until the next tile's weights; the peer never writes them) so that every
                 // warp store covers whole 128-B lines: thread h holds row h, but rows are
                 // 2 KB apart in the output.  Warp w writes back its own rows 32w..32w+31.
                 {
                     uint8_t *stg = ps + rank * kPPage;
-                    float *obase = orow - (int64_t)h * kDLatent;  // row 0 of this item's output
                     if (lane == 0) bulk_wait_read_all();  // this warp's last message has left these rows
                     __syncwarp();
-                    store_rows(trow + kColO, stg, obase, inv, h, warp, lane, a.H);
+                    if constexpr (kTree) {
+                        const int64_t at = (w.slot < 0 ? row0 : (int64_t)w.slot * kRowTile) * kDLatent + rank * 256;
+                        if (w.slot < 0 && a.out16)
+                            store_tree_rows<false>(trow + kColO, stg, a.out16 + at, inv, h, warp, lane, rows);
+                        else
+                            store_tree_rows<true>(trow + kColO, stg, orow + at, inv, h, warp, lane, rows);
+                    } else {
+                        float *obase = orow - (int64_t)h * kDLatent;  // row 0 of this item's output
+                        store_rows(trow + kColO, stg, obase, inv, h, warp, lane, a.H);
+                    }
                 }
-                if (rank == 0 && h < a.H) *lrow = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                if constexpr (kTree) {
+                    if (rank == 0 && h < rows && lrow)
+                        *lrow = !live ? -INFINITY : l > 0.f ? (m + log2f(l)) * kLn2 : l != l ? l : -INFINITY;
+                } else if (rank == 0 && h < a.H) *lrow = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 ++nitem;
                 tc_fence_before();
             }
@@ -1450,11 +1626,15 @@ bool set_smem_attr() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     if (done[dev]) return true;
-    if (cudaFuncSetAttribute(decode_sm103_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+    if (cudaFuncSetAttribute(decode_sm103_kernel<0, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(decode_sm103_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+        cudaFuncSetAttribute(decode_sm103_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(decode_sm103_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+        cudaFuncSetAttribute(decode_sm103_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(decode_sm103_kernel<0, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(decode_sm103_kernel<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
             cudaSuccess) {
         cudaGetLastError();
         return false;
@@ -1478,6 +1658,7 @@ bool make_tmap(CUtensorMap *m, const void *cache, int64_t num_pages, CUtensorMap
 
 // Queries [B][H][cols] bf16 as a 3-D tensor (cols, H, B); boxes of 64 columns x 128 heads of
 // one request, 128-B swizzle.  Heads at or beyond H fall outside the tensor and read zeros.
+// (Tree decode: H is T x heads rows.)
 bool make_tmap_q(CUtensorMap *m, const void *q, int cols, int H, int B) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
@@ -1511,7 +1692,7 @@ int sm103_max_units() {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, decode_sm103_kernel<2>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, decode_sm103_kernel<2, false>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -1543,7 +1724,8 @@ cudaError_t launch_decode_sm103(const DecodeArgs &a, int num_clusters, cudaStrea
     if (!set_smem_attr()) return cudaErrorInvalidValue;
     const dim3 grid(2 * num_clusters);
     CUtensorMap tm, tm_sc, tm_rope, tm_qn, tm_qr;
-    if (!make_tmap_q(&tm_qn, a.q_nope, kDLatent, a.H, a.B) || !make_tmap_q(&tm_qr, a.q_rope, kDRope, a.H, a.B))
+    const int qrows = a.T > 0 ? a.T * a.heads : a.H, qreqs = a.T > 0 ? a.reqs : a.B;
+    if (!make_tmap_q(&tm_qn, a.q_nope, kDLatent, qrows, qreqs) || !make_tmap_q(&tm_qr, a.q_rope, kDRope, qrows, qreqs))
         return cudaErrorInvalidValue;
     if (a.kv_fp8) {
         // records of 656 B: codes as bytes (128-B boxes, a quarter of the latent of 64 rows), the 16-B
@@ -1555,7 +1737,7 @@ cudaError_t launch_decode_sm103(const DecodeArgs &a, int num_clusters, cudaStrea
             !make_tmap(&tm_rope, a.cache, a.num_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kFp8RecordBytes, 64,
                        kPageRows, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-        return launch_pdl(decode_sm103_kernel<2>, grid, kThreadsFp8, stream, tm, tm_sc, tm_rope, tm_qn, tm_qr, a);
+        return launch_pdl(a.T > 0 ? decode_sm103_kernel<2, true> : decode_sm103_kernel<2, false>, grid, kThreadsFp8, stream, tm, tm_sc, tm_rope, tm_qn, tm_qr, a);
     } else if (a.indices) {
         // one-row boxes for tile::gather4
         if (!make_tmap(&tm, a.cache, a.num_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)kDEntry * 2, 64, 1,
@@ -1566,13 +1748,13 @@ cudaError_t launch_decode_sm103(const DecodeArgs &a, int num_clusters, cudaStrea
         if (!make_tmap(&tm_page, a.cache, a.num_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)kDEntry * 2, 64,
                        kPageRows, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-        return launch_pdl(decode_sm103_kernel<1>, grid, kThreadsSparse, stream, tm, tm_page, tm, tm_qn, tm_qr, a);
+        return launch_pdl(decode_sm103_kernel<1, false>, grid, kThreadsSparse, stream, tm, tm_page, tm, tm_qn, tm_qr, a);
     } else {
         // 64-row boxes: one page
         if (!make_tmap(&tm, a.cache, a.num_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)kDEntry * 2, 64,
                        kPageRows, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-        return launch_pdl(decode_sm103_kernel<0>, grid, kThreads, stream, tm, tm, tm, tm_qn, tm_qr, a);
+        return launch_pdl(a.T > 0 ? decode_sm103_kernel<0, true> : decode_sm103_kernel<0, false>, grid, kThreads, stream, tm, tm, tm, tm_qn, tm_qr, a);
     }
     return cudaGetLastError();
 }

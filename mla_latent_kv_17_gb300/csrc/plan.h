@@ -30,6 +30,7 @@ constexpr int kDEntry = 576;
 constexpr int kPageRows = 64;
 constexpr int kFp8RecordBytes = 656;
 constexpr int kMaxHeads = 128;
+constexpr int kMaxDrafted = 64;  // drafted tokens of a request: a row's mask is one 64-bit word
 constexpr int kTileTokens = 128;
 constexpr int kSmsPerUnit = 2;
 constexpr int kMinPieceTiles = 2;
@@ -60,11 +61,13 @@ struct WsLayout {
     int max_items, max_partials, num_units;
 };
 
-MLA_HD WsLayout ws_layout(int B, int H, int num_units) {
+MLA_HD WsLayout ws_layout(int B, int H, int num_units, bool tree = false) {
     WsLayout L;
     L.num_units = num_units;
     L.max_items = B + num_units;
-    L.max_partials = L.max_items;
+    // a tree plan has many (request, row tile) pairs; what is cut is cut at a unit's border, so
+    // the pieces of all cut pairs are at most two per border
+    L.max_partials = tree ? 2 * num_units : L.max_items;
     L.header = 0;
     L.status = 128;  // 4-byte device status word, outside the header
     size_t o = 256;
@@ -96,14 +99,54 @@ MLA_HD int num_units_for(int num_sms) {
     return u < 1 ? 1 : u;
 }
 
-// Tiles request b is planned over (tokens, or index slots for sparse decode).
-MLA_HD int32_t req_len(const int32_t *seq_lens, int topk, int b) {
-    if (topk > 0) return topk;
-    int32_t L = seq_lens[b];
+// Where a plan's lengths come from.  Dense and top-k plans: one entry per request.
+struct ReqSource {
+    static constexpr bool kTree = false;
+    const int32_t *seq_lens;
+    int topk;
+};
+// Tree plans: the T x H query rows of a request (token-major) are cut into tiles of kRowTile
+// rows, and entry v = tile * B + b is tile `tile` of request b: all requests' first tiles, then
+// their second ones, so that the tiles of a request run on different units at about the same
+// time and share the request's cache pages in L2.  A tile past the request's drafted tokens is
+// empty.
+constexpr int kRowTile = 128;
+constexpr int kTreePlan = -1;  // PlanHeader::topk of a tree plan
+MLA_HD int row_tiles(int T, int H) { return (T * H + kRowTile - 1) / kRowTile; }
+struct TreeSource {
+    static constexpr bool kTree = true;
+    const int32_t *seq_lens, *tree_lens;
+    int B, T, H;
+    static constexpr int topk = 0;
+};
+// A tree plan's work item names its request and row tile in one word.
+constexpr int kTileShift = 24;
+MLA_HD int32_t pack_entry(int v, int B) { return (v % B) | (v / B) << kTileShift; }
+MLA_HD int entry_request(int32_t e) { return e & ((1 << kTileShift) - 1); }
+MLA_HD int entry_tile(int32_t e) { return e >> kTileShift; }
+
+// Drafted tokens of request b that count.
+MLA_HD int32_t tree_len(const int32_t *tree_lens, const int32_t *seq_lens, int T, int b) {
+    const int32_t L = seq_lens[b] < 0 ? 0 : seq_lens[b];
+    int32_t n = tree_lens ? tree_lens[b] : T;
+    n = n < 0 ? 0 : n > T ? T : n;
+    return n < L ? n : L;
+}
+
+// Tokens entry b is planned over (or index slots for sparse decode), and tiles of them.
+MLA_HD int32_t req_len(const ReqSource &s, int b) {
+    if (s.topk > 0) return s.topk;
+    int32_t L = s.seq_lens[b];
     return L < 0 ? 0 : L;
 }
-MLA_HD int32_t req_tiles(const int32_t *seq_lens, int topk, int b) {
-    return (req_len(seq_lens, topk, b) + kTileTokens - 1) / kTileTokens;
+MLA_HD int32_t req_len(const TreeSource &s, int v) {
+    const int b = v % s.B, tile = v / s.B;
+    if (tile * kRowTile >= tree_len(s.tree_lens, s.seq_lens, s.T, b) * s.H) return 0;
+    return s.seq_lens[b];
+}
+template <typename S>
+MLA_HD int32_t req_tiles(const S &s, int b) {
+    return (req_len(s, b) + kTileTokens - 1) / kTileTokens;
 }
 // What a piece costs beyond its tiles, in tiles: its query load, pipeline refill and
 // epilogue.  Clock traces of the decode put an item at ~3 tiles of its own mode in both
@@ -192,16 +235,20 @@ MLA_HD int64_t plan_budget(int64_t total_cost, int units, int64_t uniform_cost, 
     return per;
 }
 
-// Piece i of request b (len tokens, cut as r) as work item `item`; unit_copy, when given,
+// The word a work item names entry b of a plan by.
+MLA_HD int32_t item_entry(const ReqSource &, int b) { return b; }
+MLA_HD int32_t item_entry(const TreeSource &s, int v) { return pack_entry(v, s.B); }
+
+// Piece i of a request (`entry`; len tokens, cut as r) as work item `item`; unit_copy, when given,
 // receives the item's unit as well.
-MLA_HD void emit_piece(unsigned char *ws, const WsLayout &L, int b, int32_t len, const ReqSplit &r, int i,
+MLA_HD void emit_piece(unsigned char *ws, const WsLayout &L, int32_t entry, int32_t len, const ReqSplit &r, int i,
                        int64_t per, int units, int32_t item, int32_t slot0, int32_t *unit_copy) {
     WorkItem *items = reinterpret_cast<WorkItem *>(ws + L.items);
     int32_t *item_unit = reinterpret_cast<int32_t *>(ws + L.item_unit);
     int32_t tb, te, u;
     req_piece(r, i, per, units, &tb, &te, &u);
     WorkItem w;
-    w.b = b;
+    w.b = entry;
     w.t0 = tb * kTileTokens;
     const int32_t e = te * kTileTokens;
     w.t1 = e < len ? e : len;
@@ -213,17 +260,18 @@ MLA_HD void emit_piece(unsigned char *ws, const WsLayout &L, int b, int32_t len,
 
 // Writes the pieces of request b (its item offset `off`, its first partial slot `slot0`
 // or -1) into the workspace.
-MLA_HD void emit_request(unsigned char *ws, const WsLayout &L, const int32_t *seq_lens, int topk,
-                         int b, int64_t S, int64_t per, int units, int ovh, int32_t off, int32_t slot0,
-                         int32_t *unit_copy = nullptr) {
-    const int32_t len = req_len(seq_lens, topk, b);
+template <typename Src>
+MLA_HD void emit_request(unsigned char *ws, const WsLayout &L, const Src &src, int b, int64_t S, int64_t per,
+                         int units, int ovh, int32_t off, int32_t slot0, int32_t *unit_copy = nullptr) {
+    const int32_t len = req_len(src, b);
     const int32_t tiles = (len + kTileTokens - 1) / kTileTokens;
     const ReqSplit r = req_split(S, tiles, per, units, ovh);
-    for (int i = 0; i < r.n; ++i) emit_piece(ws, L, b, len, r, i, per, units, off + i, slot0, unit_copy);
+    for (int i = 0; i < r.n; ++i) emit_piece(ws, L, item_entry(src, b), len, r, i, per, units, off + i, slot0, unit_copy);
 }
 
 MLA_HD void write_header(unsigned char *ws, const WsLayout &L, int B, int H, int topk, int units,
-                         int n_items, int64_t per, int n_partials, int n_split_reqs, int ovh) {
+                         int n_items, int64_t per, int n_partials, int n_split_reqs, int ovh, int tree_tokens = 0,
+                         int tree_heads = 0) {
     PlanHeader *hd = reinterpret_cast<PlanHeader *>(ws + L.header);
     hd->magic = kPlanMagic;
     hd->B = B;
@@ -238,6 +286,17 @@ MLA_HD void write_header(unsigned char *ws, const WsLayout &L, int B, int H, int
     hd->num_split_reqs = n_split_reqs;
     hd->piece_overhead = ovh;
     for (int i = 0; i < 4; ++i) hd->reserved[i] = 0;
+    hd->reserved[0] = tree_tokens;
+    hd->reserved[1] = tree_heads;
+}
+
+MLA_HD void write_source_header(unsigned char *ws, const WsLayout &L, const ReqSource &s, int B, int H, int units,
+                                int n_items, int64_t per, int n_partials, int n_split_reqs, int ovh) {
+    write_header(ws, L, B, H, s.topk, units, n_items, per, n_partials, n_split_reqs, ovh);
+}
+MLA_HD void write_source_header(unsigned char *ws, const WsLayout &L, const TreeSource &s, int B, int H, int units,
+                                int n_items, int64_t per, int n_partials, int n_split_reqs, int ovh) {
+    write_header(ws, L, B, H, kTreePlan, units, n_items, per, n_partials, n_split_reqs, ovh, s.T, s.H);
 }
 
 // First item index whose unit is >= u (items are ordered by unit).
@@ -255,9 +314,9 @@ MLA_HD int32_t lower_bound_unit(const int32_t *item_unit, int32_t n, int32_t u) 
 
 // Host planner: the same per-request functions in serial loops.  The device planner
 // (plan kernel) computes the same prefix sums in parallel and writes identical bytes.
-inline void build_plan_serial(const int32_t *seq_lens, int B, int H, int topk, int units, int ovh,
-                              unsigned char *ws) {
-    const WsLayout L = ws_layout(B, H, units);
+template <typename Src>
+inline void build_plan_serial(const Src &src, int B, int H, int units, int ovh, unsigned char *ws) {
+    const WsLayout L = ws_layout(B, H, units, Src::kTree);
     int32_t *num_splits = reinterpret_cast<int32_t *>(ws + L.num_splits);
     int32_t *split_base = reinterpret_cast<int32_t *>(ws + L.split_base);
     int64_t *req_start = reinterpret_cast<int64_t *>(ws + L.req_start);
@@ -267,15 +326,15 @@ inline void build_plan_serial(const int32_t *seq_lens, int B, int H, int topk, i
     int64_t S = 0;
     for (int b = 0; b < B; ++b) {
         req_start[b] = S;
-        S += req_cost(req_tiles(seq_lens, topk, b), ovh);
+        S += req_cost(req_tiles(src, b), ovh);
     }
-    const int64_t per = plan_budget(S, units, topk > 0 ? req_cost(req_tiles(seq_lens, topk, 0), ovh) : 0, B, ovh);
+    const int64_t per = plan_budget(S, units, src.topk > 0 ? req_cost(req_tiles(src, 0), ovh) : 0, B, ovh);
     int32_t off = 0, slots = 0, nsr = 0;
     for (int b = 0; b < B; ++b) {
-        const ReqSplit r = req_split(req_start[b], req_tiles(seq_lens, topk, b), per, units, ovh);
+        const ReqSplit r = req_split(req_start[b], req_tiles(src, b), per, units, ovh);
         num_splits[b] = r.n;
         split_base[b] = r.n > 1 ? slots : -1;
-        emit_request(ws, L, seq_lens, topk, b, req_start[b], per, units, ovh, off, split_base[b]);
+        emit_request(ws, L, src, b, req_start[b], per, units, ovh, off, split_base[b]);
         off += r.n;
         if (r.n > 1) {
             slots += r.n;
@@ -284,7 +343,7 @@ inline void build_plan_serial(const int32_t *seq_lens, int B, int H, int topk, i
     }
     for (int u = 0; u <= units; ++u)
         unit_begin[u] = u == units ? off : lower_bound_unit(item_unit, off, u);
-    write_header(ws, L, B, H, topk, units, off, per, slots, nsr, ovh);
+    write_source_header(ws, L, src, B, H, units, off, per, slots, nsr, ovh);
 }
 
 }  // namespace mla

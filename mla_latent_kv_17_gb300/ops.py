@@ -74,6 +74,14 @@ def lib():
             L.mla_cache_write.restype = I
             L.mla_cache_read.argtypes = [P, I, I64, P, I, I, P, P, I64, P, I64, P, P]
             L.mla_cache_read.restype = I
+            L.mla_decode_tree_workspace_size.argtypes = [I, I, I, I]
+            L.mla_decode_tree_workspace_size.restype = SZ
+            L.mla_decode_tree_plan.argtypes = [P, P, I, I, I, I, I, P, SZ, P]
+            L.mla_decode_tree_plan.restype = I
+            L.mla_decode_tree_plan_host.argtypes = [P, P, I, I, I, I, I, P, SZ]
+            L.mla_decode_tree_plan_host.restype = I
+            L.mla_decode_tree.argtypes = [P, SZ, P, P, P, I, I64, P, I, P, P, P, I, I, I, F, P, I, P, P]
+            L.mla_decode_tree.restype = I
             L.mla_verify_draft.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P, P]
             L.mla_verify_draft.restype = I
             L.mla_decode_status.argtypes = [P, SZ, P]
@@ -623,6 +631,80 @@ def cache_read(cache, block_table, requests, positions, entries=None, device_sta
     return entries
 
 
+class TreeWorkspace:
+    """Device workspace of a tree attention over B requests of T drafted tokens and H heads: its
+    plan, split-KV partials and status word (status() reads it)."""
+
+    def __init__(self, B: int, T: int, H: int, num_sms: int = 0, device=None):
+        self.B, self.T, self.H = int(B), int(T), int(H)
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        with _on(dev):
+            self.nbytes = int(lib().mla_decode_tree_workspace_size(self.B, self.T, self.H, int(num_sms)))
+            if self.nbytes == 0:
+                raise MlaError("mla_decode_tree_workspace_size", 1, "invalid arguments")
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+            self.buf[:256].zero_()  # no plan yet, no error
+
+    def ptr(self):
+        return _ptr(self.buf)
+
+
+def plan_tree(ws: TreeWorkspace, seq_lens, tree_lens=None, num_sms: int = 0, stream=None, kv_dtype="bf16"):
+    """Builds the plan of decode_tree for seq_lens and tree_lens (device int32 [B]; tree_lens
+    None: T); kv_dtype ('bf16' or 'fp8') is the cache layout the attention will read."""
+    dev = _device_of(("seq_lens", seq_lens), ("tree_lens", tree_lens), ("workspace", ws.buf))
+    _ints(seq_lens, (ws.B,), "seq_lens")
+    if tree_lens is not None:
+        _ints(tree_lens, (ws.B,), "tree_lens")
+    with _on(dev):
+        _check("mla_decode_tree_plan", lib().mla_decode_tree_plan(
+            _ptr(seq_lens), _ptr(tree_lens), ws.B, ws.T, ws.H, _kv_code(kv_dtype), int(num_sms), ws.ptr(), ws.nbytes,
+            _stream(stream)))
+    return ws
+
+
+def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens, tree_lens, tree_mask,
+                softmax_scale: float, out=None, lse=None, out_dtype=torch.float32, with_lse: bool = True,
+                stream=None):
+    """Tree attention with the plan in ws: q_nope bf16 [B,T,H,512], q_rope bf16 [B,T,H,64]; cache bf16
+    [P,64,576] or uint8 FP8 records [P,64,656], holding seq_lens[b] entries of request b, the last
+    tree_lens[b] (None: T) of them its drafted tokens'; tree_mask int64 [B,T]: bit j of [b,i] set:
+    token i attends drafted token j.  -> (out fp32 or bf16 [B,T,H,512], lse fp32 [B,T,H] or None)."""
+    B, T, H = ws.B, ws.T, ws.H
+    dev = _device_of(("q_nope", q_nope), ("q_rope", q_rope), ("cache", cache), ("block_table", block_table),
+                     ("seq_lens", seq_lens), ("tree_lens", tree_lens), ("tree_mask", tree_mask), ("out", out),
+                     ("lse", lse), ("workspace", ws.buf))
+    for t, d, name in ((q_nope, 512, "q_nope"), (q_rope, 64, "q_rope")):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (B, T, H, d) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bf16 [{B},{T},{H},{d}]")
+    kind = _cache_kind(cache)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
+            or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be contiguous int32 [{B},max_pages]")
+    _ints(seq_lens, (B,), "seq_lens")
+    if tree_lens is not None:
+        _ints(tree_lens, (B,), "tree_lens")
+    if tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (B, T) or not tree_mask.is_contiguous():
+        raise ValueError(f"tree_mask must be contiguous int64 [{B},{T}]")
+    with _on(dev):
+        if out is None:
+            out = _new((B, T, H, 512), out_dtype, dev, stream)
+        if out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (B, T, H, 512) \
+                or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous fp32 or bf16 [{B},{T},{H},512]")
+        if lse is None and with_lse:
+            lse = _new((B, T, H), torch.float32, dev, stream)
+        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, T, H) or not lse.is_contiguous()):
+            raise ValueError(f"lse must be contiguous fp32 [{B},{T},{H}]")
+        _check("mla_decode_tree", lib().mla_decode_tree(
+            ws.ptr(), ws.nbytes, _ptr(q_nope), _ptr(q_rope), _ptr(cache), kind, cache.shape[0], _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), _ptr(tree_lens), _ptr(tree_mask), B, T, H, float(softmax_scale),
+            _ptr(out), 1 if out.dtype == torch.bfloat16 else 0, _ptr(lse), _stream(stream)))
+    return out, lse
+
+
 def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None, tree_lens=None,
                  device_status=None, stream=None):
     """Which drafted tokens stand, and the next token: target_probs fp32 [B,T+1,V] (row 0 after
@@ -656,6 +738,18 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
             _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(parents), _ptr(tree_lens),
             _ptr(uniforms), B, T, V, _ptr(num), _ptr(depths), _ptr(nxt), _ptr(device_status), _stream(stream)))
     return num, depths, nxt
+
+
+def plan_tree_host(seq_lens, tree_lens, B: int, T: int, H: int, num_sms: int = 148, kv_dtype="bf16"):
+    """Host twin of the tree planner: the plan bytes (numpy uint8) for host lengths."""
+    import numpy as np
+    n = lib().mla_decode_tree_workspace_size(int(B), int(T), int(H), int(num_sms))
+    buf = np.zeros(n, dtype=np.uint8)
+    ints = [None if x is None else np.ascontiguousarray(np.asarray(x, dtype=np.int32)) for x in (seq_lens, tree_lens)]
+    ptrs = [None if x is None else x.ctypes.data_as(ctypes.c_void_p) for x in ints]
+    _check("mla_decode_tree_plan_host", lib().mla_decode_tree_plan_host(
+        *ptrs, int(B), int(T), int(H), _kv_code(kv_dtype), int(num_sms), buf.ctypes.data_as(ctypes.c_void_p), n))
+    return buf
 
 
 def plan_host(seq_lens, B: int, H: int, topk: int = 0, num_sms: int = 148, kv_dtype="bf16"):

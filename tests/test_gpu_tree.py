@@ -1,0 +1,206 @@
+"""Tree attention on the GPU against its 64-bit definition, with bounds derived in tree_ref."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from guards import Guarded
+from mla_latent_kv_17_gb300 import inputs, ops
+from planview import parse
+import tree_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from mla_latent_kv_17_gb300 import build
+    build.build()
+    ops.lib()
+
+
+def make(B, T, H, contexts, lens=None, kv="bf16", seed=0, chain=False, q_scale=1.0):
+    """Requests of contexts[b] committed tokens and lens[b] drafted ones, shuffled pages, NaN behind
+    each request's last token, a random tree per request."""
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.full((B,), T, dtype=torch.int32) if lens is None else torch.tensor(lens, dtype=torch.int32)
+    seq = torch.tensor(contexts, dtype=torch.int32) + lens
+    c = inputs.make_case(B, 1, seq, seed=seed + 1, kv_dtype=kv, device="cuda", extra_pages=3)
+    qn = (torch.randn(B, T, H, 512, generator=g) * q_scale).to(torch.bfloat16).cuda()
+    qr = (torch.randn(B, T, H, 64, generator=g) * q_scale).to(torch.bfloat16).cuda()
+    mask = np.zeros((B, T), dtype=np.uint64)
+    for b in range(B):
+        for i in range(T):
+            par = i - 1 if chain else int(torch.randint(-1, i, (1,), generator=g)) if i else -1
+            mask[b, i] = (mask[b, par] if par >= 0 else np.uint64(0)) | np.uint64(1) << np.uint64(i)
+    mask = torch.from_numpy(mask.view(np.int64)).cuda()
+    return dict(qn=qn, qr=qr, cache=c.cache, bt=c.block_table, seq=seq.cuda(), lens=lens.cuda(), mask=mask)
+
+
+def run(d, out_dtype=torch.float32, with_lse=True, kv=None, num_sms=0):
+    B, T, H, _ = d["qn"].shape
+    ws = ops.TreeWorkspace(B, T, H)
+    guard = Guarded(ws.nbytes)
+    guard.inner[:256].zero_()
+    ws.buf = guard.inner
+    ops.plan_tree(ws, d["seq"], d["lens"], kv_dtype="fp8" if d["cache"].dtype == torch.uint8 else "bf16", num_sms=num_sms)
+    go, gl = Guarded(B * T * H * 512 * (4 if out_dtype == torch.float32 else 2)), Guarded(B * T * H * 4)
+    out = go.inner.view(out_dtype).view(B, T, H, 512).fill_(7.0)
+    lse = gl.inner.view(torch.float32).view(B, T, H).fill_(7.0) if with_lse else None
+    ops.decode_tree(ws, d["qn"], d["qr"], d["cache"], d["bt"], d["seq"], d["lens"], d["mask"], tree_ref.SCALE, out=out,
+                    lse=lse, with_lse=with_lse)
+    st = ops.status(ws)
+    for x, n in ((guard, "workspace"), (go, "out"), (gl, "lse")):
+        x.check(n)
+    return out, lse, st, ws
+
+
+def both(d, out_dtype=torch.float32, what="", **kw):
+    out, lse, st, ws = run(d, out_dtype, **kw)
+    assert st == 0, what
+    tree_ref.check(out, lse, tree_ref.tree(d["qn"], d["qr"], d["cache"], d["bt"], d["seq"], d["lens"], d["mask"]), what)
+    return out, lse, ws
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 128), (2, 128), (3, 48), (5, 16), (8, 16), (64, 2), (13, 10)])
+def test_tree_shapes(T, H, kv):
+    both(make(3, T, H, [200, 0, 65], seed=T * 100 + H, kv=kv), torch.float32, f"T {T} H {H} {kv}")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_tree_ragged(kv, out_dtype):
+    # trees of different sizes, one empty request, one without drafted tokens, borders of pages and tiles
+    contexts = [0, 63, 64, 127, 128, 60, 1000, 0, 300, 1]
+    lens = [7, 1, 7, 2, 5, 7, 3, 0, 0, 6]
+    d = make(10, 7, 24, contexts, lens, kv, seed=5)
+    out, lse, _ = both(d, out_dtype, f"ragged {kv}")
+    assert bool((out[7:9] == 0).all()) and bool(torch.isneginf(lse[7:9]).all())
+    assert bool((out[1, 1:] == 0).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_tree_splits(kv):
+    # few requests with long contexts are cut into pieces over the units, and merged
+    d = make(2, 3, 128, [9000, 20000], kv=kv, seed=6)
+    _, _, ws = both(d, torch.bfloat16, f"split {kv}")
+    d = make(1, 4, 16, [30001], kv=kv, seed=7)
+    both(d, torch.float32, f"split {kv}, one tile")
+    both(make(2, 40, 16, [5000, 77], kv=kv, seed=8), torch.bfloat16, f"split {kv}, five tiles", with_lse=False)
+
+
+def test_peaked_scores():
+    both(make(2, 4, 32, [500, 1300], seed=9, q_scale=8.0), torch.float32, "peaked")
+
+
+def test_chain_of_one_equals_plain_decode():
+    # T = 1 attending itself is the single-token decode: the same kernels and items, the same bits
+    d = make(5, 1, 128, [100, 64, 4000, 0, 511], seed=10)
+    out, lse, st, _ = run(d)
+    ws = ops.Workspace(5, 128)
+    ops.plan(ws, d["seq"])
+    o, l = ops.decode(ws, d["qn"].view(5, 128, 512), d["qr"].view(5, 128, 64), d["cache"], d["bt"], d["seq"], tree_ref.SCALE)
+    assert torch.equal(out.view(5, 128, 512), o) and torch.equal(lse.view(5, 128), l)
+
+
+def test_chain_equals_decode_of_each_prefix():
+    d = make(2, 6, 16, [150, 58], seed=11, chain=True)
+    out, lse, _, _ = run(d)
+    for i in range(6):
+        seq = (d["seq"] - 5 + i).contiguous()
+        ws = ops.Workspace(2, 16)
+        ops.plan(ws, seq)
+        o, l = ops.decode(ws, d["qn"][:, i].contiguous(), d["qr"][:, i].contiguous(), d["cache"], d["bt"], seq, tree_ref.SCALE)
+        ref = tree_ref.tree(d["qn"], d["qr"], d["cache"], d["bt"], d["seq"], d["lens"], d["mask"])
+        assert bool(((out[:, i] - o).double().abs() <= 2 * ref[2][:, i]).all())
+        assert bool(((lse[:, i] - l).double().abs() <= 2 * ref[3][:, i]).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_masks_that_leave_a_row_empty(kv):
+    d = make(3, 5, 20, [0, 0, 70], kv=kv, seed=12)
+    d["mask"][0] = 0                     # no context and no ancestors: nothing is attended
+    d["mask"][1, 2] = 0
+    d["mask"][2, 3] = 0                  # only the context
+    d["mask"][1, 4] = -1                 # every bit set, those behind the tree too
+    out, lse, _ = both(d, torch.float32, "empty rows")
+    assert bool((out[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
+    assert bool((out[1, 2] == 0).all()) and bool(torch.isneginf(lse[1, 2]).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("context", [0, 61, 500, 12000])
+def test_bad_values_reach_only_the_rows_that_attend_them(kv, context):
+    d = make(1, 6, 40, [context], kv=kv, seed=13)
+    bits = np.array([1, 2, 4, 8 | 1, 16 | 2, 32 | 16 | 2], dtype=np.uint64)  # token 2 is attended by itself only
+    d["mask"][0] = torch.from_numpy(bits.view(np.int64)).cuda()
+    want = run(d, torch.bfloat16)
+    at = context + 2
+    page, row = int(d["bt"][0, at // 64]), at % 64
+    if kv == "bf16":
+        d["cache"][page, row, 3::7] = float("nan")
+        d["cache"][page, row, 100] = float("inf")
+    else:
+        d["cache"][page, row, 3:500:7] = 0x7F  # the NaN code
+    out, lse, st, _ = run(d, torch.bfloat16)
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(out[0, keep], want[0][0, keep]) and torch.equal(lse[0, keep], want[1][0, keep])
+    assert bool(torch.isnan(out[0, 2]).all()) and bool(torch.isnan(lse[0, 2]).all())
+
+
+def test_device_errors_are_reported():
+    d = make(2, 4, 16, [100, 200], seed=14)
+    d["lens"][0] = 9                     # above T: clamped
+    assert run(d)[2] == 5
+    d["lens"][0] = -1
+    out, _, st, _ = run(d)
+    assert st == 5 and bool((out[0] == 0).all())
+    d = make(2, 4, 16, [100, 200], seed=14)
+    d["seq"][0] = 2                      # fewer entries than drafted tokens
+    assert run(d)[2] == 5
+    d = make(2, 4, 16, [100, 200], seed=14)
+    d["bt"][1, 1] = 10 ** 6              # a page outside the pool
+    assert run(d)[2] == 5
+    # a plan of another shape, and no plan
+    d = make(2, 4, 16, [100, 200], seed=14)
+    ws = ops.TreeWorkspace(2, 4, 16)
+    args = (d["qn"], d["qr"], d["cache"], d["bt"], d["seq"], d["lens"], d["mask"], tree_ref.SCALE)
+    ops.decode_tree(ws, *args)
+    assert ops.status(ws) == 3
+    other = ops.TreeWorkspace(2, 2, 32)  # the same number of row tiles
+    ops.plan_tree(other, d["seq"], None)
+    ws.buf = other.buf
+    ops.decode_tree(ws, *args)
+    assert ops.status(ws) == 3
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_device_plan_equals_host_plan(kv):
+    for B, T, H, hi in ((3, 5, 16, 3000), (40, 16, 128, 3000), (1, 64, 128, 90000), (300, 2, 128, 400)):
+        g = torch.Generator().manual_seed(B)
+        lens = torch.randint(0, T + 1, (B,), generator=g, dtype=torch.int32)
+        seq = torch.randint(0, hi, (B,), generator=g, dtype=torch.int32) + lens
+        ws = ops.TreeWorkspace(B, T, H)
+        ops.plan_tree(ws, seq.cuda(), lens.cuda(), kv_dtype=kv)
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        host = ops.plan_tree_host(seq, lens, B, T, H, num_sms=sms, kv_dtype=kv)
+        entries = B * ((T * H + 127) // 128)
+        a, b = parse(ws.buf.cpu().numpy(), entries, 128), parse(host, entries, 128)
+        for k in ("unit_begin", "items", "num_splits", "split_base", "split_list", "n_partials", "per"):
+            assert np.array_equal(a[k], b[k]), k
+
+
+def test_stall_is_reported_and_the_workspace_stays_usable():
+    d = make(2, 3, 32, [700, 90], seed=15)
+    want = run(d)
+    ops.set_wait_limit(2_000_000)
+    ops.inject_stall(True)
+    try:
+        assert run(d)[2] == 6  # MLA_ERR_TIMEOUT
+    finally:
+        ops.inject_stall(False)
+        ops.set_wait_limit(0)
+    got = run(d)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
