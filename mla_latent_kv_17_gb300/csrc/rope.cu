@@ -1,12 +1,13 @@
 // Rotary positions of part of every head.  The definition is in include/mla_decode.h
 // (mla_rope).
 //
-// Every value is read and written once, so memory bounds it.  A CTA takes a few tokens (or
-// part of one token's heads) and first computes those tokens' cosines and sines once, into
-// shared memory; then thread (u, y) owns unit u of a row - a vector of the passing part, or
-// two vectors a, b whose values are the pairs of kVec (half layout) or 2 kVec values in a row
-// (interleaved) - and walks the rows y, y + blockDim.y, ..., so that its cosines and sines
-// stay in registers while it goes through a token's heads and no index is divided.
+// Every value is read and written once, so memory bounds it.  A CTA takes kRopeRows rows per
+// thread row: part of a token's heads, or several tokens of few heads.  Thread (u, y) owns unit
+// u of a row - two vectors of the passing part, or the two vectors whose values are the pairs -
+// and rows y, y + blockDim.y, ...; it issues the loads of all its rows first, then the CTA
+// computes its tokens' cosines and sines once into shared memory while they are in flight.
+// (Angles first, then rows in turn, ran at 36 % of the memory's rate: the short CTAs waited for
+// their angles with nothing in flight.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -19,6 +20,8 @@ namespace mla {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 4;                // rows per thread, in flight together
+constexpr int kRopeCtas = 3;                // CTAs per SM (registers)
 constexpr int kRopeTableBytes = 16 * 1024;  // shared memory for the CTA's (cos, sin) pairs, at most
 
 struct RopeArgs {
@@ -68,7 +71,7 @@ struct Vec<1> {
 
 // Rotates the kVec pairs of two vectors: pairs (a_i, b_i), or neighbours when interleaved.
 template <int kVec>
-__device__ __forceinline__ void rotate(Vec<kVec> &va, Vec<kVec> &vb, const float2 (&cs)[kVec], bool interleaved) {
+__device__ __forceinline__ void rotate(Vec<kVec> &va, Vec<kVec> &vb, const float2 *cs, bool interleaved) {
     float a[kVec], b[kVec];
     va.get(a);
     vb.get(b);
@@ -95,95 +98,63 @@ __device__ __forceinline__ void rotate(Vec<kVec> &va, Vec<kVec> &vb, const float
     vb.set(b);
 }
 
-template <int kVec>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
+// kOne: the CTA's rows are heads of one token (rows at a fixed distance, no division).
+template <int kVec, bool kOne>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeArgs a) {
     extern __shared__ float2 s_cs[];  // [tokens][d_rot / 2]
     grid_dep_wait();
     grid_dep_launch();
     const int64_t n0 = (int64_t)blockIdx.x * a.tokens;
-    const int nt = (int)min((int64_t)a.tokens, a.N - n0);
+    const int nt = kOne ? 1 : (int)min((int64_t)a.tokens, a.N - n0);
     const int h0 = (int)blockIdx.y * a.heads, nh = min(a.heads, a.H - h0);
     const int half = a.d_rot / 2;
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthreads = blockDim.x * blockDim.y;
-    for (int i = tid; i < nt * half; i += nthreads) {
-        const int t = i / half;
-        s_cs[i] = turn(a.positions[n0 + t], turns_fixed(a.freqs[i - t * half]), a.mscale);
-    }
-    __syncthreads();
-    const int np = a.out_pass ? a.d_pass / kVec : 0;  // units that only pass
-    const int units = np + half / kVec;
-    for (int u = threadIdx.x; u < units; u += blockDim.x) {
-        if (u < np) {
-            int t = 0, h = threadIdx.y;
-            while (h >= nh) {
-                h -= nh;
-                ++t;
+    const int pvec = a.out_pass ? a.d_pass / kVec : 0;  // vectors that only pass, two to a unit
+    const int np = (pvec + 1) / 2, units = np + half / kVec;
+    const int rows = nt * nh;
+    const uint16_t *src0 = a.x + n0 * a.x_ts + (int64_t)h0 * a.x_hs;
+    bool first = true;
+    for (int u = threadIdx.x; u < units || first; u += blockDim.x) {
+        const bool pass = u < np;
+        const int j = (u - np) * kVec;  // a rotated unit's first pair
+        const int offa = pass ? 2 * u * kVec : a.d_pass + (a.interleaved ? 2 * j : j);
+        const int offb = pass ? offa + kVec : a.d_pass + (a.interleaved ? 2 * j + kVec : j + half);
+        const bool has_b = !pass || 2 * u + 1 < pvec;
+        for (int r0 = threadIdx.y; r0 < rows || first; r0 += kRopeRows * blockDim.y) {
+            // this thread's rows of the unit, all loads in flight; the first ones before the
+            // angles are computed
+            Vec<kVec> va[kRopeRows], vb[kRopeRows];
+#pragma unroll
+            for (int k = 0; k < kRopeRows; ++k) {
+                const int r = r0 + k * blockDim.y;
+                if (u < units && r < rows) {
+                    const int t = kOne ? 0 : r / nh, h = kOne ? r : r - t * nh;
+                    const uint16_t *src = src0 + t * a.x_ts + h * a.x_hs;
+                    va[k].load(src + offa);
+                    if (has_b) vb[k].load(src + offb);
+                }
             }
-            while (t < nt) {
-                // four rows in flight
-                Vec<kVec> v[4];
-                uint16_t *dst[4];
-                int m = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (t < nt) {
-                        v[k].load(a.x + (n0 + t) * a.x_ts + (int64_t)(h0 + h) * a.x_hs + u * kVec);
-                        dst[k] = a.out_pass + (n0 + t) * a.p_ts + (int64_t)(h0 + h) * a.p_hs + u * kVec;
-                        m = k + 1;
-                        h += blockDim.y;
-                        while (h >= nh) {
-                            h -= nh;
-                            ++t;
-                        }
-                    }
+            if (first) {
+                for (int i = tid; i < nt * half; i += nthreads) {
+                    const int t = kOne ? 0 : i / half;
+                    s_cs[i] = turn(a.positions[n0 + t], turns_fixed(a.freqs[i - t * half]), a.mscale);
                 }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < m) v[k].store(dst[k]);
+                __syncthreads();
+                first = false;
             }
-        } else {
-            const int j = (u - np) * kVec;  // the unit's first pair
-            const int offa = a.interleaved ? 2 * j : j, offb = a.interleaved ? 2 * j + kVec : j + half;
-            int t = 0, h = threadIdx.y;
-            while (h >= nh) {
-                h -= nh;
-                ++t;
-            }
-            int tcs = -1;
-            float2 cs[kVec];
-            while (t < nt) {
-                if (t != tcs) {
+            if (u >= units) break;
+            uint16_t *dst0 = pass ? a.out_pass + n0 * a.p_ts + (int64_t)h0 * a.p_hs + offa
+                                  : a.out_rot + n0 * a.r_ts + (int64_t)h0 * a.r_hs + (offa - a.d_pass);
+            const int64_t dts = pass ? a.p_ts : a.r_ts, dhs = pass ? a.p_hs : a.r_hs;
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) cs[i] = s_cs[t * half + j + i];
-                    tcs = t;
-                }
-                Vec<kVec> va[2], vb[2];
-                uint16_t *dst[2];
-                int m = 0;
-                // two rows of the same token in flight
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (t == tcs && t < nt) {
-                        const uint16_t *src = a.x + (n0 + t) * a.x_ts + (int64_t)(h0 + h) * a.x_hs + a.d_pass;
-                        va[k].load(src + offa);
-                        vb[k].load(src + offb);
-                        dst[k] = a.out_rot + (n0 + t) * a.r_ts + (int64_t)(h0 + h) * a.r_hs;
-                        m = k + 1;
-                        h += blockDim.y;
-                        while (h >= nh) {
-                            h -= nh;
-                            ++t;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (k < m) {
-                        rotate<kVec>(va[k], vb[k], cs, a.interleaved != 0);
-                        va[k].store(dst[k] + offa);
-                        vb[k].store(dst[k] + offb);
-                    }
-                }
+            for (int k = 0; k < kRopeRows; ++k) {
+                const int r = r0 + k * (int)blockDim.y;
+                if (r >= rows) break;
+                const int t = kOne ? 0 : r / nh, h = kOne ? r : r - t * nh;
+                if (!pass) rotate<kVec>(va[k], vb[k], s_cs + t * half + j, a.interleaved != 0);
+                uint16_t *dst = dst0 + t * dts + h * dhs;
+                va[k].store(dst);
+                if (has_b) vb[k].store(dst + (offb - offa));
             }
         }
     }
@@ -191,24 +162,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
 
 template <int kVec>
 mla_status launch_rope(RopeArgs a, cudaStream_t stream) {
-    const int units = (a.out_pass ? a.d_pass / kVec : 0) + a.d_rot / 2 / kVec;
+    const int units = (a.out_pass ? (a.d_pass / kVec + 1) / 2 : 0) + a.d_rot / 2 / kVec;
     const int bx = units < kRopeThreads ? units : kRopeThreads;
-    const int by = kRopeThreads / bx < 1 ? 1 : kRopeThreads / bx;
-    // Rows per CTA: enough CTAs to fill the GPU several times over, and at most eight rows
-    // per thread row; with many heads part of a token, with few several tokens.
-    const int64_t rows = a.N * a.H;
-    int64_t per = rows / (152 * 8);
-    if (per < by) per = by;
-    if (per > 8 * by) per = 8 * by;
+    int by = 1;  // a power of two, like most head counts
+    while (2 * by * bx <= kRopeThreads) by *= 2;
+    // by * kRopeRows rows per CTA: part of a token's heads, or several tokens of few heads
+    const int per = by * kRopeRows;
     if (per >= a.H) {
         a.heads = a.H;
-        a.tokens = (int)(per / a.H);
+        a.tokens = per / a.H;
         const int most = kRopeTableBytes / ((a.d_rot / 2) * (int)sizeof(float2));
         if (a.tokens > most) a.tokens = most;
-        if (a.tokens < 1) a.tokens = 1;
     } else {
         a.tokens = 1;
-        const int groups = (int)((a.H + per - 1) / per);
+        const int groups = (a.H + per - 1) / per;
         a.heads = (a.H + groups - 1) / groups;
     }
     const int64_t gx = (a.N + a.tokens - 1) / a.tokens;
@@ -224,7 +191,9 @@ mla_status launch_rope(RopeArgs a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_kernel<kVec>, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, a.tokens == 1 ? rope_kernel<kVec, true> : rope_kernel<kVec, false>, a) == cudaSuccess
+               ? MLA_OK
+               : MLA_ERR_CUDA;
 }
 
 }  // namespace

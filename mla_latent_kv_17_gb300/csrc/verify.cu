@@ -14,8 +14,8 @@
 // per cycle and SM here.)
 //
 // Per stop the sum pass leaves a partial sum per warp (a contiguous chunk) and per CTA (a
-// contiguous slice); the draw then finds its slice and chunk from those sums, and one warp
-// searches its chunk again, from L2.
+// contiguous slice); the draw then finds its slice and chunk from those sums, and the CTA that
+// owns them searches the chunk again, from L2.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -27,10 +27,9 @@ namespace mla {
 namespace {
 
 constexpr int kVfCluster = 8;
-constexpr int kVfThreads = 512;
+constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxT = 64;
-constexpr float kVfOne = 288230376151711744.f;  // 2^58
 
 struct VerifyArgs {
     const float *target, *draft;
@@ -41,10 +40,16 @@ struct VerifyArgs {
     int *status;
 };
 
-// A probability as a multiple of 2^-58 (NaN and negative values: 0, above 1: 1).
+// A probability as a multiple of 2^-58 (NaN and negative values: 0, above 1: 1): the significand
+// at the top of a 64-bit word, shifted down by what the exponent lacks (shifts of 64 and more
+// give 0).  The conversion instruction to 64-bit integers runs on the fp64 pipe, which it kept
+// 75 % busy: 53 us for 64 x 131,072 against 22 us.
 __device__ __forceinline__ uint64_t fixed58(float p) {
-    p = p > 0.f ? fminf(p, 1.f) : 0.f;
-    return __float2ull_rz(p * kVfOne);
+    const uint32_t b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
+    const uint64_t m = (uint64_t)((b << 8) | 0x80000000u) << 32;  // 2^63 x 1.fraction
+    uint64_t r;
+    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(132u - (b >> 23)));
+    return r;
 }
 
 // What is left of the target's row after the rejected drafts rej[0 .. n): their masses are the
@@ -74,15 +79,59 @@ struct Residual {
     }
 };
 
+__device__ __forceinline__ uint64_t left_of(float p, float q) {
+    const uint64_t x = fixed58(p), y = fixed58(q);
+    return x > y ? x - y : 0;
+}
+
+// A lane's part of the sum of max(p - q, 0) (or of p) over [c0, c1).  16-byte loads where both
+// rows allow them (c0 is a multiple of 32), single values otherwise.
+template <bool kQ>
+__device__ __forceinline__ uint64_t sum_rows(const float *p, const float *q, int c0, int c1, int lane) {
+    uint64_t sum = 0;
+    int v = c0;
+    if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0) {
+        for (; v + 512 <= c1; v += 512) {
+            float4 pv[4], qv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pv[i] = *reinterpret_cast<const float4 *>(p + v + 128 * i + 4 * lane);
+                if constexpr (kQ) qv[i] = *reinterpret_cast<const float4 *>(q + v + 128 * i + 4 * lane);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kQ)
+                    sum += left_of(pv[i].x, qv[i].x) + left_of(pv[i].y, qv[i].y) + left_of(pv[i].z, qv[i].z) +
+                           left_of(pv[i].w, qv[i].w);
+                else
+                    sum += fixed58(pv[i].x) + fixed58(pv[i].y) + fixed58(pv[i].z) + fixed58(pv[i].w);
+            }
+        }
+    }
+    for (; v < c1; v += 256) {
+        float pv[8], qv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int w = v + 32 * i + lane;
+            pv[i] = w < c1 ? p[w] : 0.f;
+            if constexpr (kQ) qv[i] = w < c1 ? q[w] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += kQ ? left_of(pv[i], qv[i]) : fixed58(pv[i]);
+    }
+    return sum;
+}
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-__global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads) verify_kernel(VerifyArgs a) {
+__global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads, 4) verify_kernel(VerifyArgs a) {
     __shared__ int32_t s_tok[kVfMaxT], s_par[kVfMaxT], s_depth[kVfMaxT];
-    __shared__ float s_u[kVfMaxT + 1], s_p[kVfMaxT], s_q[kVfMaxT];
+    __shared__ bool s_stands[kVfMaxT];            // would token i stand as the first one tried at its place?
+    __shared__ bool s_answer;
     __shared__ int s_rej[kVfMaxT];
     __shared__ double s_mass[kVfMaxT];
     __shared__ uint64_t s_warp[kVfWarps];         // sums of this CTA's chunks
@@ -95,27 +144,34 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads)
     grid_dep_launch();
     const float *target = a.target + (int64_t)b * (T + 1) * V;
     const float *draft = a.draft ? a.draft + (int64_t)b * T * V : nullptr;
-    int len = a.tree_lens ? a.tree_lens[b] : T;
-    if (len < 0 || len > T) {
-        if (tid == 0 && rank == 0 && a.status) record_error(a.status, MLA_ERR_INDEX);
-        len = min(max(len, 0), T);
-    }
-    // the tokens and the probabilities their first test needs, all at once
+    // every small load at once, then the probabilities the tokens' first tests need
+    int32_t len = a.tree_lens ? a.tree_lens[b] : T;
+    const float u_draw = a.uniforms[(int64_t)b * (T + 1) + T];
+    int32_t x = -1, par = tid - 1;
+    float u = 0.f;
     if (tid < T) {
-        const int32_t x = a.tokens[(int64_t)b * T + tid];
-        const int32_t par = a.parents ? a.parents[(int64_t)b * T + tid] : tid - 1;
+        x = a.tokens[(int64_t)b * T + tid];
+        if (a.parents) par = a.parents[(int64_t)b * T + tid];
+        u = a.uniforms[(int64_t)b * (T + 1) + tid];
+    }
+    // (the cluster's CTAs all run before one writes into another's s_slice: waited for there)
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    bool wrong = len < 0 || len > T;
+    len = min(max(len, 0), T);
+    if (tid < T) {
         const bool fine = x >= 0 && x < V && par >= -1 && par < tid;
-        if (!fine && tid < len && rank == 0 && a.status) record_error(a.status, MLA_ERR_INDEX);
+        wrong = wrong || (!fine && tid < len);
         s_tok[tid] = x >= 0 && x < V ? x : -1;
         s_par[tid] = par >= -1 && par < tid ? par : -2;  // -2: a parent that is never reached
         s_depth[tid] = -1;
-        s_u[tid] = a.uniforms[(int64_t)b * (T + 1) + tid];
-        s_p[tid] = fine ? target[(int64_t)(par + 1) * V + x] : 0.f;
-        s_q[tid] = fine && draft ? draft[(int64_t)tid * V + x] : 1.f;
+        // (fp64: 48-bit products, exact; by the token's own thread only, since the units are few)
+        const float p = fine ? target[(int64_t)(par + 1) * V + x] : 0.f;
+        const float q = fine && draft ? draft[(int64_t)tid * V + x] : 1.f;
+        s_stands[tid] = (double)u * (double)q < (double)p;
+        if (wrong && rank == 0 && a.status) record_error(a.status, MLA_ERR_INDEX);
     }
-    if (tid == 0) s_u[T] = a.uniforms[(int64_t)b * (T + 1) + T];
-    __syncwarp();
-    ptx::cluster_sync();  // and every CTA runs before another one writes into its s_slice
+    __syncthreads();
 
     // contiguous slices of whole 128-element groups, one per CTA, and chunks, one per warp
     const int slice = ((V + kVfCluster - 1) / kVfCluster + 127) & ~127;
@@ -128,22 +184,9 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads)
     auto total_left = [&](const Residual &r) -> uint64_t {
         uint64_t sum = 0;
         if (r.n == 0 || (r.n == 1 && r.q)) {
-            // the usual case: one or two rows, eight loads of each in flight
+            // the usual case: one or two rows, sixteen values of each in flight per lane
             const float *p = r.p, *q = r.n == 1 ? r.q + (int64_t)r.rej[0] * V : nullptr;
-            for (int v = c0 + lane; v < c1; v += 32 * 8) {
-                float pv[8], qv[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int w = v + 32 * i;
-                    pv[i] = w < c1 ? p[w] : 0.f;
-                    qv[i] = q && w < c1 ? q[w] : 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint64_t x = fixed58(pv[i]), y = fixed58(qv[i]);
-                    sum += x > y ? x - y : 0;
-                }
-            }
+            sum = q ? sum_rows<true>(p, q, c0, c1, lane) : sum_rows<false>(p, p, c0, c1, lane);
         } else {
             for (int v = c0 + lane; v < c1; v += 32) sum += r.at(v);
         }
@@ -151,6 +194,7 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads)
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
         const int turn = turns & 1;
+        if (turns == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (warp == 0) {
             uint64_t t = lane < kVfWarps ? s_warp[lane] : 0;
             t = warp_sum(t);
@@ -175,11 +219,14 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads)
     for (int i = 0; i < len; ++i) {
         const int x = s_tok[i];
         if (s_par[i] != at || x < 0) continue;
-        bool stands;
-        if (nrej == 0) {
-            stands = (double)s_u[i] * (double)s_q[i] < (double)s_p[i];  // 48-bit products: exact
-        } else {
-            stands = (double)s_u[i] * (double)s_q[i] * mass < (double)r.at(x);
+        bool stands = s_stands[i];
+        if (nrej > 0) {
+            if (tid == 0) {
+                const double u = a.uniforms[(int64_t)b * (T + 1) + i];
+                s_answer = u * (double)(draft ? draft[(int64_t)i * V + x] : 1.f) * mass < (double)r.at(x);
+            }
+            __syncthreads();
+            stands = s_answer;
         }
         if (stands) {
             if (tid == 0) s_depth[i] = depth;
@@ -201,7 +248,16 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads)
         // the mass left is needed by a sibling's test (the draw sums again only if none came)
         bool sibling = false;
         for (int k = i + 1; k < len; ++k) sibling = sibling || (s_par[k] == at && s_tok[k] >= 0);
-        if (sibling) mass = (double)total_left(r);
+        if (!sibling) continue;
+        if (!draft && nrej > 1) {
+            // certain drafts: only the token itself is lost (nothing, where it was lost before);
+            // the first rejection's sum is the only pass a place needs
+            r.n = nrej - 1;
+            mass -= (double)r.at(x);
+            r.n = nrej;
+        } else {
+            mass = (double)total_left(r);
+        }
     }
     uint64_t all = total_left(r);
     if (all == 0 && nrej > 0) {  // nothing is left: the target's own row
@@ -212,41 +268,42 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads)
     if (all == 0) {
         if (rank == 0 && tid == 0) a.next_token[b] = -1;
     } else {
-        const float u = s_u[T];
-        uint64_t want = u > 0.f ? __double2ull_rz((double)u * (double)all) : 0;
-        if (want >= all) want = all - 1;
+        // floor(u total), exact: u as a 64-bit fraction
+        uint64_t want = u_draw < 1.f ? __umul64hi(fixed58(u_draw) << 6, all) : all - 1;
         const int turn = (turns - 1) & 1;
         int owner = 0;
         while (owner < kVfCluster - 1 && want >= s_slice[turn][owner]) want -= s_slice[turn][owner++];
         if ((int)rank == owner) {
             int w = 0;
             while (w < kVfWarps - 1 && want >= s_warp[w]) want -= s_warp[w++];
-            if (warp == w) {
-                // each lane a contiguous run of the chunk; the lane whose run holds the place
-                // searches it
-                const int per = (c1 - c0 + 31) / 32;
-                const int l0 = min(c1, c0 + lane * per), l1 = min(c1, l0 + per);
-                uint64_t mine = 0;
-#pragma unroll 4
-                for (int v = l0; v < l1; ++v) mine += r.at(v);
-                uint64_t upto = mine;
+            // chunk w again, by the whole CTA: each thread a run of it; the thread whose run
+            // holds the place searches the run
+            const int k0 = min(v1, v0 + w * chunk), k1 = min(v1, k0 + chunk);
+            const int per = (k1 - k0 + kVfThreads - 1) / kVfThreads;
+            const int l0 = min(k1, k0 + tid * per), l1 = min(k1, l0 + per);
+            uint64_t mine = 0;
+#pragma unroll 8
+            for (int v = l0; v < l1; ++v) mine += r.at(v);
+            uint64_t upto = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            __syncthreads();  // s_warp has been read
+            if (lane == 31) s_warp[warp] = upto;
+            __syncthreads();
+            for (int k = 0; k < warp; ++k) upto += s_warp[k];
+            if (upto > want && upto - mine <= want) {  // one thread
+                uint64_t run = upto - mine;
+                int v = l0;
+                for (; v < l1 - 1; ++v) {
+                    run += r.at(v);
+                    if (run > want) break;
                 }
-                const unsigned past = __ballot_sync(0xffffffffu, upto > want);
-                if (past && lane == __ffs(past) - 1) {
-                    uint64_t run = upto - mine;
-                    int v = l0;
-                    for (; v < l1 - 1; ++v) {
-                        run += r.at(v);
-                        if (run > want) break;
-                    }
-                    a.next_token[b] = v;
-                } else if (!past && lane == 0) {
-                    a.next_token[b] = min(c0, V - 1);  // sums that overflowed: rows far from adding up to 1
-                }
+                a.next_token[b] = v;
+            } else if (tid == kVfThreads - 1 && upto <= want) {
+                a.next_token[b] = max(k1 - 1, 0);  // sums that overflowed: rows far from adding up to 1
             }
         }
     }

@@ -411,18 +411,21 @@ def status(ws: Workspace, stream=None) -> int:
 # These take tensors of any one CUDA device (the launch goes to that device's current stream,
 # or to `stream`) and allocate the outputs they are not given.
 
-def _device_of(*named):
-    """The CUDA device that all given tensors (name, tensor or None) live on."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+# (A small call is bound by this file: tensors are checked by their device's number, pointers
+# and the stream pass as plain integers.)
+
+def _device_of(first, **others):
+    """The number of the CUDA device that all given tensors (or None) live on; `first` decides."""
+    dev = first.get_device()
+    for name, t in others.items():
+        if t is not None and t.get_device() != dev:
+            dev = -1
+            break
+    if dev < 0:
+        for name, t in others.items():
+            if t is not None and not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError("arguments are on different devices")
     return dev
 
 
@@ -439,20 +442,30 @@ class _Same:
 _SAME = _Same()
 
 
-def _on(dev):
-    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _on(dev: int):
+    return _SAME if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _new(shape, dtype, dev, stream):
-    """An output tensor; memory that a stream other than the current one writes is recorded on it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+def _raw(stream, dev: int) -> int:
+    """The handle of `stream`, or of the device's current stream."""
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _new(like, shape, dtype, stream):
+    """An output on `like`'s device; memory that a stream other than the current one writes is
+    recorded on it."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
 def _ints(t, shape, name):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
 
 
@@ -524,35 +537,39 @@ def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pas
     d_pass = D - d_rot
     if d_rot < 2 or d_pass < 0:
         raise ValueError(f"x has {D} values per head, freqs turns {d_rot}")
-    dev = _device_of(("x", x), ("positions", positions), ("freqs", freqs), ("out_pass", out_pass), ("out_rot", out_rot))
+    dev = _device_of(x, x=x, positions=positions, freqs=freqs, out_pass=out_pass, out_rot=out_rot)
     _ints(positions, (N,), "positions")
     _freqs(freqs, d_rot)
+    code = _layout(layout)
     with _on(dev):
-        if out_pass is None and copy_pass and d_pass > 0:
-            out_pass = _new((N, H, d_pass), torch.bfloat16, dev, stream)
-        elif not copy_pass:
+        if not copy_pass or d_pass == 0:
             out_pass = None
+        elif out_pass is None:
+            out_pass = _new(x, (N, H, d_pass), torch.bfloat16, stream)
+        elif out_pass.dtype != torch.bfloat16 or out_pass.shape != (N, H, d_pass):
+            raise ValueError(f"out_pass must be bf16 [{N},{H},{d_pass}]")
         if out_rot is None:
-            out_rot = _new((N, H, d_rot), torch.bfloat16, dev, stream)
-        for t, n, d in ((out_pass, "out_pass", d_pass), (out_rot, "out_rot", d_rot)):
-            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (N, H, d)):
-                raise ValueError(f"{n} must be bf16 [{N},{H},{d}]")
-        for t, n in ((x, "x"), (out_pass, "out_pass"), (out_rot, "out_rot")):
-            if t is not None and t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
-                raise ValueError(f"{n} must have unit stride within a row")
-        ps = out_pass.stride() if out_pass is not None else (0, 0)
-        rs, xs = out_rot.stride(), x.stride()
-        if N and H:
-            _check("mla_rope", lib().mla_rope(
-                _ptr(x), xs[0], xs[1], N, H, d_pass, d_rot, _layout(layout), _ptr(positions), _ptr(freqs),
-                float(mscale), _ptr(out_pass), ps[0], ps[1], _ptr(out_rot), rs[0], rs[1], _stream(stream)))
+            out_rot = _new(x, (N, H, d_rot), torch.bfloat16, stream)
+        elif out_rot.dtype != torch.bfloat16 or out_rot.shape != (N, H, d_rot):
+            raise ValueError(f"out_rot must be bf16 [{N},{H},{d_rot}]")
+        xs, rs = x.stride(), out_rot.stride()
+        ps = rs if out_pass is None else out_pass.stride()
+        if N == 0 or H == 0:
+            return out_pass, out_rot
+        if (xs[2] != 1 and D > 1) or rs[2] != 1 or (ps[2] != 1 and d_pass > 1):
+            raise ValueError("x, out_pass and out_rot must have unit stride within a row")
+        st = lib().mla_rope(x.data_ptr(), xs[0], xs[1], N, H, d_pass, d_rot, code, positions.data_ptr(),
+                            freqs.data_ptr(), mscale, _at(out_pass), ps[0], ps[1], out_rot.data_ptr(), rs[0], rs[1],
+                            _raw(stream, dev))
+    if st:
+        _check("mla_rope", st)
     return out_pass, out_rot
 
 
 def _cache_kind(cache) -> int:
-    if cache.dtype == torch.bfloat16 and tuple(cache.shape[1:]) == (64, 576):
+    if cache.dtype == torch.bfloat16 and cache.shape[1:] == (64, 576):
         kv = KV_BF16
-    elif cache.dtype == torch.uint8 and tuple(cache.shape[1:]) == (64, 656):
+    elif cache.dtype == torch.uint8 and cache.shape[1:] == (64, 656):
         kv = KV_FP8
     else:
         raise ValueError("cache must be bf16 [P,64,576] or uint8 [P,64,656]")
@@ -575,7 +592,7 @@ def _tokens(block_table, requests, positions):
 
 
 def _entry_rows(t, N, name):
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (N, 576) or (N and t.stride(1) != 1):
+    if t.dtype != torch.bfloat16 or t.shape != (N, 576) or (N and t.stride(1) != 1):
         raise ValueError(f"{name} must be bf16 [{N},576] with unit stride within a row")
     return t.stride(0) if N > 1 else 576
 
@@ -588,9 +605,8 @@ def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_po
     [P,64,576] or uint8 FP8 records [P,64,656] (quantised on the way in).  With norm_weight
     (bf16 [512]) the latent is RMS-normalised first; with freqs (float64 [32]) the key is rotated
     at rope_positions (None: positions).  device_status: optional int32 [1] for MLA_ERR_INDEX."""
-    dev = _device_of(("cache", cache), ("block_table", block_table), ("requests", requests),
-                     ("positions", positions), ("kv", kv), ("freqs", freqs), ("rope_positions", rope_positions),
-                     ("norm_weight", norm_weight), ("device_status", device_status))
+    dev = _device_of(cache, cache=cache, block_table=block_table, requests=requests, positions=positions, kv=kv,
+                     freqs=freqs, rope_positions=rope_positions, norm_weight=norm_weight, device_status=device_status)
     kind = _cache_kind(cache)
     N = _tokens(block_table, requests, positions)
     stride = _entry_rows(kv, N, "kv")
@@ -600,15 +616,18 @@ def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_po
         if freqs is None:
             raise ValueError("rope_positions without freqs")
         _ints(rope_positions, (N,), "rope_positions")
-    if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or tuple(norm_weight.shape) != (512,)
+    if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or norm_weight.shape != (512,)
                                     or not norm_weight.is_contiguous()):
         raise ValueError("norm_weight must be contiguous bf16 [512]")
     _status_word(device_status)
+    code = _layout(layout)
     with _on(dev):
-        _check("mla_cache_write", lib().mla_cache_write(
-            _ptr(cache), kind, cache.shape[0], _ptr(block_table), block_table.shape[0], block_table.shape[1],
-            _ptr(requests), _ptr(positions), _ptr(kv), stride, N, _ptr(norm_weight), float(norm_eps), _ptr(freqs),
-            _ptr(rope_positions), _layout(layout), float(mscale), _ptr(device_status), _stream(stream)))
+        st = lib().mla_cache_write(
+            cache.data_ptr(), kind, cache.shape[0], block_table.data_ptr(), block_table.shape[0],
+            block_table.shape[1], _at(requests), positions.data_ptr(), kv.data_ptr(), stride, N, _at(norm_weight),
+            norm_eps, _at(freqs), _at(rope_positions), code, mscale, _at(device_status), _raw(stream, dev))
+    if st:
+        _check("mla_cache_write", st)
     return cache
 
 
@@ -616,18 +635,21 @@ def cache_read(cache, block_table, requests, positions, entries=None, device_sta
     """Reads many tokens' entries back: bf16 [N,576], row n = position positions[n] of request
     requests[n] (None: request n); FP8 records are dequantised.  Rows of skipped tokens (negative
     or unmapped positions) stay as they were in `entries` (undefined where it is allocated here)."""
-    dev = _device_of(("cache", cache), ("block_table", block_table), ("requests", requests),
-                     ("positions", positions), ("entries", entries), ("device_status", device_status))
+    dev = _device_of(cache, cache=cache, block_table=block_table, requests=requests, positions=positions,
+                     entries=entries, device_status=device_status)
     kind = _cache_kind(cache)
     N = _tokens(block_table, requests, positions)
     _status_word(device_status)
     with _on(dev):
         if entries is None:
-            entries = _new((N, 576), torch.bfloat16, dev, stream)
+            entries = _new(cache, (N, 576), torch.bfloat16, stream)
         stride = _entry_rows(entries, N, "entries")
-        _check("mla_cache_read", lib().mla_cache_read(
-            _ptr(cache), kind, cache.shape[0], _ptr(block_table), block_table.shape[0], block_table.shape[1],
-            _ptr(requests), _ptr(positions), N, _ptr(entries), stride, _ptr(device_status), _stream(stream)))
+        st = lib().mla_cache_read(
+            cache.data_ptr(), kind, cache.shape[0], block_table.data_ptr(), block_table.shape[0],
+            block_table.shape[1], _at(requests), positions.data_ptr(), N, entries.data_ptr(), stride,
+            _at(device_status), _raw(stream, dev))
+    if st:
+        _check("mla_cache_read", st)
     return entries
 
 
@@ -637,10 +659,10 @@ class TreeWorkspace:
 
     def __init__(self, B: int, T: int, H: int, num_sms: int = 0, device=None):
         self.B, self.T, self.H = int(B), int(T), int(H)
-        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        dev = torch.device(device if device is not None else "cuda")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        with _on(dev):
+        with _on(dev.index):
             self.nbytes = int(lib().mla_decode_tree_workspace_size(self.B, self.T, self.H, int(num_sms)))
             if self.nbytes == 0:
                 raise MlaError("mla_decode_tree_workspace_size", 1, "invalid arguments")
@@ -654,14 +676,15 @@ class TreeWorkspace:
 def plan_tree(ws: TreeWorkspace, seq_lens, tree_lens=None, num_sms: int = 0, stream=None, kv_dtype="bf16"):
     """Builds the plan of decode_tree for seq_lens and tree_lens (device int32 [B]; tree_lens
     None: T); kv_dtype ('bf16' or 'fp8') is the cache layout the attention will read."""
-    dev = _device_of(("seq_lens", seq_lens), ("tree_lens", tree_lens), ("workspace", ws.buf))
+    dev = _device_of(seq_lens, seq_lens=seq_lens, tree_lens=tree_lens, workspace=ws.buf)
     _ints(seq_lens, (ws.B,), "seq_lens")
     if tree_lens is not None:
         _ints(tree_lens, (ws.B,), "tree_lens")
     with _on(dev):
-        _check("mla_decode_tree_plan", lib().mla_decode_tree_plan(
-            _ptr(seq_lens), _ptr(tree_lens), ws.B, ws.T, ws.H, _kv_code(kv_dtype), int(num_sms), ws.ptr(), ws.nbytes,
-            _stream(stream)))
+        st = lib().mla_decode_tree_plan(seq_lens.data_ptr(), _at(tree_lens), ws.B, ws.T, ws.H, _kv_code(kv_dtype),
+                                        num_sms, ws.buf.data_ptr(), ws.nbytes, _raw(stream, dev))
+    if st:
+        _check("mla_decode_tree_plan", st)
     return ws
 
 
@@ -673,11 +696,10 @@ def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens,
     tree_lens[b] (None: T) of them its drafted tokens'; tree_mask int64 [B,T]: bit j of [b,i] set:
     token i attends drafted token j.  -> (out fp32 or bf16 [B,T,H,512], lse fp32 [B,T,H] or None)."""
     B, T, H = ws.B, ws.T, ws.H
-    dev = _device_of(("q_nope", q_nope), ("q_rope", q_rope), ("cache", cache), ("block_table", block_table),
-                     ("seq_lens", seq_lens), ("tree_lens", tree_lens), ("tree_mask", tree_mask), ("out", out),
-                     ("lse", lse), ("workspace", ws.buf))
+    dev = _device_of(q_nope, q_nope=q_nope, q_rope=q_rope, cache=cache, block_table=block_table, seq_lens=seq_lens,
+                     tree_lens=tree_lens, tree_mask=tree_mask, out=out, lse=lse, workspace=ws.buf)
     for t, d, name in ((q_nope, 512, "q_nope"), (q_rope, 64, "q_rope")):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (B, T, H, d) or not t.is_contiguous():
+        if t.dtype != torch.bfloat16 or t.shape != (B, T, H, d) or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous bf16 [{B},{T},{H},{d}]")
     kind = _cache_kind(cache)
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
@@ -686,22 +708,25 @@ def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens,
     _ints(seq_lens, (B,), "seq_lens")
     if tree_lens is not None:
         _ints(tree_lens, (B,), "tree_lens")
-    if tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (B, T) or not tree_mask.is_contiguous():
+    if tree_mask.dtype != torch.int64 or tree_mask.shape != (B, T) or not tree_mask.is_contiguous():
         raise ValueError(f"tree_mask must be contiguous int64 [{B},{T}]")
     with _on(dev):
         if out is None:
-            out = _new((B, T, H, 512), out_dtype, dev, stream)
-        if out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (B, T, H, 512) \
+            out = _new(q_nope, (B, T, H, 512), out_dtype, stream)
+        if out.dtype not in (torch.float32, torch.bfloat16) or out.shape != (B, T, H, 512) \
                 or not out.is_contiguous():
             raise ValueError(f"out must be contiguous fp32 or bf16 [{B},{T},{H},512]")
         if lse is None and with_lse:
-            lse = _new((B, T, H), torch.float32, dev, stream)
-        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, T, H) or not lse.is_contiguous()):
+            lse = _new(q_nope, (B, T, H), torch.float32, stream)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous()):
             raise ValueError(f"lse must be contiguous fp32 [{B},{T},{H}]")
-        _check("mla_decode_tree", lib().mla_decode_tree(
-            ws.ptr(), ws.nbytes, _ptr(q_nope), _ptr(q_rope), _ptr(cache), kind, cache.shape[0], _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), _ptr(tree_lens), _ptr(tree_mask), B, T, H, float(softmax_scale),
-            _ptr(out), 1 if out.dtype == torch.bfloat16 else 0, _ptr(lse), _stream(stream)))
+        st = lib().mla_decode_tree(
+            ws.buf.data_ptr(), ws.nbytes, q_nope.data_ptr(), q_rope.data_ptr(), cache.data_ptr(), kind,
+            cache.shape[0], block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), _at(tree_lens),
+            tree_mask.data_ptr(), B, T, H, softmax_scale, out.data_ptr(), 1 if out.dtype == torch.bfloat16 else 0,
+            _at(lse), _raw(stream, dev))
+    if st:
+        _check("mla_decode_tree", st)
     return out, lse
 
 
@@ -713,9 +738,8 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
     [0,1), parents int32 [B,T] (-1: the last committed token; None: a chain), tree_lens int32 [B]
     -> (num_accepted int32 [B], depths int32 [B,T]: place among the accepted tokens or -1,
     next_token int32 [B])."""
-    dev = _device_of(("target_probs", target_probs), ("draft_probs", draft_probs), ("draft_tokens", draft_tokens),
-                     ("uniforms", uniforms), ("parents", parents), ("tree_lens", tree_lens),
-                     ("device_status", device_status))
+    dev = _device_of(target_probs, target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
+                     uniforms=uniforms, parents=parents, tree_lens=tree_lens, device_status=device_status)
     if draft_tokens.dim() != 2 or target_probs.dim() != 3:
         raise ValueError("draft_tokens must be int32 [B,T], target_probs fp32 [B,T+1,V]")
     B, T = draft_tokens.shape
@@ -723,7 +747,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
     _ints(draft_tokens, (B, T), "draft_tokens")
     for t, shape, name in ((target_probs, (B, T + 1, V), "target_probs"), (draft_probs, (B, T, V), "draft_probs"),
                            (uniforms, (B, T + 1), "uniforms")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous fp32 {list(shape)}")
     if parents is not None:
         _ints(parents, (B, T), "parents")
@@ -731,12 +755,15 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
         _ints(tree_lens, (B,), "tree_lens")
     _status_word(device_status)
     with _on(dev):
-        num = _new((B,), torch.int32, dev, stream)
-        depths = _new((B, T), torch.int32, dev, stream)
-        nxt = _new((B,), torch.int32, dev, stream)
-        _check("mla_verify_draft", lib().mla_verify_draft(
-            _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(parents), _ptr(tree_lens),
-            _ptr(uniforms), B, T, V, _ptr(num), _ptr(depths), _ptr(nxt), _ptr(device_status), _stream(stream)))
+        num = _new(draft_tokens, (B,), torch.int32, stream)
+        depths = _new(draft_tokens, (B, T), torch.int32, stream)
+        nxt = _new(draft_tokens, (B,), torch.int32, stream)
+        st = lib().mla_verify_draft(
+            target_probs.data_ptr(), _at(draft_probs), draft_tokens.data_ptr(), _at(parents), _at(tree_lens),
+            uniforms.data_ptr(), B, T, V, num.data_ptr(), depths.data_ptr(), nxt.data_ptr(), _at(device_status),
+            _raw(stream, dev))
+    if st:
+        _check("mla_verify_draft", st)
     return num, depths, nxt
 
 

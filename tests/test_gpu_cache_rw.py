@@ -166,3 +166,21 @@ def test_long_cache_offsets_and_empty_calls():
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
     ops.cache_write(cache, bt, none, none, kv[:0])
     assert ops.cache_read(cache, bt, none, none).shape == (0, 576)
+
+
+def test_records_of_extreme_values_equal_the_oracle():
+    # blocks from the smallest bf16 values to the largest: scales below and above the range in
+    # which the quotient's Newton step is exact, subnormal ones among them
+    n = 260
+    bt, pages, req, pos, kv = _case(n, 2, 21)
+    kv = kv.contiguous()
+    g = torch.Generator().manual_seed(22)
+    e = torch.linspace(-133, 127, n).round()
+    kv[:, :512] = (torch.rand(n, 512, generator=g).double() * 1.99 - 0.99).mul(2.0 ** e.double()[:, None]).to(torch.bfloat16)
+    pool = _pool(True, pages, 3)
+    ref, err = oracle.append(pool.reshape(-1).numpy(), True, bt[req.long()].numpy(), pos.numpy(),
+                             _bits(kv[:, :512]), _bits(kv[:, 512:]))
+    assert err == 0
+    cache = pool.clone().cuda()
+    ops.cache_write(cache, bt.cuda(), req.cuda(), pos.cuda(), kv.cuda())
+    assert np.array_equal(cache.cpu().reshape(-1).numpy(), ref)
