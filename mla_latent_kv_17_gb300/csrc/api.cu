@@ -258,6 +258,7 @@ combine_kernel(DecodeArgs a) {
             const int rq = b % a.reqs, y = b / a.reqs * kRowTile + h;
             if (y >= a.T * a.heads) continue;
             orow = (int64_t)rq * a.T * a.heads + y;
+            if (y >= tree_len(a.tree_lens, a.seq_lens, a.T, rq) * a.heads) n = 0;  // a padded row: no pieces
         }
         const float *plse = part_lse + (int64_t)s0 * H + h;
         const float4 *po = part_o + ((int64_t)s0 * H + h) * (kDLatent / 4);

@@ -1322,7 +1322,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     const int n = tree_len(a.tree_lens, a.seq_lens, a.T, rq);
                     if (h == 0 && rank == 0 && (n != (a.tree_lens ? a.tree_lens[rq] : a.T) || a.seq_lens[rq] < 0))
                         record_error(a.status, MLA_ERR_INDEX);  // clamped
-                    rows = min(kRowTile, a.T * a.heads - y0);
+                    // (a partial result's padded rows are neither written nor read)
+                    rows = min(kRowTile, (w.slot < 0 ? a.T : n) * a.heads - y0);
                     live = token < n;
                     first = total - n;
                     tbits = live ? a.tree_mask[(int64_t)rq * a.T + token] : 0ull;

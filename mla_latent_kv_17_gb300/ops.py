@@ -447,8 +447,9 @@ def _on(dev: int):
 
 
 def _raw(stream, dev: int) -> int:
-    """The handle of `stream`, or of the device's current stream."""
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    """The handle of `stream`, or of the device's current stream (asked for without building the
+    Stream object, a microsecond of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _at(t) -> int:
@@ -494,7 +495,8 @@ def rope_frequencies(d_rot: int = 64, base: float = 10000.0, scaling: str = "non
     'none'; 'linear' (f / factor: positions interpolated); 'ntk' (base * factor^(d/(d-2)): the
     highest frequency kept, the lowest divided by factor); 'yarn' (frequencies that turn more
     than beta_fast times over the trained length kept, those below beta_slow turns divided by
-    factor, a linear ramp over j between; mscale = 0.1 ln factor + 1 on the rotated values).
+    factor, a linear ramp over j between; mscale = 0.1 ln factor + 1 on the rotated values, of
+    queries and keys alike).
     """
     import math
     if d_rot < 2 or d_rot % 2 or not base > 1.0 or not (math.isfinite(factor) and factor >= 1.0):

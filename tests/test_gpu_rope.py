@@ -34,7 +34,7 @@ def check(x, pos, freqs, layout, mscale, got_pass, got_rot, d_pass):
 CASES = [  # tokens, heads, passing, rotated
     (1, 1, 128, 64), (1, 128, 128, 64), (7, 3, 128, 64), (300, 16, 128, 64), (33, 128, 64, 128), (5, 2, 0, 16),
     (9, 5, 8, 2), (4, 3, 3, 6), (2, 2, 5, 64), (6, 1, 512, 64), (3, 7, 16, 24), (2, 1, 0, 2048),
-    (1500, 1, 512, 64), (5000, 2, 0, 64)]
+    (1500, 1, 512, 64), (5000, 2, 0, 64), (3, 2, 1003, 10), (2, 130, 24, 16)]
 
 
 @pytest.mark.parametrize("layout", ["interleaved", "half"])

@@ -119,6 +119,28 @@ def test_chain_equals_decode_of_each_prefix():
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_split_pieces_of_padded_rows(kv):
+    # few real rows in a split tile: the padded ones have no partial results and come out empty
+    d = make(2, 8, 16, [30000, 12000], lens=[3, 1], kv=kv, seed=16)
+    d["qn"][0, 3:], d["qr"][0, 3:] = float("nan"), float("nan")
+    out, lse, ws = both(d, torch.bfloat16, f"padded {kv}")
+    assert bool((out[0, 3:] == 0).all()) and bool(torch.isneginf(lse[1, 1:]).all())
+
+
+def test_one_plan_serves_several_calls():
+    # the layers of a model share lengths: one plan, other queries and caches
+    d, e = (make(3, 4, 32, [900, 64, 3000], seed=s) for s in (17, 18))
+    ws = ops.TreeWorkspace(3, 4, 32)
+    ops.plan_tree(ws, d["seq"], d["lens"])
+    got = [ops.decode_tree(ws, x["qn"], x["qr"], x["cache"], x["bt"], x["seq"], x["lens"], x["mask"], tree_ref.SCALE)
+           for x in (d, e, d)]
+    assert ops.status(ws) == 0
+    for x, (o, l) in zip((d, e), got):
+        tree_ref.check(o, l, tree_ref.tree(x["qn"], x["qr"], x["cache"], x["bt"], x["seq"], x["lens"], x["mask"]))
+    assert torch.equal(got[0][0], got[2][0]) and torch.equal(got[0][1], got[2][1])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_masks_that_leave_a_row_empty(kv):
     d = make(3, 5, 20, [0, 0, 70], kv=kv, seed=12)
     d["mask"][0] = 0                     # no context and no ancestors: nothing is attended
