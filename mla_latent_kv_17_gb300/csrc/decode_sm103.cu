@@ -660,38 +660,81 @@ __device__ __forceinline__ void expand_chunk(uint4 v, float s, uint8_t *box, int
     *reinterpret_cast<uint4 *>(box + (((2 * q + 1) ^ (r & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// FP8 records: the jobs of the latent-half ring (which 0: own(0), own(1), peer(0), then
-// peer(g + 1), own(g + 2) for g = 0, 1, ...), of the other-columns stage (which 1: oth(g),
-// one per tile), or all of them in the order they are consumed (which 2: oth(0), own(0),
-// own(1), peer(0), then oth(g + 1), peer(g + 1), own(g + 2)).  f(kind, g, cursor): kind 0 own
-// page, 1 peer page, 2 other columns.  Every job comes after the jobs whose consumers free its
+// FP8 records: the jobs of the latent-half ring (kWhich 0: own(0), own(1), peer(0), then
+// peer(g + 1), own(g + 2) for g = 0, 1, ...), of the other-columns stage (kWhich 1: oth(g),
+// one per tile), or all of them in the order they are consumed (kWhich 2: oth(0), own(0),
+// own(1), peer(0), then oth(g + 1), peer(g + 1), own(g + 2)).  Kind 0 own page, 1 peer page,
+// 2 other columns.  Every job comes after the jobs whose consumers free its
 // buffer: peer(g + 1) and own(g + 2) take the slots PV(g) frees, oth(g + 1) the stage QK(g)
 // frees; and peer(g + 1), which PV(g + 1) waits for, goes before own(g + 2), which only
-// QK(g + 2) needs.  One call site of f: the job bodies are large.
-template <typename F>
-__device__ bool fp8_jobs(const TileCursor &start, int which, F &&f) {
-    TileCursor cur[3] = {start, start, start};  // next own, peer, other-columns job
-    uint32_t gk[3] = {0u, 0u, 0u};
-    for (int step = 0;; ++step) {
-        int kind;
-        if (which == 1) {
-            kind = 2;
-        } else if (which == 0) {
-            kind = step < 3 ? (step < 2 ? 0 : 1) : ((step - 3) & 1) ? 0 : 1;
-        } else {
-            const int k = (step - 4) % 3;
-            kind = step < 4 ? (step == 0 ? 2 : step < 3 ? 0 : 1) : k == 0 ? 2 : k == 1 ? 1 : 0;
+// QK(g + 2) needs.
+// The jobs of a step touch two neighbouring tiles, kept in registers as they slide along (three
+// cursors picked by kind lay in local memory and cost ~650 cycles between two jobs).
+template <int kWhich>
+struct Fp8Jobs {
+    struct Tile {
+        WorkItem w;  // t1 < t0: none
+        int t;
+    };
+    TileCursor cur;  // the tile after `hi`
+    Tile lo, hi;
+    uint32_t g;      // number of tile `lo`
+    int r;           // place in the opening (negative) or in the round
+    // the job next() found
+    int kind;
+    uint32_t tile;
+    Tile at;
+
+    __device__ Tile take() {
+        Tile x{WorkItem{0, 1, 0, -1}, 0};
+        if (!cur.done()) {
+            x.w = cur.w;
+            x.t = cur.t;
+            cur.next();
         }
-        if (cur[kind].done()) {
-            const bool dh_done = cur[0].done() && cur[1].done();
-            if (which == 0 ? dh_done : which == 1 ? true : dh_done && cur[2].done()) return true;
-            continue;
-        }
-        if (!f(kind, gk[kind], cur[kind])) return false;
-        ++gk[kind];
-        cur[kind].next();
+        return x;
     }
-}
+    __device__ static bool none(const Tile &x) { return x.w.t1 < x.w.t0; }
+    __device__ explicit Fp8Jobs(const TileCursor &start) : cur(start), g(0), r(kWhich == 2 ? -4 : kWhich == 0 ? -3 : 0) {
+        lo = take();
+        hi = take();
+    }
+    __device__ bool next() {
+        for (;;) {
+            bool upper;  // the job belongs to tile `hi`
+            if (kWhich == 1) {
+                if (none(lo)) return false;
+                kind = 2;
+                upper = false;
+            } else if (r < 0) {
+                // opening: [oth(0)] own(0) own(1) peer(0)
+                kind = r == -4 ? 2 : r == -1 ? 1 : 0;
+                upper = r == -2;
+            } else {
+                if (r == 0) {  // the round of tiles g + 1 and g + 2
+                    lo = hi;
+                    hi = take();
+                    ++g;
+                }
+                if (none(lo)) return false;
+                const bool last = r == (kWhich == 2 ? 2 : 1);
+                kind = last ? 0 : kWhich == 2 && r == 0 ? 2 : 1;
+                upper = last;
+            }
+            at = upper ? hi : lo;
+            tile = g + (upper ? 1u : 0u);
+            if (kWhich == 1) {
+                lo = hi;
+                hi = take();
+                ++g;
+            } else {
+                ++r;
+                if (r == (kWhich == 2 ? 3 : 2)) r = 0;
+            }
+            if (!none(at)) return true;
+        }
+    }
+};
 
 // kMode 0: dense bf16 tiles (128 consecutive tokens, two pages, 64-row boxes).
 // kMode 1: DSA sparse tiles (128 index slots gathered row by row, tile::gather4).
@@ -790,10 +833,24 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         const int r = 32 * (eidx & 1) + lane, p = eidx >> 1;
         TileCursor start;
         start.begin(unit_begin, items, units, cl, ncl);
-        const bool ok = fp8_jobs(start, 2, [&](int kind, uint32_t g, const TileCursor &t) -> bool {
+        // The next job's page id is read while the present job is worked on.
+        Fp8Jobs<2> jobs(start);
+        auto raw_page = [&]() -> int32_t {
+            const int lp = (jobs.at.t + kPageRows * (jobs.kind == 1 ? (int)peer : (int)rank)) / kPageRows;
+            return lp < a.max_pages ? ld_early(a.block_table + (int64_t)item_request<kTree>(jobs.at.w.b) * a.max_pages + lp) : -1;
+        };
+        bool have = jobs.next(), ok = true;
+        int32_t next_id = have ? raw_page() : -1;
+        while (have && ok) {
+            const int kind = jobs.kind;
+            const uint32_t g = jobs.tile;
+            const int left = jobs.at.w.t1 - (jobs.at.t + kPageRows * (kind == 1 ? (int)peer : (int)rank));
             // a page that was not loaded (past the item's end, or an id out of range) is not
             // expanded; its stage only completes
-            const PageRef pg = page_of<kTree>(a, t.w, t.t, kind == 1 ? (int)peer : (int)rank);
+            const PageRef pg{min(kPageRows, max(0, left)),
+                             next_id >= 0 && next_id < a.num_pages ? (int64_t)next_id : (int64_t)-1};
+            have = jobs.next();
+            if (have) next_id = raw_page();
             int raw_bar, half;
             uint32_t raw_phase, region, scale_off, full_bar;
             if (kind == 2) {
@@ -812,7 +869,10 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 half = (int)rank;
                 full_bar = bar(base, d.full);
             }
-            if (!warp_wait(c, bar(base, raw_bar), raw_phase & 1u, false)) return false;
+            if (!warp_wait(c, bar(base, raw_bar), raw_phase & 1u, false)) {
+                ok = false;
+                break;
+            }
             if (pg.rows > 0 && pg.id >= 0) {
                 const float sc = reinterpret_cast<const float *>(gbase + scale_off + r * 16)[2 * half + p];
                 // code x scale must stay inside the fp16 range of the operand (|x| <= 65504);
@@ -838,8 +898,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(full_bar);
-            return true;
-        });
+        }
         if (!ok && lane == 0) drain_pause();
     } else if (kFp8 && (warp == 8 || warp == 11)) {
         // ------------------------------------------------------------ FP8 raw loads (one thread each:
@@ -847,10 +906,13 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         if (lane == 0) {
             TileCursor start;
             start.begin(unit_begin, items, units, cl, ncl);
-            const bool ok = fp8_jobs(start, warp == 8 ? 0 : 1, [&](int kind, uint32_t g, const TileCursor &t) -> bool {
-                if (kind == 2) {
-                    const PageRef pg = page_of<kTree>(a, t.w, t.t, (int)rank);  // read before the wait
-                    if (!wait_bar(c, bar(base, B_OTH_EMPTY), (g & 1u) ^ 1u, false)) return false;
+            bool ok = true;
+            if (warp == 11) {
+                Fp8Jobs<1> jobs(start);
+                while (ok && jobs.next()) {
+                    const PageRef pg = page_of<kTree>(a, jobs.at.w, jobs.at.t, (int)rank);  // read before the wait
+                    ok = wait_bar(c, bar(base, B_OTH_EMPTY), (jobs.tile & 1u) ^ 1u, false);
+                    if (!ok) break;
                     const uint32_t rb = bar(base, B_RAW + 3), dst = base + kOffOth;
                     if (pg.rows > 0 && pg.id >= 0) {
                         const int32_t y = (int32_t)(pg.id * kPageRows);
@@ -862,25 +924,27 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     } else {
                         mbar_arrive(rb);
                     }
-                    return true;
                 }
-                const PageRef pg = page_of<kTree>(a, t.w, t.t, kind == 0 ? (int)rank : (int)peer);
-                const DhSlot d = dh_slot<kSparse>(g, kind);
-                if (d.fill > 0 && !wait_bar(c, bar(base, B_DH_EMPTY + d.slot), (d.fill - 1u) & 1u, false))
-                    return false;
-                const uint32_t rb = bar(base, B_RAW + d.slot), dst = base + kOffDh + d.slot * kDhBytes;
-                if (pg.rows > 0 && pg.id >= 0) {
-                    const int32_t y = (int32_t)(pg.id * kPageRows);
-                    mbar_arrive_expect_tx(rb, 16384 + kScaleBytes);
-                    tma_load_2d(dst, &tmap, 256 * (int)rank, y, rb);  // own latent half, codes
-                    tma_load_2d(dst + 2 * kBox, &tmap, 256 * (int)rank + 128, y, rb);
-                    tma_load_2d(base + kOffScale + d.slot * kScaleBytes, &tmap_sc, kDLatent, y, rb);
-                } else {
-                    if (pg.rows > 0) record_error(a.status, MLA_ERR_INDEX);
-                    mbar_arrive(rb);
+            } else {
+                Fp8Jobs<0> jobs(start);
+                while (ok && jobs.next()) {
+                    const PageRef pg = page_of<kTree>(a, jobs.at.w, jobs.at.t, jobs.kind == 0 ? (int)rank : (int)peer);
+                    const DhSlot d = dh_slot<kSparse>(jobs.tile, jobs.kind);
+                    ok = d.fill == 0 || wait_bar(c, bar(base, B_DH_EMPTY + d.slot), (d.fill - 1u) & 1u, false);
+                    if (!ok) break;
+                    const uint32_t rb = bar(base, B_RAW + d.slot), dst = base + kOffDh + d.slot * kDhBytes;
+                    if (pg.rows > 0 && pg.id >= 0) {
+                        const int32_t y = (int32_t)(pg.id * kPageRows);
+                        mbar_arrive_expect_tx(rb, 16384 + kScaleBytes);
+                        tma_load_2d(dst, &tmap, 256 * (int)rank, y, rb);  // own latent half, codes
+                        tma_load_2d(dst + 2 * kBox, &tmap, 256 * (int)rank + 128, y, rb);
+                        tma_load_2d(base + kOffScale + d.slot * kScaleBytes, &tmap_sc, kDLatent, y, rb);
+                    } else {
+                        if (pg.rows > 0) record_error(a.status, MLA_ERR_INDEX);
+                        mbar_arrive(rb);
+                    }
                 }
-                return true;
-            });
+            }
             if (!ok) drain_pause();
         }
     } else if (warp == 4 || warp == 7 || (kSparse && warp >= 8)) {
