@@ -660,18 +660,65 @@ __device__ __forceinline__ void expand_chunk(uint4 v, float s, uint8_t *box, int
     *reinterpret_cast<uint4 *>(box + (((2 * q + 1) ^ (r & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// FP8 records: the jobs of the latent-half ring (kWhich 0: own(0), own(1), peer(0), then
-// peer(g + 1), own(g + 2) for g = 0, 1, ...), of the other-columns stage (kWhich 1: oth(g),
-// one per tile), or all of them in the order they are consumed (kWhich 2: oth(0), own(0),
-// own(1), peer(0), then oth(g + 1), peer(g + 1), own(g + 2)).  Kind 0 own page, 1 peer page,
-// 2 other columns.  Every job comes after the jobs whose consumers free its
-// buffer: peer(g + 1) and own(g + 2) take the slots PV(g) frees, oth(g + 1) the stage QK(g)
-// frees; and peer(g + 1), which PV(g + 1) waits for, goes before own(g + 2), which only
-// QK(g + 2) needs.
-// The jobs of a step touch two neighbouring tiles, kept in registers as they slide along (three
-// cursors picked by kind lay in local memory and cost ~650 cycles between two jobs).
+// Tree decode: the same expansion in packed fp16 arithmetic, half as many instructions.  The scale
+// is split into two fp16 parts, so that code x scale = code x hi + code x lo is one product (tiny)
+// and one fused multiply-add, rounded once; a scale of 2^-10 or more is then held to 2^-15 of
+// itself, and the result is off by 2^-11 (1 + 2^-4) of its value at most.  Smaller scales (whose
+// parts would lie among fp16's subnormals) take expand_chunk, out of line.
+struct ScaleParts {
+    uint32_t hi, lo;  // fp16 pairs
+};
+__device__ __forceinline__ ScaleParts split_scale(float s) {
+    const __half h = __float2half_rn(s), l = __float2half_rn(s - __half2float(h));
+    const __half2 hh = __half2half2(h), ll = __half2half2(l);
+    return ScaleParts{*reinterpret_cast<const uint32_t *>(&hh), *reinterpret_cast<const uint32_t *>(&ll)};
+}
+__device__ __forceinline__ bool scale_splits(float s) { return s >= 0x1p-10f && s <= 128.f; }
+__device__ __forceinline__ uint32_t e4m3x2_times(uint32_t two, const ScaleParts &s) {
+    uint32_t c, t, r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(c) : "r"(two));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(c), "r"(s.lo));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(s.hi), "r"(t));
+    return r;
+}
+__device__ __forceinline__ void expand_chunk_packed(uint4 v, const ScaleParts &s, uint8_t *box, int q, int r) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        o[2 * k] = e4m3x2_times(w[k], s);
+        o[2 * k + 1] = e4m3x2_times(w[k] >> 16, s);
+    }
+    *reinterpret_cast<uint4 *>(box + (((2 * q) ^ (r & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4 *>(box + (((2 * q + 1) ^ (r & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+__device__ __noinline__ void expand_chunk_ool(uint4 v, float s, uint8_t *box, int q, int r) {
+    expand_chunk(v, s, box, q, r);
+}
+
+// FP8 records: what the expansion warps do, in order: oth(0), own(0), own(1), oth(1), peer(0), then
+// oth(g + 2), peer(g + 1), own(g + 2) for g = 0, 1, ... (tiles past the last are left out).  Kind 0
+// own page, 1 peer page, 2 other columns.  Every job comes after the jobs whose consumers free its
+// buffer: peer(g + 1) and own(g + 2) take the slots PV(g) frees, oth(g + 2) the stage QK(g + 1)
+// frees; and peer(g + 1), which PV(g + 1) waits for, goes before own(g + 2), which only QK(g + 2)
+// needs.  oth(g + 2), whose codes are there by then, fills the time the codes of the other two take
+// to land after PV(g): with oth(g + 1) in its place a step of the FP8-ragged workload took 368 us
+// instead of 338.
+struct Fp8Job {
+    int kind, tile;
+};
+__device__ __forceinline__ Fp8Job fp8_job(int n) {
+    if (n < 5) return Fp8Job{n == 0 || n == 3 ? 2 : n == 4 ? 1 : 0, n == 2 || n == 3 ? 1 : 0};
+    const int g = (n - 5) / 3, k = (n - 5) % 3;
+    return Fp8Job{k == 0 ? 2 : k == 1 ? 1 : 0, k == 1 ? g + 1 : g + 2};
+}
+__device__ __forceinline__ int fp8_job_count(int ntiles) { return ntiles > 0 ? 5 + 3 * (ntiles - 1) : 0; }
+
+// The loads of the latent-half ring for them (kWhich 0: own(0), own(1), peer(0), then peer(g + 1),
+// own(g + 2)) and of the other-columns stage (kWhich 1: oth(g)), with the places they come from.
+// The jobs of a step touch two neighbouring tiles, kept in registers as they slide along.
 template <int kWhich>
-struct Fp8Jobs {
+struct Fp8Loads {
     struct Tile {
         WorkItem w;  // t1 < t0: none
         int t;
@@ -695,20 +742,24 @@ struct Fp8Jobs {
         return x;
     }
     __device__ static bool none(const Tile &x) { return x.w.t1 < x.w.t0; }
-    __device__ explicit Fp8Jobs(const TileCursor &start) : cur(start), g(0), r(kWhich == 2 ? -4 : kWhich == 0 ? -3 : 0) {
+    __device__ explicit Fp8Loads(const TileCursor &start) : cur(start), g(0), r(kWhich == 0 ? -3 : 0) {
         lo = take();
         hi = take();
     }
     __device__ bool next() {
         for (;;) {
-            bool upper;  // the job belongs to tile `hi`
             if (kWhich == 1) {
                 if (none(lo)) return false;
                 kind = 2;
-                upper = false;
-            } else if (r < 0) {
-                // opening: [oth(0)] own(0) own(1) peer(0)
-                kind = r == -4 ? 2 : r == -1 ? 1 : 0;
+                tile = g++;
+                at = lo;
+                lo = hi;
+                hi = take();
+                return true;
+            }
+            bool upper;  // the job belongs to tile `hi`
+            if (r < 0) {
+                kind = r == -1 ? 1 : 0;
                 upper = r == -2;
             } else {
                 if (r == 0) {  // the round of tiles g + 1 and g + 2
@@ -717,20 +768,12 @@ struct Fp8Jobs {
                     ++g;
                 }
                 if (none(lo)) return false;
-                const bool last = r == (kWhich == 2 ? 2 : 1);
-                kind = last ? 0 : kWhich == 2 && r == 0 ? 2 : 1;
-                upper = last;
+                kind = 1 - r;
+                upper = r == 1;
             }
             at = upper ? hi : lo;
             tile = g + (upper ? 1u : 0u);
-            if (kWhich == 1) {
-                lo = hi;
-                hi = take();
-                ++g;
-            } else {
-                ++r;
-                if (r == (kWhich == 2 ? 3 : 2)) r = 0;
-            }
+            if (++r == 2) r = 0;
             if (!none(at)) return true;
         }
     }
@@ -762,7 +805,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(gbase + kOffMisc);
-    // misc[0]: TMEM base address, misc[1]: abort flag
+    // misc[0]: TMEM base address, misc[1]: abort flag, misc[2..5]: FP8 records, valid rows of the
+    // page in raw stage 0..3
     Ctx c{base, a.status, misc + 1, a.wait_cycles};
 
     if (threadIdx.x == 0) {
@@ -831,26 +875,19 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         // read into registers beforehand.  No thread writes another thread's codes.
         const int eidx = warp == 4 ? 0 : warp == 10 ? 1 : warp == 7 ? 2 : 3;
         const int r = 32 * (eidx & 1) + lane, p = eidx >> 1;
-        TileCursor start;
-        start.begin(unit_begin, items, units, cl, ncl);
-        // The next job's page id is read while the present job is worked on.
-        Fp8Jobs<2> jobs(start);
-        auto raw_page = [&]() -> int32_t {
-            const int lp = (jobs.at.t + kPageRows * (jobs.kind == 1 ? (int)peer : (int)rank)) / kPageRows;
-            return lp < a.max_pages ? ld_early(a.block_table + (int64_t)item_request<kTree>(jobs.at.w.b) * a.max_pages + lp) : -1;
-        };
-        bool have = jobs.next(), ok = true;
-        int32_t next_id = have ? raw_page() : -1;
-        while (have && ok) {
-            const int kind = jobs.kind;
-            const uint32_t g = jobs.tile;
-            const int left = jobs.at.w.t1 - (jobs.at.t + kPageRows * (kind == 1 ? (int)peer : (int)rank));
-            // a page that was not loaded (past the item's end, or an id out of range) is not
-            // expanded; its stage only completes
-            const PageRef pg{min(kPageRows, max(0, left)),
-                             next_id >= 0 && next_id < a.num_pages ? (int64_t)next_id : (int64_t)-1};
-            have = jobs.next();
-            if (have) next_id = raw_page();
+        // The order is fp8_job's; what a page holds (its valid rows, 0: not loaded) the raw loader
+        // leaves beside its stage, so these warps walk no work items and read no block table: they
+        // set the pace of this mode, and that walk cost some 700 cycles between two jobs.
+        int ntiles = 0;
+        for (int u = cl; u < units; u += ncl)
+            for (int it = unit_begin[u]; it < unit_begin[u + 1]; ++it)
+                if (items[it].t1 > items[it].t0) ntiles += (items[it].t1 - items[it].t0 + kTile - 1) / kTile;
+        bool ok = true;
+        for (int n = 0; n < fp8_job_count(ntiles) && ok; ++n) {
+            const Fp8Job job = fp8_job(n);
+            if (job.tile >= ntiles) continue;
+            const int kind = job.kind;
+            const uint32_t g = (uint32_t)job.tile;
             int raw_bar, half;
             uint32_t raw_phase, region, scale_off, full_bar;
             if (kind == 2) {
@@ -873,27 +910,48 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 ok = false;
                 break;
             }
-            if (pg.rows > 0 && pg.id >= 0) {
+            // a page that was not loaded (past the item's end, or an id out of range) is not
+            // expanded; its stage only completes
+            const int rows = misc[2 + raw_bar - B_RAW];
+            if (rows > 0) {
                 const float sc = reinterpret_cast<const float *>(gbase + scale_off + r * 16)[2 * half + p];
                 // code x scale must stay inside the fp16 range of the operand (|x| <= 65504);
                 // rows past the item's end may hold anything and are not checked
-                if (r < pg.rows && !(fabsf(sc) * 448.f <= kF16Max)) record_error(a.status, MLA_ERR_RANGE);
+                if (r < rows && !(fabsf(sc) * 448.f <= kF16Max)) record_error(a.status, MLA_ERR_RANGE);
                 uint8_t *row = gbase + region + r * 128;                 // row r of box 0
                 const uint8_t *codes = row + 2 * p * kBox;               // its 8 chunks of 16 codes
                 uint8_t *first = row + 2 * p * kBox, *second = first + kBox;
-                uint4 v[4];  // chunks (i + r) % 4, read before their box is overwritten
+                if constexpr (kTree) {
+                    // all eight chunks are read before either box is written
+                    uint4 v[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(codes + ((i + r) & 3) * 16);
-                // chunks 4 + (i + r) % 4 -> second box (rotated: no bank conflicts on the stores)
-                uint4 nxt = *reinterpret_cast<const uint4 *>(codes + (4 + (r & 3)) * 16);
+                    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4 *>(codes + ((i + r) & 7) * 16);
+                    const bool packed = __all_sync(0xffffffffu, scale_splits(sc));
+                    const ScaleParts sp = split_scale(sc);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int q = (i + r) & 7;
+                        uint8_t *box = q < 4 ? first : second;
+                        if (packed)
+                            expand_chunk_packed(v[i], sp, box, q & 3, r);
+                        else
+                            expand_chunk_ool(v[i], sc, box, q & 3, r);
+                    }
+                } else {
+                    uint4 v[4];  // chunks (i + r) % 4, read before their box is overwritten
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(codes + ((i + r) & 3) * 16);
+                    // chunks 4 + (i + r) % 4 -> second box (rotated: no bank conflicts on the stores)
+                    uint4 nxt = *reinterpret_cast<const uint4 *>(codes + (4 + (r & 3)) * 16);
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 cur = nxt;
-                    if (i < 3) nxt = *reinterpret_cast<const uint4 *>(codes + (4 + ((i + 1 + r) & 3)) * 16);
-                    expand_chunk(cur, sc, second, (i + r) & 3, r);
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 cur = nxt;
+                        if (i < 3) nxt = *reinterpret_cast<const uint4 *>(codes + (4 + ((i + 1 + r) & 3)) * 16);
+                        expand_chunk(cur, sc, second, (i + r) & 3, r);
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) expand_chunk(v[i], sc, first, (i + r) & 3, r);
+                    for (int i = 0; i < 4; ++i) expand_chunk(v[i], sc, first, (i + r) & 3, r);
+                }
                 fence_proxy_async_smem();
             }
             __syncwarp();
@@ -908,12 +966,13 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
             start.begin(unit_begin, items, units, cl, ncl);
             bool ok = true;
             if (warp == 11) {
-                Fp8Jobs<1> jobs(start);
+                Fp8Loads<1> jobs(start);
                 while (ok && jobs.next()) {
                     const PageRef pg = page_of<kTree>(a, jobs.at.w, jobs.at.t, (int)rank);  // read before the wait
                     ok = wait_bar(c, bar(base, B_OTH_EMPTY), (jobs.tile & 1u) ^ 1u, false);
                     if (!ok) break;
                     const uint32_t rb = bar(base, B_RAW + 3), dst = base + kOffOth;
+                    misc[2 + 3] = pg.id >= 0 ? pg.rows : 0;  // (before the arrival below)
                     if (pg.rows > 0 && pg.id >= 0) {
                         const int32_t y = (int32_t)(pg.id * kPageRows);
                         mbar_arrive_expect_tx(rb, 16384 + kScaleBytes + kBox);
@@ -926,13 +985,14 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     }
                 }
             } else {
-                Fp8Jobs<0> jobs(start);
+                Fp8Loads<0> jobs(start);
                 while (ok && jobs.next()) {
                     const PageRef pg = page_of<kTree>(a, jobs.at.w, jobs.at.t, jobs.kind == 0 ? (int)rank : (int)peer);
                     const DhSlot d = dh_slot<kSparse>(jobs.tile, jobs.kind);
                     ok = d.fill == 0 || wait_bar(c, bar(base, B_DH_EMPTY + d.slot), (d.fill - 1u) & 1u, false);
                     if (!ok) break;
                     const uint32_t rb = bar(base, B_RAW + d.slot), dst = base + kOffDh + d.slot * kDhBytes;
+                    misc[2 + d.slot] = pg.id >= 0 ? pg.rows : 0;
                     if (pg.rows > 0 && pg.id >= 0) {
                         const int32_t y = (int32_t)(pg.id * kPageRows);
                         mbar_arrive_expect_tx(rb, 16384 + kScaleBytes);

@@ -226,3 +226,16 @@ def test_stall_is_reported_and_the_workspace_stays_usable():
         ops.set_wait_limit(0)
     got = run(d)
     assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -14, 2.0 ** -3, 40.0])
+def test_fp8_scales_of_other_magnitudes(scale):
+    # record scales below, inside and at the top of the range in which they are split into fp16
+    # parts, and a batch that mixes them
+    d = make(2, 3, 20, [300, 90], kv="fp8", seed=19)
+    s = d["cache"][..., 512:528].view(torch.float32)
+    s.mul_(scale * 448 / 3)              # (about max |x| / 448 = 3 / 448 before)
+    d["qn"] = (d["qn"].float() / max(1.0, scale * 100)).to(torch.bfloat16)
+    both(d, torch.float32, f"scale {scale}")
+    s[:, ::3] *= 2.0 ** -9
+    both(d, torch.float32, f"mixed {scale}")

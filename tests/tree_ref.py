@@ -21,7 +21,8 @@ def tree(qn, qr, cache, bt, seq, lens, mask, scale=SCALE):
 
     The kernel's scores are fp32 sums of 576 exact products: off by at most 576 x 2^-23 (its
     accumulator may cut instead of round) of scale sum |q||c|, d below; FP8 latents also enter as
-    fp16 (2^-11 |x|, 2^-25 below the normal range).  A weight is off by the factor e^2d (its score and the
+    fp16 (2^-11 (1 + 2^-4) |x|: one rounding of code x scale, the scale held to 2^-15; 2^-25 below the
+    normal range).  A weight is off by the factor e^2d (its score and the
     normaliser) and is rounded to bf16 (2^-8; fp16 for FP8 records 2^-11) when formed and once more when its page is
     rescaled; the values of FP8 records are rounded once (2^-11)."""
     B, T, H, _ = qn.shape
@@ -48,9 +49,9 @@ def tree(qn, qr, cache, bt, seq, lens, mask, scale=SCALE):
             out[b, i] = p @ k[:, :512]
             d = (q.abs() @ k.T.abs()).amax(-1) * scale * 576 * 2.0 ** -23
             if fp8:
-                d = d + (q[:, :512].abs() @ (2.0 ** -11 * k[:, :512].abs() + 2.0 ** -25).T).amax(-1) * scale
+                d = d + (q[:, :512].abs() @ (2.0 ** -11 * (1 + 2.0 ** -4) * k[:, :512].abs() + 2.0 ** -25).T).amax(-1) * scale
             mean = p @ k[:, :512].abs()
-            bo[b, i] = mean * (2 * half + (half if fp8 else 0.0) + 2.1 * d[:, None]) * 1.01
+            bo[b, i] = mean * (2 * half + (half * (1 + 2.0 ** -4) if fp8 else 0.0) + 2.1 * d[:, None]) * 1.01
             bl[b, i] = d + 2.0 ** -20 * (1 + lse[b, i].abs())
     return out, lse, bo, bl
 
