@@ -40,12 +40,14 @@ struct VerifyArgs {
     int *status;
 };
 
-// A probability as a multiple of 2^-58 (NaN and negative values: 0, above 1: 1): the significand
-// at the top of a 64-bit word, shifted down by what the exponent lacks (shifts of 64 and more
-// give 0).  The conversion instruction to 64-bit integers runs on the fp64 pipe, which it kept
-// 75 % busy: 53 us for 64 x 131,072 against 22 us.
+// A probability as it counts (NaN and negative values: 0, above 1: 1).
+__device__ __forceinline__ float counted(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+
+// The same as a multiple of 2^-58: the significand at the top of a 64-bit word, shifted down by
+// what the exponent lacks (shifts of 64 and more give 0).  The conversion instruction to 64-bit
+// integers runs on the fp64 pipe, which it kept 75 % busy: 53 us for 64 x 131,072 against 22 us.
 __device__ __forceinline__ uint64_t fixed58(float p) {
-    const uint32_t b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
+    const uint32_t b = __float_as_uint(counted(p));
     const uint64_t m = (uint64_t)((b << 8) | 0x80000000u) << 32;  // 2^63 x 1.fraction
     uint64_t r;
     asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(132u - (b >> 23)));
@@ -64,7 +66,7 @@ struct Residual {
 
     __device__ __forceinline__ uint64_t minus(uint64_t left, int k, float qv) const {
         // the first draft is subtracted exactly; later ones are scaled by the mass left
-        const uint64_t d = k == 0 ? fixed58(qv) : __double2ull_rz((double)(qv > 0.f ? fminf(qv, 1.f) : 0.f) * mass[k]);
+        const uint64_t d = k == 0 ? fixed58(qv) : __double2ull_rz((double)counted(qv) * mass[k]);
         return left > d ? left - d : 0;
     }
     __device__ __forceinline__ uint64_t at(int v) const {
@@ -168,7 +170,7 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
         // (fp64: 48-bit products, exact; by the token's own thread only, since the units are few)
         const float p = fine ? target[(int64_t)(par + 1) * V + x] : 0.f;
         const float q = fine && draft ? draft[(int64_t)tid * V + x] : 1.f;
-        s_stands[tid] = (double)u * (double)q < (double)p;
+        s_stands[tid] = (double)u * (double)counted(q) < (double)counted(p);
         if (wrong && rank == 0 && a.status) record_error(a.status, MLA_ERR_INDEX);
     }
     __syncthreads();
@@ -223,7 +225,7 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
         if (nrej > 0) {
             if (tid == 0) {
                 const double u = a.uniforms[(int64_t)b * (T + 1) + i];
-                s_answer = u * (double)(draft ? draft[(int64_t)i * V + x] : 1.f) * mass < (double)r.at(x);
+                s_answer = u * (double)(draft ? counted(draft[(int64_t)i * V + x]) : 1.f) * mass < (double)r.at(x);
             }
             __syncthreads();
             stands = s_answer;

@@ -111,6 +111,30 @@ def test_odd_values():
     assert int(status) == 5
 
 
+@pytest.mark.parametrize("sibling", [False, True])
+@pytest.mark.parametrize("q,p,want", [(-0.5, 0.0, 0), (-0.5, 0.25, 1), (float("nan"), 0.25, 1), (2.0, 0.6, 1), (2.0, 0.4, 0),
+                                      (float("inf"), 0.6, 1)])
+def test_a_draft_probability_out_of_range_counts_as_clamped(q, p, want, sibling):
+    # token x with u = 1/2: it stands where q/2 < p, for q clamped to [0, 1]; as a second sibling
+    # what is left has the mass 1 - 2^-3 (the first one, certain, takes 2^-3 and nothing of x)
+    V, x = 300, 17
+    T = 2 if sibling else 1
+    target, draft = torch.zeros(1, T + 1, V, device="cuda"), torch.zeros(1, T, V, device="cuda")
+    target[:, :, 5] = 0.125
+    target[:, :, x] = p
+    target[:, :, 200] = 0.875 - p
+    draft[0, -1, x] = q
+    tok = torch.full((1, T), x, dtype=torch.int32, device="cuda")
+    parents = torch.full((1, T), -1, dtype=torch.int32, device="cuda")
+    if sibling:
+        draft[0, 0, 5] = 1.0
+        tok[0, 0] = 5
+    u = torch.full((1, T + 1), 0.5, device="cuda")
+    u[0, 0] = 0.5
+    n, d, _ = run(target, draft, tok, u, parents)
+    assert int(n[0]) == want and int(d[0, -1]) == want - 1
+
+
 def test_a_draw_next_to_a_border():
     # 2^18 equal tokens: u k / 2^18 lies on a border, the first token past it is drawn
     V = 1 << 18
