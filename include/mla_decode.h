@@ -356,7 +356,8 @@ mla_status mla_decode_tree_plan_host(const int32_t *seq_lens, const int32_t *tre
  * are never accepted.  A token id outside [0, V) is rejected with its residual unchanged, a
  * tree_lens outside [0, T] is clamped; both record MLA_ERR_INDEX in *device_status
  * (optional).  1 <= T <= 64, 1 <= V <= 2^20.  Probabilities fp32, rows adding up to about 1;
- * values that are negative or NaN count as 0, above 1 as 1. */
+ * values that are negative or NaN count as 0, above 1 as 1.  (Rows that add up to 64 or more
+ * overflow the sums: some token of [0, V) is drawn then, or -1.) */
 mla_status mla_verify_draft(const float *target, const float *draft, const int32_t *tokens, const int32_t *parents,
                             const int32_t *tree_lens, const float *uniforms, int B, int T, int V,
                             int32_t *num_accepted, int32_t *depths, int32_t *next_token, int32_t *device_status,

@@ -292,11 +292,13 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
                 const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += y;
             }
+            // (sums that overflowed, of rows far from adding up to 1, may hold the place nowhere)
+            if (tid == 0) a.next_token[b] = max(k1 - 1, 0);
             __syncthreads();  // s_warp has been read
             if (lane == 31) s_warp[warp] = upto;
             __syncthreads();
             for (int k = 0; k < warp; ++k) upto += s_warp[k];
-            if (upto > want && upto - mine <= want) {  // one thread
+            if (upto > want && upto - mine <= want) {  // one thread, unless they overflowed
                 uint64_t run = upto - mine;
                 int v = l0;
                 for (; v < l1 - 1; ++v) {
@@ -304,8 +306,6 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
                     if (run > want) break;
                 }
                 a.next_token[b] = v;
-            } else if (tid == kVfThreads - 1 && upto <= want) {
-                a.next_token[b] = max(k1 - 1, 0);  // sums that overflowed: rows far from adding up to 1
             }
         }
     }

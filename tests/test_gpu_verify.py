@@ -135,6 +135,20 @@ def test_a_draft_probability_out_of_range_counts_as_clamped(q, p, want, sibling)
     assert int(n[0]) == want and int(d[0, -1]) == want - 1
 
 
+@pytest.mark.parametrize("V", [65, 5000, 131072])
+def test_rows_that_overflow_the_sums_still_give_a_token(V):
+    # every probability 1, or one in three: totals of 2^58 V wrap around
+    target = torch.ones(40, 2, V, device="cuda")
+    target[20:, :, 1::3] = 0.9
+    target[20:, :, 2::3] = 0.0
+    tok = torch.full((40, 1), V - 1, dtype=torch.int32, device="cuda")
+    u = torch.rand(40, 2, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    for lens in (None, torch.zeros(40, dtype=torch.int32, device="cuda")):
+        torch.full((40,), 1 << 30, dtype=torch.int32, device="cuda")  # (freed: the outputs' memory)
+        _, _, nxt = ops.verify_draft(target, None, tok, u, tree_lens=lens)
+        assert bool(((nxt >= -1) & (nxt < V)).all())
+
+
 def test_a_draw_next_to_a_border():
     # 2^18 equal tokens: u k / 2^18 lies on a border, the first token past it is drawn
     V = 1 << 18
