@@ -1417,7 +1417,14 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     }
                 }
                 fence_proxy_async_smem();
-                if (qmax > kF16Max) record_error(a.status, MLA_ERR_RANGE);
+                if (qmax > kF16Max) {
+                    bool counts = true;  // (a padded token's query may hold anything)
+                    if constexpr (kTree) {
+                        const int rq = entry_request(bq);
+                        counts = (entry_tile(bq) * kRowTile + h) / a.heads < tree_len(a.tree_lens, a.seq_lens, a.T, rq);
+                    }
+                    if (counts) record_error(a.status, MLA_ERR_RANGE);
+                }
                 qmax = 0.f;
             }
             tmem_wait_st();

@@ -172,6 +172,19 @@ def test_bad_values_reach_only_the_rows_that_attend_them(kv, context):
     assert bool(torch.isnan(out[0, 2]).all()) and bool(torch.isnan(lse[0, 2]).all())
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("contexts", [[100, 30], [20000, 30]])
+def test_queries_of_padded_tokens_may_hold_anything(kv, contexts):
+    d = make(2, 9, 16, contexts, lens=[3, 0], kv=kv, seed=15)  # two row tiles, the second all padding
+    want = both(d, torch.float32, "finite padding")
+    for q in (d["qn"], d["qr"]):
+        q[0, 3:] = float("nan")
+        q[0, 4::2] = float("inf")
+        q[1] = -1e30
+    out, lse, st, _ = run(d)
+    assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_device_errors_are_reported():
     d = make(2, 4, 16, [100, 200], seed=14)
     d["lens"][0] = 9                     # above T: clamped
