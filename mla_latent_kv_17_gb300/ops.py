@@ -457,11 +457,15 @@ def _at(t) -> int:
 
 
 def _new(like, shape, dtype, stream):
-    """An output on `like`'s device; memory that a stream other than the current one writes is
-    recorded on it."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
+    """An output on `like`'s device.  What a given stream writes is allocated on that stream (memory
+    of the current one may still be in use by work queued there) and recorded on the current one,
+    where it will be read."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    reader = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(reader)
     return t
 
 

@@ -209,6 +209,29 @@ def test_calls_on_a_given_stream():
     assert e.shape == (B * T, 576)
 
 
+def test_an_output_on_a_given_stream_takes_no_memory_still_in_use():
+    # a tensor freed while work queued on the current stream has yet to read it; a call on another
+    # stream, whose output has the same size, must not be given that memory
+    n = 1 << 14
+    x = torch.randn(n, 1, 576, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    freqs, _ = ops.rope_frequencies()
+    s = torch.cuda.Stream()
+    want = ops.rope(x, pos, freqs)
+    torch.cuda.synchronize()
+    # blocks of the outputs' two sizes, and no other free ones of those sizes
+    held = [torch.full_like(t, 3.0) for t in want for _ in range(8)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms of the current stream
+    copies = [t.clone() for t in held]
+    del held[:]
+    got = ops.rope(x, pos, freqs, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((c == 3.0).all()) for c in copies)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_prefix_read_back_feeds_the_prefill(kv):
     # a prompt written into pages, read back as entries, decompressed: bit for bit what the
