@@ -283,7 +283,8 @@ mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride
  *           positions[n]; a drafted token's place in its tree differs from its slot).
  * A bf16 cache receives y and the key rounded once to bf16.  An FP8 record receives, per 128
  * latent channels, scale = max|y| / 448 (1 for a zero block) and the e4m3 codes nearest to
- * y / scale (fp32 division, clamped to +-448), and the key in bf16, as mla_cache_append does.
+ * y / scale (fp32 division, clamped to +-448; with norm_weight a block whose products
+ * x * weight are all of 2^-142 or less counts as zero), and the key in bf16, as mla_cache_append does.
  * positions[n] < 0 skips token n.  A request outside [0, num_requests), a position beyond the
  * block table or a page id outside [0, num_pages) skips the token and records MLA_ERR_INDEX
  * in *device_status (optional).  cache and kv rows 16-byte aligned (kv_stride a multiple of

@@ -245,7 +245,10 @@ __global__ void __launch_bounds__(32 * kRwWarps, 4) write_kernel(RwArgs a, int p
                 }
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-                const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+                // (products with a weight may be so small that amax / 448 is 0 in fp32: a zero block)
+                float s = __fdiv_rn(amax, 448.f);
+                const bool zero = !(s > 0.f);
+                if (zero) s = 1.f;
                 // Blocks of very small or large values are moved by a power of two first, which leaves
                 // the quotients as they are and the remainders exact.  (What underflows on the way down
                 // lies below 2^-40 of the scale: code 0.)
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 4) write_kernel(RwArgs a, int p
                 }
                 reinterpret_cast<uint4 *>(dst)[lane] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
                 if ((lane & 7) == 0)
-                    reinterpret_cast<float *>(dst + kDLatent)[lane >> 3] = amax > 0.f && kNorm ? s * r : s;
+                    reinterpret_cast<float *>(dst + kDLatent)[lane >> 3] = kNorm && !zero ? s * r : s;
             }
         }
     }

@@ -168,6 +168,28 @@ def test_long_cache_offsets_and_empty_calls():
     assert ops.cache_read(cache, bt, none, none).shape == (0, 576)
 
 
+def test_norm_weights_that_underflow_leave_zero_blocks():
+    # x * weight near fp32's smallest values: max / 448 rounds to 0, which is no scale to divide by
+    bt, pages, req, pos, kv = _case(6, 2, 30)
+    kv = kv.contiguous()
+    kv[:, :512] = (kv[:, :512].double() * 1e-20).to(torch.bfloat16)
+    w = torch.full((512,), 1e-24, dtype=torch.bfloat16)
+    w[128:256] = 0.0
+    w[256:384] = 1e-16
+    w[384:] = 1.0
+    cache = _pool(True, pages, 3).cuda()
+    ops.cache_write(cache, bt.cuda(), req.cuda(), pos.cuda(), kv.cuda(), norm_weight=w.cuda(), norm_eps=1e-6)
+    got = ops.cache_read(cache, bt.cuda(), req.cuda(), pos.cuda())[:, :512].double().cpu()
+    x = kv[:, :512].double()
+    y = x / (x.pow(2).mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
+    assert bool((got[:, :256] == 0).all())
+    # the others are ordinary blocks: half a step of e4m3 (2^-4, or 2^-10 of the scale), then bf16 (2^-8)
+    s = y.view(-1, 4, 128).abs().amax(2).repeat_interleave(128, 1) / 448
+    tol = (2.0 ** -4 + 2.0 ** -7) * y.abs() + 2.0 ** -9 * s
+    assert bool(((got - y).abs()[:, 256:] <= tol[:, 256:]).all())
+    assert bool(torch.isfinite(got).all())
+
+
 def test_records_of_extreme_values_equal_the_oracle():
     # blocks from the smallest bf16 values to the largest: scales below and above the range in
     # which the quotient's Newton step is exact, subnormal ones among them
