@@ -211,6 +211,8 @@ extern "C" mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_
     if (!isfinite(mscale)) return MLA_ERR_INVALID_ARG;
     if (d_pass > 8192 || d_rot > 2048) return MLA_ERR_UNSUPPORTED;  // one token's cosines fit the CTA's table
     if (N == 0) return MLA_OK;
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out_rot) | reinterpret_cast<uintptr_t>(out_pass)) % 2)
+        return MLA_ERR_INVALID_ARG;  // no bf16 values
     if (!x || !positions || !freqs || !out_rot) return MLA_ERR_INVALID_ARG;
     RopeArgs a;
     a.x = (const uint16_t *)x;

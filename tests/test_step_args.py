@@ -28,7 +28,8 @@ def _rope(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(x=0), dict(pos=0), dict(freqs=0), dict(orr=0), dict(N=-1), dict(H=0), dict(dp=-8),
-                                dict(dr=0), dict(dr=63), dict(layout=2), dict(m=math.nan), dict(m=math.inf)])
+                                dict(dr=0), dict(dr=63), dict(layout=2), dict(m=math.nan), dict(m=math.inf),
+                                dict(x=A + 1), dict(op=A + 1), dict(orr=A + 3)])
 def test_rope_refuses(kw):
     assert _rope(**kw) == INVALID
 
