@@ -62,7 +62,7 @@ constexpr uint32_t kPBytes = 2 * kPPage + 2 * kRlBytes;
 constexpr uint32_t kMsgBytes = kPPage + kRlBytes;
 constexpr int kThreads = 256;         // dense tiles
 constexpr int kThreadsSparse = 384;   // sparse tiles: loader warps in pairs (see the loaders)
-constexpr int kThreadsFp8 = 384;      // FP8 records: + raw-load and expansion warps
+constexpr int kThreadsFp8 = 512;      // FP8 records: + raw-load and expansion warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr uint32_t kColQRope = kColQ + 128, kColQOther = kColQ + 160;
@@ -105,6 +105,8 @@ enum {
 };
 static_assert(B_COUNT <= 32, "barrier area");
 
+// kCopy: warps of different register budgets (see the FP8 records' roles) call functions of their own.
+template <int kCopy>
 struct Ctx {
     uint32_t base;
     int *status;
@@ -117,7 +119,8 @@ __device__ __forceinline__ uint32_t bar(uint32_t base, int i) { return base + kO
 // Bounded wait by the calling thread.  False on timeout (recorded) or when another role
 // has already given up.  The first test is inline; the polling loop is out of line, which
 // keeps every role's code small in the instruction cache.
-__device__ __noinline__ bool wait_bar_slow(const Ctx c, uint32_t b, uint32_t parity, bool cluster_scope) {
+template <int kCopy>
+__device__ __noinline__ bool wait_bar_slow(const Ctx<kCopy> c, uint32_t b, uint32_t parity, bool cluster_scope) {
     const long long t0 = (long long)clock64_now();
     for (uint32_t i = 0;; ++i) {
         const bool ok = cluster_scope ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity);
@@ -133,13 +136,15 @@ __device__ __noinline__ bool wait_bar_slow(const Ctx c, uint32_t b, uint32_t par
     }
 }
 
-__device__ __forceinline__ bool wait_bar(const Ctx &c, uint32_t b, uint32_t parity, bool cluster_scope) {
+template <int kCopy>
+__device__ __forceinline__ bool wait_bar(const Ctx<kCopy> &c, uint32_t b, uint32_t parity, bool cluster_scope) {
     const bool ok = cluster_scope ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity);
     return ok || wait_bar_slow(c, b, parity, cluster_scope);
 }
 
 // All lanes of a warp wait; the outcome is made warp-uniform.
-__device__ __forceinline__ bool warp_wait(const Ctx &c, uint32_t b, uint32_t parity,
+template <int kCopy>
+__device__ __forceinline__ bool warp_wait(const Ctx<kCopy> &c, uint32_t b, uint32_t parity,
                                           bool cluster_scope) {
     const bool ok = wait_bar(c, b, parity, cluster_scope);
     return __all_sync(0xffffffffu, ok);
@@ -697,25 +702,25 @@ __device__ __noinline__ void expand_chunk_ool(uint4 v, float s, uint8_t *box, in
 }
 
 // FP8 records: what the expansion warps do, in order: oth(0), own(0), own(1), oth(1), peer(0), then
-// oth(g + 2), peer(g + 1), own(g + 2) for g = 0, 1, ... (tiles past the last are left out).  Kind 0
+// oth(g + 2), own(g + 2), peer(g + 1) for g = 0, 1, ... (tiles past the last are left out).  Kind 0
 // own page, 1 peer page, 2 other columns.  Every job comes after the jobs whose consumers free its
-// buffer: peer(g + 1) and own(g + 2) take the slots PV(g) frees, oth(g + 2) the stage QK(g + 1)
-// frees; and peer(g + 1), which PV(g + 1) waits for, goes before own(g + 2), which only QK(g + 2)
-// needs.  oth(g + 2), whose codes are there by then, fills the time the codes of the other two take
-// to land after PV(g): with oth(g + 1) in its place a step of the FP8-ragged workload took 368 us
-// instead of 338.
+// buffer: own(g + 2) and peer(g + 1) take the slots PV(g) frees, oth(g + 2) the stage QK(g + 1)
+// frees.  own(g + 2) goes before peer(g + 1): QK(g + 2), the softmax and PV(g + 2) hang on it, while
+// PV(g + 1) has its softmax to wait for.  oth(g + 2), whose codes are there by then, fills the
+// time the codes of the other two take to land after PV(g): with oth(g + 1) in its place a step of
+// the FP8-ragged workload took 368 us instead of 338.
 struct Fp8Job {
     int kind, tile;
 };
 __device__ __forceinline__ Fp8Job fp8_job(int n) {
     if (n < 5) return Fp8Job{n == 0 || n == 3 ? 2 : n == 4 ? 1 : 0, n == 2 || n == 3 ? 1 : 0};
     const int g = (n - 5) / 3, k = (n - 5) % 3;
-    return Fp8Job{k == 0 ? 2 : k == 1 ? 1 : 0, k == 1 ? g + 1 : g + 2};
+    return Fp8Job{k == 0 ? 2 : k == 1 ? 0 : 1, k == 2 ? g + 1 : g + 2};
 }
 __device__ __forceinline__ int fp8_job_count(int ntiles) { return ntiles > 0 ? 5 + 3 * (ntiles - 1) : 0; }
 
-// The loads of the latent-half ring for them (kWhich 0: own(0), own(1), peer(0), then peer(g + 1),
-// own(g + 2)) and of the other-columns stage (kWhich 1: oth(g)), with the places they come from.
+// The loads of the latent-half ring for them (kWhich 0: own(0), own(1), peer(0), then own(g + 2),
+// peer(g + 1)) and of the other-columns stage (kWhich 1: oth(g)), with the places they come from.
 // The jobs of a step touch two neighbouring tiles, kept in registers as they slide along.
 template <int kWhich>
 struct Fp8Loads {
@@ -768,8 +773,8 @@ struct Fp8Loads {
                     ++g;
                 }
                 if (none(lo)) return false;
-                kind = 1 - r;
-                upper = r == 1;
+                kind = r;
+                upper = r == 0;
             }
             at = upper ? hi : lo;
             tile = g + (upper ? 1u : 0u);
@@ -797,7 +802,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     const __grid_constant__ CUtensorMap tmap_qr, DecodeArgs a) {
     constexpr bool kSparse = kMode == 1, kFp8 = kMode == 2;
     // arrivals that complete a latent / other-columns stage
-    constexpr uint32_t kFullCount = kFp8 ? 4u : kSparse ? 2u : 1u;
+    constexpr uint32_t kFullCount = kFp8 ? 8u : kSparse ? 2u : 1u;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -807,7 +812,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(gbase + kOffMisc);
     // misc[0]: TMEM base address, misc[1]: abort flag, misc[2..5]: FP8 records, valid rows of the
     // page in raw stage 0..3
-    Ctx c{base, a.status, misc + 1, a.wait_cycles};
+    const Ctx<0> c{base, a.status, misc + 1, a.wait_cycles};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kDhSlots; ++s) {
@@ -865,16 +870,22 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
     const int units = hd->num_units;
     const int cl = (int)cluster_id_x(), ncl = (int)nclusters_x();
 
-    if (kFp8 && (warp == 4 || warp == 10 || warp == 7 || warp == 9)) {
-        // ------------------------------------------------------------ FP8 expansion (4 warps)
-        // Warps 4, 10, 7 and 9 (one per SM sub-partition) expand every job, in the order the
-        // jobs are consumed.  Thread (r, p) expands part p (codes 128 p .. 128 p + 127) of row
-        // r.  The codes of part p of row r arrive as one 128-B row of box 2p of the bf16
-        // destination, the box that receives the first half of that part's output; the second
-        // half goes to box 2p + 1 first, then the first half lands on the codes it came from,
-        // read into registers beforehand.  No thread writes another thread's codes.
-        const int eidx = warp == 4 ? 0 : warp == 10 ? 1 : warp == 7 ? 2 : 3;
-        const int r = 32 * (eidx & 1) + lane, p = eidx >> 1;
+    if constexpr (kFp8) {
+        // 512 threads start with 128 registers each; the softmax warps, which keep a row of scores in
+        // theirs, take what the others leave (4 x 32 x 208 + 12 x 32 x 96 of them in all)
+        if (warp >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    }
+    if (kFp8 && (warp == 4 || warp == 7 || warp == 9 || warp == 10 || warp >= 12)) {
+        // ------------------------------------------------------------ FP8 expansion (8 warps)
+        // Warps 4, 7, 9, 10 and 12-15 (two per SM sub-partition) expand every job, in the order the
+        // jobs are consumed: a warp takes part p (codes 128 p .. 128 p + 127) of 16 rows, a lane
+        // every other 16-code chunk of a row.  The codes of part p of row r arrive as one 128-B row
+        // of box 2p of the bf16 destination, the box that receives the first half of that part's
+        // output (the second half goes to box 2p + 1): a row's two lanes read all their codes before
+        // either writes.  (With four warps, the peer page first and a page found between two loads:
+        // 225 us instead of 220 for 32 requests x 4 tokens x 128 heads.)
+        const int xw = warp >= 12 ? warp - 8 : warp == 4 ? 0 : warp == 7 ? 1 : warp == 9 ? 2 : 3;
+        const int r = 16 * (xw & 3) + (lane & 15), p = xw >> 2;
         // The order is fp8_job's; what a page holds (its valid rows, 0: not loaded) the raw loader
         // leaves beside its stage, so these warps walk no work items and read no block table: they
         // set the pace of this mode, and that walk cost some 700 cycles between two jobs.
@@ -921,36 +932,29 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 uint8_t *row = gbase + region + r * 128;                 // row r of box 0
                 const uint8_t *codes = row + 2 * p * kBox;               // its 8 chunks of 16 codes
                 uint8_t *first = row + 2 * p * kBox, *second = first + kBox;
+                uint4 v[4];  // chunks (r + 2 i + lane / 16) % 8: no bank conflicts, here or on the stores
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = *reinterpret_cast<const uint4 *>(codes + ((r + 2 * i + (lane >> 4)) & 7) * 16);
+                __syncwarp();
+                bool packed = false;
+                ScaleParts sp{};
                 if constexpr (kTree) {
-                    // all eight chunks are read before either box is written
-                    uint4 v[8];
+                    packed = __all_sync(0xffffffffu, scale_splits(sc));
+                    sp = split_scale(sc);
+                }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4 *>(codes + ((i + r) & 7) * 16);
-                    const bool packed = __all_sync(0xffffffffu, scale_splits(sc));
-                    const ScaleParts sp = split_scale(sc);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int q = (i + r) & 7;
-                        uint8_t *box = q < 4 ? first : second;
+                for (int i = 0; i < 4; ++i) {
+                    const int q = (r + 2 * i + (lane >> 4)) & 7;
+                    uint8_t *box = q < 4 ? first : second;
+                    if constexpr (kTree) {
                         if (packed)
                             expand_chunk_packed(v[i], sp, box, q & 3, r);
                         else
                             expand_chunk_ool(v[i], sc, box, q & 3, r);
+                    } else {
+                        expand_chunk(v[i], sc, box, q & 3, r);
                     }
-                } else {
-                    uint4 v[4];  // chunks (i + r) % 4, read before their box is overwritten
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(codes + ((i + r) & 3) * 16);
-                    // chunks 4 + (i + r) % 4 -> second box (rotated: no bank conflicts on the stores)
-                    uint4 nxt = *reinterpret_cast<const uint4 *>(codes + (4 + (r & 3)) * 16);
-#pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 cur = nxt;
-                        if (i < 3) nxt = *reinterpret_cast<const uint4 *>(codes + (4 + ((i + 1 + r) & 3)) * 16);
-                        expand_chunk(cur, sc, second, (i + r) & 3, r);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) expand_chunk(v[i], sc, first, (i + r) & 3, r);
                 }
                 fence_proxy_async_smem();
             }
@@ -985,10 +989,30 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     }
                 }
             } else {
+                // PV(g) frees the slots of both jobs of a round: their pages are found before the
+                // first one's wait (between the two loads that took 1,000 cycles).  One place finds
+                // a page and one loads it: the roles share the instruction cache, and with two more
+                // copies of this code the softmax warps took 1,600 cycles for what takes 1,080.
                 Fp8Loads<0> jobs(start);
-                while (ok && jobs.next()) {
-                    const PageRef pg = page_of<kTree>(a, jobs.at.w, jobs.at.t, jobs.kind == 0 ? (int)rank : (int)peer);
-                    const DhSlot d = dh_slot<kSparse>(jobs.tile, jobs.kind);
+                PageRef pg = {0, -1}, pg2 = {0, -1};
+                DhSlot d = {0, 0, 0, 0}, d2 = d;
+                int have = 0, want = 1;  // own(0) by itself, then own(1) and peer(0), then the rounds
+                bool more = true;
+#pragma unroll 1
+                while (ok) {
+                    if (have < want && more) {
+                        more = jobs.next();
+                        if (!more) continue;
+                        pg2 = page_of<kTree>(a, jobs.at.w, jobs.at.t, jobs.kind == 0 ? (int)rank : (int)peer);
+                        d2 = dh_slot<kSparse>(jobs.tile, jobs.kind);
+                        if (have++ == 0) {
+                            pg = pg2;
+                            d = d2;
+                        }
+                        continue;
+                    }
+                    if (have == 0) break;
+                    want = 0;
                     ok = d.fill == 0 || wait_bar(c, bar(base, B_DH_EMPTY + d.slot), (d.fill - 1u) & 1u, false);
                     if (!ok) break;
                     const uint32_t rb = bar(base, B_RAW + d.slot), dst = base + kOffDh + d.slot * kDhBytes;
@@ -1003,6 +1027,9 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         if (pg.rows > 0) record_error(a.status, MLA_ERR_INDEX);
                         mbar_arrive(rb);
                     }
+                    pg = pg2;
+                    d = d2;
+                    if (--have == 0) want = 2;
                 }
             }
             if (!ok) drain_pause();
@@ -1333,6 +1360,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
             if (!ok) drain_pause();
         }
     } else if (warp < 4) {
+        if constexpr (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const Ctx<kFp8 ? 1 : 0> c{base, a.status, misc + 1, a.wait_cycles};
         // ------------------------------------------------------------ softmax + epilogue
         // Per tile: part A (scores -> own weights -> message to the peer), then part B
         // (merge with the peer's message -> PV may start).
