@@ -108,10 +108,10 @@ plan_kernel(const Src src, int B, int H, int units, int ovh, unsigned char *ws, 
 
     // budget positions: the running position stays in a register (req_start is only written)
     int64_t local = 0;
-    for (int b = b0; b < b1; ++b) local += req_cost(req_tiles(src, b), ovh);
+    for (int b = b0; b < b1; ++b) local += req_cost(src, req_tiles(src, b), ovh);
     int64_t total;
     const int64_t pos0 = block_exclusive_scan(local, &total, sh);
-    const int64_t per = plan_budget(total, units, src.topk > 0 ? req_cost(req_tiles(src, 0), ovh) : 0, B, ovh);
+    const int64_t per = plan_budget(total, units, src.topk > 0 ? req_cost(src, req_tiles(src, 0), ovh) : 0, B, ovh);
 
     // With at most one request per thread, its cut stays in a register and every thread then
     // emits one work item at a time (a request cut into many pieces is not left to one thread);
@@ -133,7 +133,7 @@ plan_kernel(const Src src, int B, int H, int units, int ovh, unsigned char *ws, 
                 s_local += r.n;
                 ++r_local;
             }
-            pos += req_cost(tiles, ovh);
+            pos += req_cost(src, tiles, ovh);
         }
     }
     Sum3 tot;
@@ -163,7 +163,7 @@ plan_kernel(const Src src, int B, int H, int units, int ovh, unsigned char *ws, 
                 slot += r.n;
                 split_list[rpos++] = b;
             }
-            pos += req_cost(tiles, ovh);
+            pos += req_cost(src, tiles, ovh);
         }
     }
     if (one_each) {
@@ -542,7 +542,7 @@ mla_status mla_decode_tree_plan(const int32_t *seq_lens, const int32_t *tree_len
     const int units = units_for(num_sms), entries = B * row_tiles(T, H);
     if (ws_bytes < ws_layout(entries, kRowTile, units, true).total) return MLA_ERR_WORKSPACE;
     return launch_plan(TreeSource{seq_lens, tree_lens, B, T, H}, entries, kRowTile, units,
-                       piece_overhead(kv_dtype == MLA_KV_FP8_E4M3), workspace, stream);
+                       tree_piece_overhead(kv_dtype == MLA_KV_FP8_E4M3, T), workspace, stream);
 }
 
 mla_status mla_decode_tree_plan_host(const int32_t *seq_lens, const int32_t *tree_lens, int B, int T, int H,
@@ -554,7 +554,7 @@ mla_status mla_decode_tree_plan_host(const int32_t *seq_lens, const int32_t *tre
     const WsLayout L = ws_layout(entries, kRowTile, units, true);
     if (ws_bytes < L.plan_end) return MLA_ERR_WORKSPACE;
     build_plan_serial(TreeSource{seq_lens, tree_lens, B, T, H}, entries, kRowTile, units,
-                      piece_overhead(kv_dtype == MLA_KV_FP8_E4M3), (unsigned char *)workspace_host);
+                      tree_piece_overhead(kv_dtype == MLA_KV_FP8_E4M3, T), (unsigned char *)workspace_host);
     *reinterpret_cast<int *>((unsigned char *)workspace_host + L.status) = 0;
     return MLA_OK;
 }

@@ -1498,17 +1498,17 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     lrow = part_lse + (int64_t)w.slot * a.H + h;
                 }
                 if (kTree && w.t1 <= w.t0) {
-                    if (h < rows) {
-                        const int64_t at = (row0 + h) * kDLatent + rank * 256;
-                        for (int q = 0; q < 64; ++q) {
-                            if (a.out16) {
-                                if (q < 32) reinterpret_cast<uint4 *>(a.out16 + at)[q] = make_uint4(0u, 0u, 0u, 0u);
-                            } else {
-                                reinterpret_cast<float4 *>(a.out + at)[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            }
+                    // zeros: a row of this CTA's columns is one or two warp stores
+                    for (int row = warp * 32; row < min(rows, warp * 32 + 32); ++row) {
+                        const int64_t at = (row0 + row) * kDLatent + rank * 256;
+                        if (a.out16) {
+                            reinterpret_cast<uint4 *>(a.out16 + at)[lane] = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            reinterpret_cast<uint4 *>(a.out + at)[lane] = make_uint4(0u, 0u, 0u, 0u);
+                            reinterpret_cast<uint4 *>(a.out + at)[32 + lane] = make_uint4(0u, 0u, 0u, 0u);
                         }
-                        if (rank == 0 && lrow) *lrow = -INFINITY;
                     }
+                    if (h < rows && rank == 0 && lrow) *lrow = -INFINITY;
                     continue;
                 }
                 if (w.t1 <= w.t0) {

@@ -153,7 +153,18 @@ MLA_HD int32_t req_tiles(const S &s, int b) {
 // layouts; planned at 2 the bf16 cache runs fastest, and FP8 records (whose softmax warps
 // also convert each item's query) at 3.
 MLA_HD int piece_overhead(int fp8_records) { return fp8_records ? 3 : 2; }
-MLA_HD int64_t req_cost(int32_t tiles, int ovh) { return tiles > 0 ? tiles + ovh : 0; }
+// A tree's items are shorter and more (every row tile of a request): one tile more each (16 requests
+// x 8 tokens x 128 heads 134.5 us instead of 136.9, FP8 records 32 x 4 x 128 193.5 instead of 195.2;
+// two more: 135.4 and 195.9).  One token is planned as the plain decode plans it, and so gives its
+// very bits.
+MLA_HD int tree_piece_overhead(int fp8_records, int T) { return piece_overhead(fp8_records) + (T > 1 ? 1 : 0); }
+// An entry without tiles costs nothing, but for a tree's row tiles past the drafted tokens: many of
+// them follow one another, and the zeros they write (64 KB per SM) would all fall to one unit (24 us
+// at the end of 16 requests x 8 tokens x 128 heads).
+MLA_HD int empty_cost(const ReqSource &) { return 0; }
+MLA_HD int empty_cost(const TreeSource &s) { return s.T > 1 ? 1 : 0; }
+template <typename S>
+MLA_HD int64_t req_cost(const S &s, int32_t tiles, int ovh) { return tiles > 0 ? tiles + ovh : empty_cost(s); }
 
 // The budget axis: request b occupies cost positions [S_b, S_b + cost_b); its overhead
 // comes first, so tile t sits at S_b + overhead + t.  Unit u owns positions
@@ -326,9 +337,9 @@ inline void build_plan_serial(const Src &src, int B, int H, int units, int ovh, 
     int64_t S = 0;
     for (int b = 0; b < B; ++b) {
         req_start[b] = S;
-        S += req_cost(req_tiles(src, b), ovh);
+        S += req_cost(src, req_tiles(src, b), ovh);
     }
-    const int64_t per = plan_budget(S, units, src.topk > 0 ? req_cost(req_tiles(src, 0), ovh) : 0, B, ovh);
+    const int64_t per = plan_budget(S, units, src.topk > 0 ? req_cost(src, req_tiles(src, 0), ovh) : 0, B, ovh);
     int32_t off = 0, slots = 0, nsr = 0;
     for (int b = 0; b < B; ++b) {
         const ReqSplit r = req_split(req_start[b], req_tiles(src, b), per, units, ovh);
