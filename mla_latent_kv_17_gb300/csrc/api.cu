@@ -216,15 +216,21 @@ template <bool kTree>
 __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm)
 combine_kernel(DecodeArgs a) {
     __shared__ int32_t s_b[kCombineSmemReqs], s_n[kCombineSmemReqs], s_s0[kCombineSmemReqs];
-    grid_dep_wait();
-    grid_dep_launch();  // the next kernel on the stream may launch (it waits for this one)
-    if (!plan_matches(a)) return;
+    // The plan is complete: every decode CTA waited for it before it let this kernel start.  Reading it
+    // ahead of the wait for the decode itself takes its chain of loads off the end.
+    if (!plan_matches(a)) {
+        grid_dep_wait();
+        return;
+    }
     const unsigned char *ws = a.ws;
     const int H = a.H;
     const PlanHeader *hd = reinterpret_cast<const PlanHeader *>(ws);
     const WsLayout L = ws_layout(hd->B, hd->H, hd->num_units, kTree);
     const int nsr = hd->num_split_reqs;
-    if (nsr <= 0) return;
+    if (nsr <= 0) {
+        grid_dep_wait();
+        return;
+    }
     const int32_t *split_list = reinterpret_cast<const int32_t *>(ws + L.split_list);
     const int32_t *num_splits = reinterpret_cast<const int32_t *>(ws + L.num_splits);
     const int32_t *split_base = reinterpret_cast<const int32_t *>(ws + L.split_base);
@@ -235,6 +241,8 @@ combine_kernel(DecodeArgs a) {
         s_s0[k] = split_base[b];
     }
     __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();  // the next kernel on the stream may launch (it waits for this one)
     const float *part_lse = reinterpret_cast<const float *>(ws + L.part_lse);
     const float4 *part_o = reinterpret_cast<const float4 *>(ws + L.part_o);
     const int64_t ostep = (int64_t)H * (kDLatent / 4);  // one piece to the next, in float4
@@ -242,7 +250,7 @@ combine_kernel(DecodeArgs a) {
     const int64_t nw = (int64_t)gridDim.x * (kCombineThreads / 32);
     const int64_t ntasks = (int64_t)nsr * H;
     for (int64_t t = (int64_t)blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5); t < ntasks; t += nw) {
-        const int k = (int)(t / H), h = (int)(t % H);
+        const int k = (int)((uint32_t)t / (uint32_t)H), h = (int)((uint32_t)t - (uint32_t)k * (uint32_t)H);  // (few cut requests)
         int b, n, s0;
         if (k < kCombineSmemReqs) {
             b = s_b[k];
