@@ -708,7 +708,7 @@ __device__ __noinline__ void expand_chunk_ool(uint4 v, float s, uint8_t *box, in
 // frees.  own(g + 2) goes before peer(g + 1): QK(g + 2), the softmax and PV(g + 2) hang on it, while
 // PV(g + 1) has its softmax to wait for.  oth(g + 2), whose codes are there by then, fills the
 // time the codes of the other two take to land after PV(g): with oth(g + 1) in its place a step of
-// the FP8-ragged workload took 368 us instead of 338.
+// the FP8-ragged workload took 9 % more.
 struct Fp8Job {
     int kind, tile;
 };
@@ -794,7 +794,12 @@ struct Fp8Loads {
 // FP8 RoPE (bf16, 128-B swizzle); tmap_qn / tmap_qr:
 // the queries (64 columns x 128 heads of one request, 128-B swizzle).
 // kTree: the rows are 128 of a request's T x heads query rows instead of its heads, each with its
-// own mask over the drafted tokens (modes 0 and 2).
+// own mask over the drafted tokens (modes 0 and 2).  A 128-token tile takes ~1.95 us (FP8 records:
+// ~2.95): the tensor pipe runs 8 PV operations of 128 x 256 (~1,000 cycles) and 36 QK^T operations
+// of 128 x 64 (~80 each, N = 64 being a page) in 3,750, and shared memory moves 369 KB (2,900 cycles
+// of its bandwidth).  With all heads on one GPU (16 requests x 8 tokens x 128 heads, 1,024-8,192 tokens)
+// that bounds the call: 132 us against 66 for its products; one 128-row tile per request (64 x 8 x
+// 16, the same lengths) reads the cache once and takes 99 us against 53.
 template <int kMode, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMode == 2 ? kThreadsFp8 : kMode == 1 ? kThreadsSparse : kThreads, 1)
 decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tmap_sc,
@@ -882,8 +887,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         // every other 16-code chunk of a row.  The codes of part p of row r arrive as one 128-B row
         // of box 2p of the bf16 destination, the box that receives the first half of that part's
         // output (the second half goes to box 2p + 1): a row's two lanes read all their codes before
-        // either writes.  (With four warps, the peer page first and a page found between two loads:
-        // 225 us instead of 220 for 32 requests x 4 tokens x 128 heads.)
+        // either writes.  (With four warps, the peer page first and a page found between two loads
+        // 32 requests x 4 tokens x 128 heads took 2 % more.)
         const int xw = warp >= 12 ? warp - 8 : warp == 4 ? 0 : warp == 7 ? 1 : warp == 9 ? 2 : 3;
         const int r = 16 * (xw & 3) + (lane & 15), p = xw >> 2;
         // The order is fp8_job's; what a page holds (its valid rows, 0: not loaded) the raw loader

@@ -4,7 +4,9 @@
 // What the walk needs of a token that is accepted is two probabilities; only where it stops
 // are whole rows read: the target's row and the rows of the drafts rejected there.  One
 // cluster of eight CTAs takes a request, each CTA an eighth of the vocabulary, so that a
-// single request still streams its rows through eight SMs; memory bounds a large batch.
+// single request still streams its rows through eight SMs; memory bounds a large batch (64
+// requests x 131,072 tokens, one rejection each: 67 MB, 22 us - four CTAs per SM at most have
+// their rows in flight, and the walk, the cluster's sum and the draw stand before and after).
 //
 // All sums are 64-bit integers: a probability is cut to a multiple of 2^-58, which keeps every
 // bit of a value of 2^-34 or more, the residual of a first rejection is an exact subtraction,
