@@ -795,11 +795,12 @@ struct Fp8Loads {
 // the queries (64 columns x 128 heads of one request, 128-B swizzle).
 // kTree: the rows are 128 of a request's T x heads query rows instead of its heads, each with its
 // own mask over the drafted tokens (modes 0 and 2).  A 128-token tile takes ~1.95 us (FP8 records:
-// ~2.95): the tensor pipe runs 8 PV operations of 128 x 256 (~1,000 cycles) and 36 QK^T operations
-// of 128 x 64 (~80 each, N = 64 being a page) in 3,750, and shared memory moves 369 KB (2,900 cycles
-// of its bandwidth).  With all heads on one GPU (16 requests x 8 tokens x 128 heads, 1,024-8,192 tokens)
-// that bounds the call: 132 us against 66 for its products; one 128-row tile per request (64 x 8 x
-// 16, the same lengths) reads the cache once and takes 99 us against 53.
+// ~2.95).  By clock traces its 3,750 cycles are 8 PV operations of 128 x 256 (~1,000) and 36 QK^T
+// operations of 128 x 64 (~80 each, of which the arithmetic is 32), one after the other; shared
+// memory moves 369 KB meanwhile (2,900 cycles of its bandwidth).  With all heads on one GPU
+// (16 requests x 8 tokens x 128 heads, 1,024-8,192 tokens) that bounds the call: 132 us against 66
+// for its products; one 128-row tile per request (64 x 8 x 16, the same lengths) reads the cache
+// once and takes 99 us against 53.
 template <int kMode, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMode == 2 ? kThreadsFp8 : kMode == 1 ? kThreadsSparse : kThreads, 1)
 decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tmap_sc,
