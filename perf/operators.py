@@ -234,7 +234,8 @@ def _own(s):
     from mla_latent_kv_17_gb300 import ops
     case = s["case"]
     if case["op"] == "rope":
-        return ops.rope(s["x"], s["positions"], s["freqs"], layout=case["layout"], mscale=s["mscale"])
+        out = ops.rope(s["x"], s["positions"], s["freqs"], layout=case["layout"], mscale=s["mscale"])
+        return out if case["d_pass"] else (s["x"][..., :0], out[1])  # (nothing passes: no output for it)
     if case["op"] == "write":
         ops.cache_write(s["cache"], s["block_table"], s["requests"], s["positions"], s["kv"], freqs=s["freqs"],
                         layout=case["layout"], mscale=s["mscale"], norm_weight=s["weight"], norm_eps=EPS)
