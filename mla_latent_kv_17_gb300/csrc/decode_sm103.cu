@@ -788,7 +788,7 @@ struct Fp8Loads {
 // kMode 1: DSA sparse tiles (128 index slots gathered row by row, tile::gather4).
 // kMode 2: dense FP8 records: raw e4m3 codes and scales are loaded by two extra warps (one
 //          for the latent-half ring, one for the other-columns stage) and expanded to bf16
-//          operand tiles by four warps; RoPE goes in directly.
+//          operand tiles by eight warps; RoPE goes in directly.
 // tmap: the cache (kMode 2: its bytes, 128-B boxes of codes; kMode 1: one-row boxes);
 // tmap_sc: FP8 scales (16-B boxes) or, for kMode 1, the cache in 64-row boxes; tmap_rope:
 // FP8 RoPE (bf16, 128-B swizzle); tmap_qn / tmap_qr:

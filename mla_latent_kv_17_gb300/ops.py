@@ -36,6 +36,8 @@ class MlaError(RuntimeError):
 def lib():
     """The loaded libmla_decode (ctypes.CDLL); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -414,15 +416,15 @@ def status(ws: Workspace, stream=None) -> int:
 # (A small call is bound by this file: tensors are checked by their device's number, pointers
 # and the stream pass as plain integers.)
 
-def _device_of(first, **others):
+def _device_of(names, first, *others):
     """The number of the CUDA device that all given tensors (or None) live on; `first` decides."""
     dev = first.get_device()
-    for name, t in others.items():
+    for t in others:
         if t is not None and t.get_device() != dev:
             dev = -1
             break
     if dev < 0:
-        for name, t in others.items():
+        for name, t in zip(names.split(), (first, *others)):
             if t is not None and not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
         raise ValueError("arguments are on different devices")
@@ -443,7 +445,7 @@ _SAME = _Same()
 
 
 def _on(dev: int):
-    return _SAME if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _SAME if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _raw(stream, dev: int) -> int:
@@ -487,7 +489,7 @@ def _layout(layout) -> int:
 
 
 def _freqs(freqs, d_rot):
-    if freqs.dtype != torch.float64 or tuple(freqs.shape) != (d_rot // 2,) or not freqs.is_contiguous():
+    if freqs.dtype != torch.float64 or freqs.shape != (d_rot // 2,) or not freqs.is_contiguous():
         raise ValueError(f"freqs must be contiguous float64 [{d_rot // 2}]")
 
 
@@ -543,7 +545,7 @@ def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pas
     d_pass = D - d_rot
     if d_rot < 2 or d_pass < 0:
         raise ValueError(f"x has {D} values per head, freqs turns {d_rot}")
-    dev = _device_of(x, x=x, positions=positions, freqs=freqs, out_pass=out_pass, out_rot=out_rot)
+    dev = _device_of("x positions freqs out_pass out_rot", x, positions, freqs, out_pass, out_rot)
     _ints(positions, (N,), "positions")
     _freqs(freqs, d_rot)
     code = _layout(layout)
@@ -611,8 +613,8 @@ def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_po
     [P,64,576] or uint8 FP8 records [P,64,656] (quantised on the way in).  With norm_weight
     (bf16 [512]) the latent is RMS-normalised first; with freqs (float64 [32]) the key is rotated
     at rope_positions (None: positions).  device_status: optional int32 [1] for MLA_ERR_INDEX."""
-    dev = _device_of(cache, cache=cache, block_table=block_table, requests=requests, positions=positions, kv=kv,
-                     freqs=freqs, rope_positions=rope_positions, norm_weight=norm_weight, device_status=device_status)
+    dev = _device_of("cache block_table requests positions kv freqs rope_positions norm_weight device_status", cache,
+                     block_table, requests, positions, kv, freqs, rope_positions, norm_weight, device_status)
     kind = _cache_kind(cache)
     N = _tokens(block_table, requests, positions)
     stride = _entry_rows(kv, N, "kv")
@@ -641,8 +643,8 @@ def cache_read(cache, block_table, requests, positions, entries=None, device_sta
     """Reads many tokens' entries back: bf16 [N,576], row n = position positions[n] of request
     requests[n] (None: request n); FP8 records are dequantised.  Rows of skipped tokens (negative
     or unmapped positions) stay as they were in `entries` (undefined where it is allocated here)."""
-    dev = _device_of(cache, cache=cache, block_table=block_table, requests=requests, positions=positions,
-                     entries=entries, device_status=device_status)
+    dev = _device_of("cache block_table requests positions entries device_status", cache, block_table, requests, positions,
+                     entries, device_status)
     kind = _cache_kind(cache)
     N = _tokens(block_table, requests, positions)
     _status_word(device_status)
@@ -682,7 +684,7 @@ class TreeWorkspace:
 def plan_tree(ws: TreeWorkspace, seq_lens, tree_lens=None, num_sms: int = 0, stream=None, kv_dtype="bf16"):
     """Builds the plan of decode_tree for seq_lens and tree_lens (device int32 [B]; tree_lens
     None: T); kv_dtype ('bf16' or 'fp8') is the cache layout the attention will read."""
-    dev = _device_of(seq_lens, seq_lens=seq_lens, tree_lens=tree_lens, workspace=ws.buf)
+    dev = _device_of("seq_lens tree_lens workspace", seq_lens, tree_lens, ws.buf)
     _ints(seq_lens, (ws.B,), "seq_lens")
     if tree_lens is not None:
         _ints(tree_lens, (ws.B,), "tree_lens")
@@ -702,8 +704,8 @@ def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens,
     tree_lens[b] (None: T) of them its drafted tokens'; tree_mask int64 [B,T]: bit j of [b,i] set:
     token i attends drafted token j.  -> (out fp32 or bf16 [B,T,H,512], lse fp32 [B,T,H] or None)."""
     B, T, H = ws.B, ws.T, ws.H
-    dev = _device_of(q_nope, q_nope=q_nope, q_rope=q_rope, cache=cache, block_table=block_table, seq_lens=seq_lens,
-                     tree_lens=tree_lens, tree_mask=tree_mask, out=out, lse=lse, workspace=ws.buf)
+    dev = _device_of("q_nope q_rope cache block_table seq_lens tree_lens tree_mask out lse workspace", q_nope, q_rope,
+                     cache, block_table, seq_lens, tree_lens, tree_mask, out, lse, ws.buf)
     for t, d, name in ((q_nope, 512, "q_nope"), (q_rope, 64, "q_rope")):
         if t.dtype != torch.bfloat16 or t.shape != (B, T, H, d) or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous bf16 [{B},{T},{H},{d}]")
@@ -744,8 +746,8 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
     [0,1), parents int32 [B,T] (-1: the last committed token; None: a chain), tree_lens int32 [B]
     -> (num_accepted int32 [B], depths int32 [B,T]: place among the accepted tokens or -1,
     next_token int32 [B])."""
-    dev = _device_of(target_probs, target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
-                     uniforms=uniforms, parents=parents, tree_lens=tree_lens, device_status=device_status)
+    dev = _device_of("target_probs draft_probs draft_tokens uniforms parents tree_lens device_status", target_probs,
+                     draft_probs, draft_tokens, uniforms, parents, tree_lens, device_status)
     if draft_tokens.dim() != 2 or target_probs.dim() != 3:
         raise ValueError("draft_tokens must be int32 [B,T], target_probs fp32 [B,T+1,V]")
     B, T = draft_tokens.shape
