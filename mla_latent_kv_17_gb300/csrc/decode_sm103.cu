@@ -943,24 +943,21 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 for (int i = 0; i < 4; ++i)
                     v[i] = *reinterpret_cast<const uint4 *>(codes + ((r + 2 * i + (lane >> 4)) & 7) * 16);
                 __syncwarp();
-                bool packed = false;
-                ScaleParts sp{};
-                if constexpr (kTree) {
-                    packed = __all_sync(0xffffffffu, scale_splits(sc));
-                    sp = split_scale(sc);
-                }
+                auto each = [&](auto &&expand) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int q = (r + 2 * i + (lane >> 4)) & 7;
-                    uint8_t *box = q < 4 ? first : second;
-                    if constexpr (kTree) {
-                        if (packed)
-                            expand_chunk_packed(v[i], sp, box, q & 3, r);
-                        else
-                            expand_chunk_ool(v[i], sc, box, q & 3, r);
-                    } else {
-                        expand_chunk(v[i], sc, box, q & 3, r);
+                    for (int i = 0; i < 4; ++i) {
+                        const int q = (r + 2 * i + (lane >> 4)) & 7;
+                        expand(v[i], q < 4 ? first : second, q & 3);
                     }
+                };
+                if constexpr (kTree) {
+                    const ScaleParts sp = split_scale(sc);
+                    if (__all_sync(0xffffffffu, scale_splits(sc)))
+                        each([&](uint4 x, uint8_t *box, int q) { expand_chunk_packed(x, sp, box, q, r); });
+                    else
+                        each([&](uint4 x, uint8_t *box, int q) { expand_chunk_ool(x, sc, box, q, r); });
+                } else {
+                    each([&](uint4 x, uint8_t *box, int q) { expand_chunk(x, sc, box, q, r); });
                 }
                 fence_proxy_async_smem();
             }
