@@ -91,6 +91,43 @@ def test_tree_splits(kv):
     both(make(2, 40, 16, [5000, 77], kv=kv, seed=8), torch.bfloat16, f"split {kv}, five tiles", with_lse=False)
 
 
+@pytest.mark.parametrize("kv,out_dtype", [("bf16", torch.float32), ("bf16", torch.bfloat16), ("fp8", torch.bfloat16)])
+def test_many_empty_row_tiles(kv, out_dtype):
+    # eight row tiles per request, most of them past the drafted tokens: written as zeros, by all units
+    lens = [1, 0, 2, 16, 3, 0, 1, 1, 9, 2, 0, 4]
+    d = make(12, 16, 64, [150, 20, 0, 700, 64, 0, 3, 127, 40, 1, 300, 90], lens, kv, seed=16)
+    out, lse, _ = both(d, out_dtype, "empty tiles")
+    for b, n in enumerate(lens):
+        assert bool((out[b, n:] == 0).all()) and bool(torch.isneginf(lse[b, n:]).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_plans_and_calls_in_a_row_on_one_workspace(kv):
+    # the merge reads its plan while the attention before it still runs: plans of other lengths that
+    # follow one another without a pause must never mix
+    d = make(3, 4, 64, [9000, 20000, 400], kv=kv, seed=17)
+    other = d["seq"].clone()
+    other[1] = 700
+    ws = ops.TreeWorkspace(3, 4, 64)
+    lens = {False: d["seq"], True: other}
+    outs = [torch.zeros(3, 4, 64, 512, device="cuda") for _ in range(24)]
+
+    def step(k, out):
+        seq = lens[k % 3 == 1]
+        ops.plan_tree(ws, seq, d["lens"], kv_dtype=kv)
+        ops.decode_tree(ws, d["qn"], d["qr"], d["cache"], d["bt"], seq, d["lens"], d["mask"], tree_ref.SCALE, out=out)
+
+    want = [torch.zeros_like(outs[0]) for _ in range(2)]
+    for k in range(2):
+        step(k, want[k])
+        assert ops.status(ws) == 0
+    for k, out in enumerate(outs):
+        step(k, out)
+    assert ops.status(ws) == 0
+    for k, out in enumerate(outs):
+        assert torch.equal(out, want[k % 3 == 1]), k
+
+
 def test_peaked_scores():
     both(make(2, 4, 32, [500, 1300], seed=9, q_scale=8.0), torch.float32, "peaked")
 

@@ -50,6 +50,12 @@ def test_verify(B, T, V, tree, probs):
         assert 0 < int(n.sum()) < B * T
 
 
+@pytest.mark.parametrize("tree,probs", [(False, True), (True, True), (True, False)])
+def test_the_largest_vocabulary_and_tree(tree, probs):
+    target, draft, tok, u, parents = make(1, 64, 1 << 20, 29, tree, probs)
+    run(target, draft, tok, u, parents)
+
+
 def test_ragged_trees():
     target, draft, tok, u, parents = make(6, 7, 500, 4, True, True)
     lens = torch.tensor([0, 1, 7, 3, 2, 6], dtype=torch.int32, device="cuda")
