@@ -535,9 +535,9 @@ def rope_frequencies(d_rot: int = 64, base: float = 10000.0, scaling: str = "non
 def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pass=None, out_rot=None,
          copy_pass: bool = True, stream=None):
     """Rotary positions of the last 2 len(freqs) values of every head: x bf16 [N,H,D] (rows of any
-    stride, values adjacent), positions int32 [N], freqs float64 -> (x[..., :D-d] copied or None,
-    the rotated part), bf16 [N,H,D-d] and [N,H,d].  copy_pass=False leaves the first part out;
-    out_rot may be x[..., D-d:] itself (rotation in place)."""
+    stride, values adjacent), positions int32 [N], freqs float64 -> (x[..., :D-d] copied, the rotated
+    part), bf16 [N,H,D-d] and [N,H,d]; None for the first part where it is empty or copy_pass=False
+    leaves it out.  out_rot may be x[..., D-d:] itself (rotation in place)."""
     if x.dtype != torch.bfloat16 or x.dim() != 3:
         raise ValueError("x must be bf16 [N,H,D]")
     N, H, D = x.shape
@@ -550,18 +550,23 @@ def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pas
     _freqs(freqs, d_rot)
     code = _layout(layout)
     with _on(dev):
+        ps = rs = (H * d_rot, d_rot, 1)
         if not copy_pass or d_pass == 0:
             out_pass = None
         elif out_pass is None:
             out_pass = _new(x, (N, H, d_pass), torch.bfloat16, stream)
+            ps = (H * d_pass, d_pass, 1)
         elif out_pass.dtype != torch.bfloat16 or out_pass.shape != (N, H, d_pass):
             raise ValueError(f"out_pass must be bf16 [{N},{H},{d_pass}]")
+        else:
+            ps = out_pass.stride()
         if out_rot is None:
             out_rot = _new(x, (N, H, d_rot), torch.bfloat16, stream)
         elif out_rot.dtype != torch.bfloat16 or out_rot.shape != (N, H, d_rot):
             raise ValueError(f"out_rot must be bf16 [{N},{H},{d_rot}]")
-        xs, rs = x.stride(), out_rot.stride()
-        ps = rs if out_pass is None else out_pass.stride()
+        else:
+            rs = out_rot.stride()
+        xs = x.stride()
         if N == 0 or H == 0:
             return out_pass, out_rot
         if (xs[2] != 1 and D > 1) or rs[2] != 1 or (ps[2] != 1 and d_pass > 1):
@@ -575,9 +580,11 @@ def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pas
 
 
 def _cache_kind(cache) -> int:
-    if cache.dtype == torch.bfloat16 and cache.shape[1:] == (64, 576):
+    shape = cache.shape
+    width = shape[2] if len(shape) == 3 and shape[1] == 64 else 0
+    if width == 576 and cache.dtype == torch.bfloat16:
         kv = KV_BF16
-    elif cache.dtype == torch.uint8 and cache.shape[1:] == (64, 656):
+    elif width == 656 and cache.dtype == torch.uint8:
         kv = KV_FP8
     else:
         raise ValueError("cache must be bf16 [P,64,576] or uint8 [P,64,656]")
@@ -650,8 +657,9 @@ def cache_read(cache, block_table, requests, positions, entries=None, device_sta
     _status_word(device_status)
     with _on(dev):
         if entries is None:
-            entries = _new(cache, (N, 576), torch.bfloat16, stream)
-        stride = _entry_rows(entries, N, "entries")
+            entries, stride = _new(cache, (N, 576), torch.bfloat16, stream), 576
+        else:
+            stride = _entry_rows(entries, N, "entries")
         st = lib().mla_cache_read(
             cache.data_ptr(), kind, cache.shape[0], block_table.data_ptr(), block_table.shape[0],
             block_table.shape[1], _at(requests), positions.data_ptr(), N, entries.data_ptr(), stride,
@@ -719,19 +727,22 @@ def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens,
     if tree_mask.dtype != torch.int64 or tree_mask.shape != (B, T) or not tree_mask.is_contiguous():
         raise ValueError(f"tree_mask must be contiguous int64 [{B},{T}]")
     with _on(dev):
+        if out is not None:
+            out_dtype = out.dtype
+        if out_dtype not in (torch.float32, torch.bfloat16) or out is not None and (
+                out.shape != (B, T, H, 512) or not out.is_contiguous()):
+            raise ValueError(f"out must be contiguous fp32 or bf16 [{B},{T},{H},512]")
         if out is None:
             out = _new(q_nope, (B, T, H, 512), out_dtype, stream)
-        if out.dtype not in (torch.float32, torch.bfloat16) or out.shape != (B, T, H, 512) \
-                or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous fp32 or bf16 [{B},{T},{H},512]")
-        if lse is None and with_lse:
-            lse = _new(q_nope, (B, T, H), torch.float32, stream)
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous()):
+        if lse is None:
+            if with_lse:
+                lse = _new(q_nope, (B, T, H), torch.float32, stream)
+        elif (lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous()):
             raise ValueError(f"lse must be contiguous fp32 [{B},{T},{H}]")
         st = lib().mla_decode_tree(
             ws.buf.data_ptr(), ws.nbytes, q_nope.data_ptr(), q_rope.data_ptr(), cache.data_ptr(), kind,
             cache.shape[0], block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), _at(tree_lens),
-            tree_mask.data_ptr(), B, T, H, softmax_scale, out.data_ptr(), 1 if out.dtype == torch.bfloat16 else 0,
+            tree_mask.data_ptr(), B, T, H, softmax_scale, out.data_ptr(), 1 if out_dtype == torch.bfloat16 else 0,
             _at(lse), _raw(stream, dev))
     if st:
         _check("mla_decode_tree", st)
