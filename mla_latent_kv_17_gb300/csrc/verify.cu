@@ -280,34 +280,65 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
         if ((int)rank == owner) {
             int w = 0;
             while (w < kVfWarps - 1 && want >= s_warp[w]) want -= s_warp[w++];
-            // chunk w again, by the whole CTA: each thread a run of it; the thread whose run
-            // holds the place searches the run
+            // chunk w again, by the whole CTA, a piece of 8 values a thread at a time; the thread whose
+            // values hold the place finds it among them (reading them again, one after another, took
+            // 3 us of this call's end)
             const int k0 = min(v1, v0 + w * chunk), k1 = min(v1, k0 + chunk);
-            const int per = (k1 - k0 + kVfThreads - 1) / kVfThreads;
-            const int l0 = min(k1, k0 + tid * per), l1 = min(k1, l0 + per);
-            uint64_t mine = 0;
-#pragma unroll 8
-            for (int v = l0; v < l1; ++v) mine += r.at(v);
-            uint64_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
+            const float *q = r.q && r.n == 1 ? r.q + (int64_t)r.rej[0] * V : nullptr;
+            const bool plain = !r.q || r.n <= 1;
             // (sums that overflowed, of rows far from adding up to 1, may hold the place nowhere)
             if (tid == 0) a.next_token[b] = max(k1 - 1, 0);
-            __syncthreads();  // s_warp has been read
-            if (lane == 31) s_warp[warp] = upto;
-            __syncthreads();
-            for (int k = 0; k < warp; ++k) upto += s_warp[k];
-            if (upto > want && upto - mine <= want) {  // one thread, unless they overflowed
-                uint64_t run = upto - mine;
-                int v = l0;
-                for (; v < l1 - 1; ++v) {
-                    run += r.at(v);
-                    if (run > want) break;
+            for (int c = k0; c < k1; c += 8 * kVfThreads) {
+                const int v = c + 8 * tid;
+                uint64_t left[8];
+                if (plain) {
+                    float pv[8], qv[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        pv[k] = v + k < k1 ? r.p[v + k] : 0.f;
+                        qv[k] = q && v + k < k1 ? q[v + k] : 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) left[k] = left_of(pv[k], qv[k]);
+                    for (int j = 0; j < r.n && !r.q; ++j) {  // certain drafts: their tokens are lost
+                        const int d = r.tokens[r.rej[j]] - v;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (d == k) left[k] = 0;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) left[k] = v + k < k1 ? r.at(v + k) : 0;
                 }
-                a.next_token[b] = v;
+                uint64_t mine = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mine += left[k];
+                uint64_t upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                __syncthreads();  // s_warp has been read
+                if (lane == 31) s_warp[warp] = upto;
+                __syncthreads();
+                uint64_t piece = 0;
+                for (int k = 0; k < kVfWarps; ++k) {
+                    if (k == warp) upto += piece;
+                    piece += s_warp[k];
+                }
+                if (upto > want && upto - mine <= want) {  // one thread, unless they overflowed
+                    uint64_t run = upto - mine;
+                    int at_v = v + 7;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        run += left[k];
+                        if (run > want && at_v == v + 7) at_v = v + k;
+                    }
+                    a.next_token[b] = min(at_v, k1 - 1);
+                }
+                if (want < piece) break;  // the same in every thread
+                want -= piece;
             }
         }
     }
