@@ -187,10 +187,16 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
     // The sum of what is left, over the whole vocabulary; every thread of the cluster calls it.
     auto total_left = [&](const Residual &r) -> uint64_t {
         uint64_t sum = 0;
-        if (r.n == 0 || (r.n == 1 && r.q)) {
+        if (!r.q || r.n <= 1) {
             // the usual case: one or two rows, sixteen values of each in flight per lane
-            const float *p = r.p, *q = r.n == 1 ? r.q + (int64_t)r.rej[0] * V : nullptr;
+            const float *p = r.p, *q = r.q && r.n == 1 ? r.q + (int64_t)r.rej[0] * V : nullptr;
             sum = q ? sum_rows<true>(p, q, c0, c1, lane) : sum_rows<false>(p, p, c0, c1, lane);
+            for (int j = lane; j < r.n && !r.q; j += 32) {  // certain drafts: their tokens are lost, each once
+                const int x = r.tokens[r.rej[j]];
+                bool lost = x >= c0 && x < c1;
+                for (int i = 0; i < j; ++i) lost = lost && r.tokens[r.rej[i]] != x;
+                if (lost) sum -= fixed58(p[x]);
+            }
         } else {
             for (int v = c0 + lane; v < c1; v += 32) sum += r.at(v);
         }
