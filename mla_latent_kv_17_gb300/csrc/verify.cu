@@ -5,7 +5,7 @@
 // are whole rows read: the target's row and the rows of the drafts rejected there.  One
 // cluster of eight CTAs takes a request, each CTA an eighth of the vocabulary, so that a
 // single request still streams its rows through eight SMs; memory bounds a large batch (64
-// requests x 131,072 tokens, one rejection each: 67 MB, 22 us - four CTAs per SM at most have
+// requests x 131,072 tokens, one rejection each: 67 MB, 17.7 us - four CTAs per SM at most have
 // their rows in flight, and the walk, the cluster's sum and the draw stand before and after).
 //
 // All sums are 64-bit integers: a probability is cut to a multiple of 2^-58, which keeps every
@@ -47,7 +47,7 @@ __device__ __forceinline__ float counted(float p) { return fminf(fmaxf(p, 0.f), 
 
 // The same as a multiple of 2^-58: the significand at the top of a 64-bit word, shifted down by
 // what the exponent lacks (shifts of 64 and more give 0).  The conversion instruction to 64-bit
-// integers runs on the fp64 pipe, which it kept 75 % busy: 53 us for 64 x 131,072 against 22 us.
+// integers runs on the fp64 pipe, which it kept 75 % busy, for more than twice the whole call's time at 64 x 131,072.
 __device__ __forceinline__ uint64_t fixed58(float p) {
     const uint32_t b = __float_as_uint(counted(p));
     const uint64_t m = (uint64_t)((b << 8) | 0x80000000u) << 32;  // 2^63 x 1.fraction
@@ -63,12 +63,13 @@ struct Residual {
     const float *q;        // the draft's rows of this request, or null: certain of its token
     const int32_t *tokens;
     const int *rej;
-    const double *mass;
+    const uint64_t *mass;  // multiples of 2^-58
     int n, V;
 
     __device__ __forceinline__ uint64_t minus(uint64_t left, int k, float qv) const {
-        // the first draft is subtracted exactly; later ones are scaled by the mass left
-        const uint64_t d = k == 0 ? fixed58(qv) : __double2ull_rz((double)counted(qv) * mass[k]);
+        // the first draft is subtracted exactly; later ones are scaled by the mass left (q and the mass
+        // as whole multiples of 2^-58, the product cut to one; fp64 units are few on this part)
+        const uint64_t f = fixed58(qv), d = k == 0 ? f : __umul64hi(f << 5, mass[k] << 1);
         return left > d ? left - d : 0;
     }
     __device__ __forceinline__ uint64_t at(int v) const {
@@ -82,6 +83,31 @@ struct Residual {
         return left;
     }
 };
+
+// What is left of tokens v, v + kStep, ..., v + 7 kStep (0 at `end` and beyond): the rows' loads in flight
+// together.
+template <int kStep>
+__device__ __forceinline__ void left8(const Residual &r, int v, int end, uint64_t (&left)[8]) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = v + kStep * k < end ? r.p[v + kStep * k] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) left[k] = fixed58(x[k]);
+    for (int j = 0; j < r.n; ++j) {
+        if (r.q) {
+            const float *q = r.q + (int64_t)r.rej[j] * r.V;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = v + kStep * k < end ? q[v + kStep * k] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) left[k] = r.minus(left[k], j, x[k]);
+        } else {  // certain of its token
+            const int d = r.tokens[r.rej[j]] - v;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (d == kStep * k) left[k] = 0;
+        }
+    }
+}
 
 __device__ __forceinline__ uint64_t left_of(float p, float q) {
     const uint64_t x = fixed58(p), y = fixed58(q);
@@ -137,7 +163,7 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
     __shared__ bool s_stands[kVfMaxT];            // would token i stand as the first one tried at its place?
     __shared__ bool s_answer;
     __shared__ int s_rej[kVfMaxT];
-    __shared__ double s_mass[kVfMaxT];
+    __shared__ uint64_t s_mass[kVfMaxT];
     __shared__ uint64_t s_warp[kVfWarps];         // sums of this CTA's chunks
     __shared__ uint64_t s_slice[2][kVfCluster];   // sums of all slices, written by every CTA (two turns)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,7 +224,12 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
                 if (lost) sum -= fixed58(p[x]);
             }
         } else {
-            for (int v = c0 + lane; v < c1; v += 32) sum += r.at(v);
+            for (int v = c0 + lane; v < c1; v += 256) {
+                uint64_t left[8];
+                left8<32>(r, v, c1, left);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += left[k];
+            }
         }
         sum = warp_sum(sum);
         if (lane == 0) s_warp[warp] = sum;
@@ -224,7 +255,7 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
 
     // the walk; every thread takes the same decisions
     int at = -1, depth = 0, nrej = 0;
-    double mass = 1.0;
+    uint64_t mass = 0;  // what is left of the row's sum, where a sibling is tried after a rejection
     Residual r{target, draft, s_tok, s_rej, s_mass, 0, V};
     for (int i = 0; i < len; ++i) {
         const int x = s_tok[i];
@@ -233,7 +264,7 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
         if (nrej > 0) {
             if (tid == 0) {
                 const double u = a.uniforms[(int64_t)b * (T + 1) + i];
-                s_answer = u * (double)(draft ? counted(draft[(int64_t)i * V + x]) : 1.f) * mass < (double)r.at(x);
+                s_answer = u * (double)(draft ? counted(draft[(int64_t)i * V + x]) : 1.f) * (double)mass < (double)r.at(x);
             }
             __syncthreads();
             stands = s_answer;
@@ -243,7 +274,6 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
             at = i;
             ++depth;
             nrej = 0;
-            mass = 1.0;
             r.p = target + (int64_t)(i + 1) * V;
             r.n = 0;
             continue;
@@ -263,10 +293,10 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
             // certain drafts: only the token itself is lost (nothing, where it was lost before);
             // the first rejection's sum is the only pass a place needs
             r.n = nrej - 1;
-            mass -= (double)r.at(x);
+            mass -= r.at(x);
             r.n = nrej;
         } else {
-            mass = (double)total_left(r);
+            mass = total_left(r);
         }
     }
     uint64_t all = total_left(r);
@@ -290,32 +320,12 @@ __global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads,
             // values hold the place finds it among them (reading them again, one after another, took
             // 3 us of this call's end)
             const int k0 = min(v1, v0 + w * chunk), k1 = min(v1, k0 + chunk);
-            const float *q = r.q && r.n == 1 ? r.q + (int64_t)r.rej[0] * V : nullptr;
-            const bool plain = !r.q || r.n <= 1;
             // (sums that overflowed, of rows far from adding up to 1, may hold the place nowhere)
             if (tid == 0) a.next_token[b] = max(k1 - 1, 0);
             for (int c = k0; c < k1; c += 8 * kVfThreads) {
                 const int v = c + 8 * tid;
                 uint64_t left[8];
-                if (plain) {
-                    float pv[8], qv[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        pv[k] = v + k < k1 ? r.p[v + k] : 0.f;
-                        qv[k] = q && v + k < k1 ? q[v + k] : 0.f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) left[k] = left_of(pv[k], qv[k]);
-                    for (int j = 0; j < r.n && !r.q; ++j) {  // certain drafts: their tokens are lost
-                        const int d = r.tokens[r.rej[j]] - v;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (d == k) left[k] = 0;
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) left[k] = v + k < k1 ? r.at(v + k) : 0;
-                }
+                left8<1>(r, v, k1, left);
                 uint64_t mine = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mine += left[k];
