@@ -216,21 +216,17 @@ template <bool kTree>
 __global__ void __launch_bounds__(kCombineThreads, kCombineCtasPerSm)
 combine_kernel(DecodeArgs a) {
     __shared__ int32_t s_b[kCombineSmemReqs], s_n[kCombineSmemReqs], s_s0[kCombineSmemReqs];
-    // The plan is complete: every decode CTA waited for it before it let this kernel start.  Reading it
-    // ahead of the wait for the decode itself takes its chain of loads off the end.
-    if (!plan_matches(a)) {
-        grid_dep_wait();
-        return;
-    }
+    // The wait comes before the plan is read, too: that the decode waited for the plan promises this
+    // grid nothing about the plan's writes (ahead of the wait the chain of loads ran 2 us sooner).
+    grid_dep_wait();
+    grid_dep_launch();  // the next kernel on the stream may launch (it waits for this one)
+    if (!plan_matches(a)) return;
     const unsigned char *ws = a.ws;
     const int H = a.H;
     const PlanHeader *hd = reinterpret_cast<const PlanHeader *>(ws);
     const WsLayout L = ws_layout(hd->B, hd->H, hd->num_units, kTree);
     const int nsr = hd->num_split_reqs;
-    if (nsr <= 0) {
-        grid_dep_wait();
-        return;
-    }
+    if (nsr <= 0) return;
     const int32_t *split_list = reinterpret_cast<const int32_t *>(ws + L.split_list);
     const int32_t *num_splits = reinterpret_cast<const int32_t *>(ws + L.num_splits);
     const int32_t *split_base = reinterpret_cast<const int32_t *>(ws + L.split_base);
@@ -241,8 +237,6 @@ combine_kernel(DecodeArgs a) {
         s_s0[k] = split_base[b];
     }
     __syncthreads();
-    grid_dep_wait();
-    grid_dep_launch();  // the next kernel on the stream may launch (it waits for this one)
     const float *part_lse = reinterpret_cast<const float *>(ws + L.part_lse);
     const float4 *part_o = reinterpret_cast<const float4 *>(ws + L.part_o);
     const int64_t ostep = (int64_t)H * (kDLatent / 4);  // one piece to the next, in float4

@@ -289,3 +289,47 @@ def test_fp8_scales_of_other_magnitudes(scale):
     both(d, torch.float32, f"scale {scale}")
     s[:, ::3] *= 2.0 ** -9
     both(d, torch.float32, f"mixed {scale}")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("tree", [True, False])
+def test_replayed_plans_follow_the_lengths(kv, tree):
+    # a captured run of plans and calls whose lengths, and so split requests, change from step to
+    # step: every merge has to use the plan of its own step
+    T, H = (4, 64) if tree else (1, 128)
+    d = make(3, T, H, [9000, 20000, 400], kv=kv, seed=24)
+    kinds = [d["seq"].clone() for _ in range(3)]
+    kinds[1][1], kinds[2][0] = 700, 64
+    ws = ops.TreeWorkspace(3, T, H) if tree else ops.Workspace(3, H)
+    seq = d["seq"].clone()
+    shape = (3, T, H, 512) if tree else (3, H, 512)
+
+    def step(lens, out):
+        seq.copy_(lens)
+        if tree:
+            ops.plan_tree(ws, seq, d["lens"], kv_dtype=kv)
+            ops.decode_tree(ws, d["qn"], d["qr"], d["cache"], d["bt"], seq, d["lens"], d["mask"], tree_ref.SCALE, out=out)
+        else:
+            ops.plan(ws, seq, kv_dtype=kv)
+            ops.decode(ws, d["qn"].view(3, H, 512), d["qr"].view(3, H, 64), d["cache"], d["bt"], seq, tree_ref.SCALE, out=out)
+
+    want = [torch.zeros(shape, device="cuda") for _ in kinds]
+    for lens, out in zip(kinds, want):
+        step(lens, out)
+        assert ops.status(ws) == 0
+    outs = [torch.zeros(shape, device="cuda") for _ in range(12)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for k, out in enumerate(outs):
+                step(kinds[k % 3], out)
+        for _ in range(5):
+            for out in outs:
+                out.fill_(7.0)
+            graph.replay()
+            s.synchronize()
+            assert ops.status(ws, stream=s) == 0
+            for k, out in enumerate(outs):
+                assert torch.equal(out, want[k % 3]), k
