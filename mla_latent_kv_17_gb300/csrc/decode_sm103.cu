@@ -951,8 +951,10 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     }
                 };
                 if constexpr (kTree) {
+                    // by each row's own scale: the two round differently, and no row's values may hang on
+                    // another's scale (rows past the end may hold anything: masked and zeroed before PV)
                     const ScaleParts sp = split_scale(sc);
-                    if (__all_sync(0xffffffffu, scale_splits(sc)))
+                    if (r >= rows || scale_splits(sc))
                         each([&](uint4 x, uint8_t *box, int q) { expand_chunk_packed(x, sp, box, q, r); });
                     else
                         each([&](uint4 x, uint8_t *box, int q) { expand_chunk_ool(x, sc, box, q, r); });

@@ -333,3 +333,45 @@ def test_replayed_plans_follow_the_lengths(kv, tree):
             assert ops.status(ws, stream=s) == 0
             for k, out in enumerate(outs):
                 assert torch.equal(out, want[k % 3]), k
+
+
+def _behind(d):
+    """(page, first row) of what lies behind each request's last token in its last page."""
+    return [(int(d["bt"][b, int(n) // 64]), int(n) % 64) for b, n in enumerate(d["seq"]) if int(n) % 64]
+
+
+@pytest.mark.parametrize("contexts", [[300, 90, 17], [20000, 60, 1]])
+def test_fp8_bits_do_not_depend_on_what_lies_behind_the_last_token(contexts):
+    # the same inputs, whatever the last pages' unused rows held before: zeros of a fresh pool, old
+    # records of any scale, NaN
+    d = make(3, 5, 24, contexts, kv="fp8", seed=20)
+    want = None
+    for scale, code in ((0.0, 0), (3.0 / 448, 0x35), (2.0 ** -20, 0x11), (1e30, 0x7E), (float("nan"), 0x7F), (None, None)):
+        for k, (page, row) in enumerate(_behind(d)):
+            rec = d["cache"][page, row:]
+            if scale is None:  # every other row another scale
+                rec[:, 512:528].view(torch.float32)[::2] = 2.0 ** -12
+                continue
+            rec[:, :512] = code
+            rec[:, 512:528].view(torch.float32).fill_(scale)
+            rec[:, 528:] = code
+        out, lse, st, _ = run(d)
+        assert st == 0
+        want = want or (out, lse)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (scale, code)
+
+
+@pytest.mark.parametrize("context", [0, 40, 61, 12000])
+def test_fp8_scales_of_a_masked_token_leave_the_other_rows_bits(context):
+    d = make(1, 6, 40, [context], kv="fp8", seed=21)
+    bits = np.array([1, 2, 4, 8 | 1, 16 | 2, 32 | 16 | 2], dtype=np.uint64)  # token 2 is attended by itself only
+    d["mask"][0] = torch.from_numpy(bits.view(np.int64)).cuda()
+    for page, row in _behind(d):  # ordinary records
+        d["cache"][page, row:] = d["cache"][int(d["bt"][0, 0]), 0]
+    at, want, keep = context + 2, run(d), [0, 1, 3, 4, 5]
+    rec = d["cache"][int(d["bt"][0, at // 64]), at % 64]
+    for scale in (2.0 ** -16, 2.0 ** -11, 0.0, 130.0):
+        rec[512:528].view(torch.float32).fill_(scale)
+        out, lse, st, _ = run(d)
+        assert st == 0
+        assert torch.equal(out[0, keep], want[0][0, keep]) and torch.equal(lse[0, keep], want[1][0, keep]), scale
