@@ -666,24 +666,27 @@ __device__ __forceinline__ void expand_chunk(uint4 v, float s, uint8_t *box, int
 }
 
 // Tree decode: the same expansion in packed fp16 arithmetic, half as many instructions.  The scale
-// is split into two fp16 parts, so that code x scale = code x hi + code x lo is one product (tiny)
-// and one fused multiply-add, rounded once; a scale of 2^-10 or more is then held to 2^-15 of
-// itself, and the result is off by 2^-11 (1 + 2^-4) of its value at most.  Smaller scales (whose
-// parts would lie among fp16's subnormals) take expand_chunk, out of line.
+// is split into fp16 parts, hi of seven bits and lo: code x hi is exact (four bits times seven; no
+// bit of it lies below 2^-24 for scales of 2^-9 or more), so that code x lo + code x hi is rounded
+// once, as one fused multiply-add.  lo holds the rest to 2^-16 of the scale (2^-18, but for the
+// fp16 subnormals' step): the result is off by 2^-11 (1 + 2^-5) of its value at most, or by
+// 2^-25 + 2^-16 of it below fp16's normal range.  (With eleven bits in hi the product code x lo
+// falls among the subnormals, and rounding it took up to 1.85 x 2^-11.)  Other scales take
+// expand_chunk, out of line.
 struct ScaleParts {
     uint32_t hi, lo;  // fp16 pairs
 };
 __device__ __forceinline__ ScaleParts split_scale(float s) {
-    const __half h = __float2half_rn(s), l = __float2half_rn(s - __half2float(h));
-    const __half2 hh = __half2half2(h), ll = __half2half2(l);
+    const float top = __uint_as_float((__float_as_uint(s) + 0x10000u) & 0xFFFE0000u);  // seven bits, to nearest
+    const __half2 hh = __half2half2(__float2half_rn(top)), ll = __half2half2(__float2half_rn(s - top));
     return ScaleParts{*reinterpret_cast<const uint32_t *>(&hh), *reinterpret_cast<const uint32_t *>(&ll)};
 }
-__device__ __forceinline__ bool scale_splits(float s) { return s >= 0x1p-10f && s <= 128.f; }
+__device__ __forceinline__ bool scale_splits(float s) { return s >= 0x1p-9f && s <= 128.f; }
 __device__ __forceinline__ uint32_t e4m3x2_times(uint32_t two, const ScaleParts &s) {
     uint32_t c, t, r;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(c) : "r"(two));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(c), "r"(s.lo));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(s.hi), "r"(t));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(c), "r"(s.hi));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(s.lo), "r"(t));
     return r;
 }
 __device__ __forceinline__ void expand_chunk_packed(uint4 v, const ScaleParts &s, uint8_t *box, int q, int r) {

@@ -375,3 +375,39 @@ def test_fp8_scales_of_a_masked_token_leave_the_other_rows_bits(context):
         out, lse, st, _ = run(d)
         assert st == 0
         assert torch.equal(out[0, keep], want[0][0, keep]) and torch.equal(lse[0, keep], want[1][0, keep]), scale
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_fp8_values_enter_rounded_as_documented(T):
+    # one token attended with weight 1: the output is the fp16 value its code x scale became.  One
+    # rounding (2^-11, or 2^-25 below fp16's normal range) of code x scale, the scale held to 2^-15.
+    B = 256
+    g = torch.Generator().manual_seed(23)
+    scales = (2.0 ** (torch.rand(B, 4, generator=g).double() * 21 - 14)).float()  # 2^-14 .. 2^7
+    edges = [2.0 ** -10, 2.0 ** -9, 2.0 ** -8, 2.0 ** -7, 0.0010438, 3.0 / 448, 1.0, 127.9, 128.0, 145.0]
+    for k, s in enumerate(edges):
+        scales[k] = torch.tensor([s, s * (1 - 2.0 ** -24), s * (1 + 2.0 ** -23), s * 1.0037], dtype=torch.float64).float()
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8)
+    codes[codes & 0x7F == 0x7F] = 0
+    codes = torch.cat([codes, codes.flip(0)]).view(4, 128)
+    cache = torch.zeros(B, 64, 656, dtype=torch.uint8)
+    at = torch.arange(B)
+    for r in range(2):  # every scale meets all codes: the blocks change places
+        for k in range(4):
+            cache[at, r, 128 * k:128 * (k + 1)] = codes[(at[:, None] + k + r) % 4].reshape(B, -1)
+        cache[at, r, 512:528] = scales[at].contiguous().view(torch.uint8).view(B, 16)
+    cache[:, 2:] = cache[:, :1]  # (what lies behind the last token is like the tokens)
+    d = dict(qn=torch.zeros(B, T, 1, 512, dtype=torch.bfloat16, device="cuda"),
+             qr=torch.zeros(B, T, 1, 64, dtype=torch.bfloat16, device="cuda"), cache=cache.cuda(),
+             bt=torch.randperm(B, generator=g).to(torch.int32).view(B, 1).cuda(),
+             seq=torch.full((B,), T, dtype=torch.int32, device="cuda"),
+             lens=torch.full((B,), T, dtype=torch.int32, device="cuda"),
+             mask=(1 << torch.arange(T, dtype=torch.int64)).repeat(B, 1).cuda())
+    out, lse, st, _ = run(d)
+    assert st == 0 and bool((lse == 0).all())
+    rec = cache[d["bt"].cpu().long().view(-1)][:, :T]
+    x = rec[..., :512].contiguous().view(torch.float8_e4m3fn).double() \
+        * rec[..., 512:528].contiguous().view(torch.float32).double().repeat_interleave(128, -1)
+    err = (out.view(B, T, 512).cpu().double() - x).abs()
+    bound = torch.where(x.abs() >= 2.0 ** -14, 2.0 ** -11 * (1 + 2.0 ** -4) * x.abs(), 2.0 ** -25 + 2.0 ** -15 * x.abs())
+    assert bool((err <= bound).all()), float((err / x.abs().clamp(min=2.0 ** -14) * 2.0 ** 11).max())
