@@ -314,9 +314,11 @@ mla_status mla_cache_read(const void *cache, mla_kv_dtype kv_dtype, int64_t num_
  * q_nope bf16 [B][T][H][512], q_rope bf16 [B][T][H][64], tree_mask uint64 [B][T], out fp32 or
  * bf16 (rounded once; the operand type mla_project_output rounds to in any case)
  * [B][T][H][512], lse fp32 [B][T][H] or NULL.  Tokens i >= n and tokens that attend to nothing
- * get out = 0 and lse = -inf.  The queries of tokens i >= n may hold anything.  A drafted token's
- * entry may hold anything, NaN included, where no row attends to it (an FP8 record's scales are
- * checked for MLA_ERR_RANGE all the same); entries before the drafted ones must be finite.
+ * get out = 0 and lse = -inf.  The queries of tokens i >= n may hold anything; the others must be
+ * finite.  A drafted token's entry may hold anything, NaN included, and reaches only the rows that
+ * attend to it: where it holds a NaN or an infinity their out and lse are NaN, also where it scores
+ * -inf, whose weight of 0 would hide it.  (An FP8 record's scales are checked for MLA_ERR_RANGE
+ * whether attended or not.)  Entries before the drafted ones must be finite.
  * The rows of a request's T x H queries are taken 128 at a time, so a cache page is read once
  * per 128 rows: with 16 heads, eight drafted tokens cost about what one does.
  * tree_lens outside [0, T] or above seq_lens[b] are clamped and recorded as MLA_ERR_INDEX;

@@ -535,7 +535,8 @@ __device__ __noinline__ void store_tree_rows(uint32_t tcol, uint8_t *stg, void *
 // others, so a NaN or infinity in it (a branch gone wrong) must not reach the rows that mask
 // it through 0 x NaN.  Rows lo .. hi - 1 of a 64-row latent-half page (4 boxes) lose their
 // non-finite values before PV reads them; the rows that do attend the token still get a NaN,
-// from its score.
+// from its score: NaN, an infinity above every other, or one below them (looked for before the
+// scores are masked; FP8 records: bad_keys).
 template <bool kF16>
 __device__ __noinline__ void clean_rows(uint8_t *dh, int lo, int hi, int h) {
     constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
@@ -558,6 +559,38 @@ __device__ __noinline__ void clean_rows(uint8_t *dh, int lo, int hi, int h) {
         }
         if (bad) *p = v;
     }
+}
+
+// FP8 records: which of the drafted tokens (from position `first` on) at positions [t0, t1) have a key
+// part that is not finite (bit j: token j).  A row that attends one of them is NaN, whatever sign the
+// score has; the latent part holds no infinity (a scale that makes one is reported).  Looked for
+// once per item, in memory, while the last PV runs: in the tile loop, as for the bf16 cache, this
+// mode ran 8 % slower, here 0.9 % (32 requests x 4 tokens x 128 heads 188.4 -> 190.1 us).
+__device__ __noinline__ uint64_t bad_keys(const unsigned char *cache, const int32_t *table, int max_pages,
+                                          int64_t num_pages, int first, int t0, int t1, int lane) {
+    uint64_t found = 0;
+#pragma unroll 1
+    for (int j0 = 0; j0 < kMaxDrafted && first + j0 < t1; j0 += 32) {
+        const int pos = first + j0 + lane, lp = pos / kPageRows;
+        uint32_t top = 0;
+        if (pos >= t0 && pos < t1 && lp < max_pages) {
+            const int64_t page = table[lp];
+            if (page >= 0 && page < num_pages) {
+                const uint4 *key = reinterpret_cast<const uint4 *>(
+                    cache + (page * kPageRows + pos % kPageRows) * kFp8RecordBytes + kDLatent + 16);
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = key[i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // an exponent of all ones carries into its value's sign bit
+                    top |= ((v[i].x & 0x7F807F80u) + 0x00800080u) | ((v[i].y & 0x7F807F80u) + 0x00800080u) |
+                           ((v[i].z & 0x7F807F80u) + 0x00800080u) | ((v[i].w & 0x7F807F80u) + 0x00800080u);
+                }
+            }
+        }
+        found |= (uint64_t)__ballot_sync(0xffffffffu, (top & 0x80008000u) != 0u) << j0;
+    }
+    return found;
 }
 
 // Which tokens of the 64 that start at `t` a query row attends: everything before the drafted
@@ -1572,6 +1605,19 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                     if (lane == 0) mbar_arrive(bar(base, B_S_FREE));
                     // the item's last scores are read: its query area is free for the next query
                     if (kFp8 && t + kTile >= w.t1 && bnext >= 0 && threadIdx.x == 0) q_round(bnext, 0);
+                    bool bad = false;  // the row attends a drafted token whose infinity gives it the score -inf
+                    if constexpr (kTree && !kFp8) {
+                        if (t + kTile > first) {  // drafted tokens in this tile
+                            float lowest = s[0];
+#pragma unroll
+                            for (int i = 1; i < 64; ++i) lowest = fminf(lowest, s[i]);
+                            if (__builtin_expect(lowest == -INFINITY, 0)) {
+                                const uint64_t drafted = vown & ~tree_row_mask(t + kPageRows * (int)rank, first, 0ull);
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) bad = bad || (s[i] == -INFINITY && (drafted >> i & 1ull));
+                            }
+                        }
+                    }
                     if (vown != ~0ull) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
@@ -1594,6 +1640,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         lown += p0 + p1;
                         pk[i] = pack_op<kFp8>(p0, p1);
                     }
+                    if constexpr (kTree && !kFp8) lown = bad ? __uint_as_float(0x7FFFFFFFu) : lown;
                     // cache rows that PV reads but must not contribute (rows of the last
                     // 16-row step past the end, a page whose id was out of range, sparse slots
                     // that are padding or out of range) must hold zeros there, not whatever
@@ -1720,6 +1767,13 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                         break;
                     }
                     q_ready = true;
+                }
+                if constexpr (kTree && kFp8) {
+                    if (w.t1 > first) {  // drafted tokens in this item
+                        const uint64_t odd = bad_keys(a.cache, a.block_table + (int64_t)entry_request(b) * a.max_pages,
+                                                      a.max_pages, a.num_pages, first, w.t0, w.t1, lane);
+                        if ((odd & tbits) != 0ull) l = __uint_as_float(0x7FFFFFFFu);
+                    }
                 }
                 // ---- epilogue: wait for the last PV of this item, normalise, store
                 if (!warp_wait(c, bar(base, B_O_FINAL), nitem & 1u, false)) {

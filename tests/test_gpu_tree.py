@@ -411,3 +411,30 @@ def test_fp8_values_enter_rounded_as_documented(T):
     err = (out.view(B, T, 512).cpu().double() - x).abs()
     bound = torch.where(x.abs() >= 2.0 ** -14, 2.0 ** -11 * (1 + 2.0 ** -4) * x.abs(), 2.0 ** -25 + 2.0 ** -15 * x.abs())
     assert bool((err <= bound).all()), float((err / x.abs().clamp(min=2.0 ** -14) * 2.0 ** 11).max())
+
+
+@pytest.mark.parametrize("kv,channel", [("bf16", 100), ("bf16", 400), ("bf16", 530), ("fp8", 530)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("context", [0, 61, 126, 500, 12000])
+def test_one_infinity_shows_in_every_row_that_attends_it(kv, channel, value, context):
+    # whichever sign it gives the score: a weight of 0 must not hide the token
+    d = make(1, 6, 40, [context], kv=kv, seed=22)
+    bits = np.array([1, 2, 4, 8 | 1, 16 | 2, 32 | 4], dtype=np.uint64)  # token 2: by itself and by token 5
+    d["mask"][0] = torch.from_numpy(bits.view(np.int64)).cuda()
+    want = run(d)
+    at = context + 2
+    rec = d["cache"][int(d["bt"][0, at // 64]), at % 64]
+    if kv == "bf16":
+        rec[channel] = value
+        q = d["qn"][0, 2, :, channel] if channel < 512 else d["qr"][0, 2, :, channel - 512]
+    else:
+        rec[528:].view(torch.bfloat16)[channel - 512] = value
+        q = d["qr"][0, 2, :, channel - 512]
+    assert bool((q > 0).any()) and bool((q < 0).any())  # scores of both signs
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse, st, _ = run(d, dtype)
+        keep = [0, 1, 3, 4]
+        assert st == 0
+        assert torch.equal(out[0, keep], want[0][0, keep].to(dtype)) and torch.equal(lse[0, keep], want[1][0, keep])
+        for i in (2, 5):
+            assert bool(torch.isnan(out[0, i]).all()) and bool(torch.isnan(lse[0, i]).all()), i
