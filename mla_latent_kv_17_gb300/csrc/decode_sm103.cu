@@ -699,22 +699,22 @@ __device__ __forceinline__ void expand_chunk(uint4 v, float s, uint8_t *box, int
 }
 
 // Tree decode: the same expansion in packed fp16 arithmetic, half as many instructions.  The scale
-// is split into fp16 parts, hi of seven bits and lo: code x hi is exact (four bits times seven; no
-// bit of it lies below 2^-24 for scales of 2^-9 or more), so that code x lo + code x hi is rounded
-// once, as one fused multiply-add.  lo holds the rest to 2^-16 of the scale (2^-18, but for the
-// fp16 subnormals' step): the result is off by 2^-11 (1 + 2^-5) of its value at most, or by
-// 2^-25 + 2^-16 of it below fp16's normal range.  (With eleven bits in hi the product code x lo
+// is split into fp16 parts, hi of six bits and lo: code x hi is exact (four bits times six; no bit
+// of it lies below 2^-24 for scales of 2^-10 or more), so that code x lo + code x hi is rounded
+// once, as one fused multiply-add.  lo holds the rest to 2^-15 of the scale (2^-17, but for the
+// fp16 subnormals' step): the result is off by 2^-11 (1 + 2^-4) of its value at most, or by
+// 2^-25 + 2^-15 of it below fp16's normal range.  (With eleven bits in hi the product code x lo
 // falls among the subnormals, and rounding it took up to 1.85 x 2^-11.)  Other scales take
 // expand_chunk, out of line.
 struct ScaleParts {
     uint32_t hi, lo;  // fp16 pairs
 };
 __device__ __forceinline__ ScaleParts split_scale(float s) {
-    const float top = __uint_as_float((__float_as_uint(s) + 0x10000u) & 0xFFFE0000u);  // seven bits, to nearest
+    const float top = __uint_as_float((__float_as_uint(s) + 0x20000u) & 0xFFFC0000u);  // six bits, to nearest
     const __half2 hh = __half2half2(__float2half_rn(top)), ll = __half2half2(__float2half_rn(s - top));
     return ScaleParts{*reinterpret_cast<const uint32_t *>(&hh), *reinterpret_cast<const uint32_t *>(&ll)};
 }
-__device__ __forceinline__ bool scale_splits(float s) { return s >= 0x1p-9f && s <= 128.f; }
+__device__ __forceinline__ bool scale_splits(float s) { return s >= 0x1p-10f && s <= 128.f; }
 __device__ __forceinline__ uint32_t e4m3x2_times(uint32_t two, const ScaleParts &s) {
     uint32_t c, t, r;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(c) : "r"(two));
@@ -989,6 +989,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 if constexpr (kTree) {
                     // by each row's own scale: the two round differently, and no row's values may hang on
                     // another's scale (rows past the end may hold anything: masked and zeroed before PV)
+                    // (32 requests x 4 tokens x 128 heads: 190 us; with every scale below the split's range 244;
+                    // with one row of a page below it 256, since a warp then runs both)
                     const ScaleParts sp = split_scale(sc);
                     if (r >= rows || scale_splits(sc))
                         each([&](uint4 x, uint8_t *box, int q) { expand_chunk_packed(x, sp, box, q, r); });
