@@ -989,8 +989,8 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
                 if constexpr (kTree) {
                     // by each row's own scale: the two round differently, and no row's values may hang on
                     // another's scale (rows past the end may hold anything: masked and zeroed before PV)
-                    // (32 requests x 4 tokens x 128 heads: 190 us; with every scale below the split's range 244;
-                    // with one row of a page below it 256, since a warp then runs both)
+                    // (32 requests x 4 tokens x 128 heads, replayed on one input: 197 us; with every scale
+                    // below the split's range 250; with one row of a page below it 262: a warp then runs both)
                     const ScaleParts sp = split_scale(sc);
                     if (r >= rows || scale_splits(sc))
                         each([&](uint4 x, uint8_t *box, int q) { expand_chunk_packed(x, sp, box, q, r); });
