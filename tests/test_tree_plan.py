@@ -96,3 +96,30 @@ def test_binding_refuses_host_tensors():
         ops.plan_tree(Fake(), z)
     with pytest.raises(ValueError, match="CUDA"):
         ops.decode_tree(Fake(), z, z, z, z, z, z, z, 0.1)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,T,H,hi,short", [(16, 64, 128, 300, 1), (16, 64, 128, 0, 0), (12, 16, 64, 700, 2), (40, 8, 128, 9000, 8),
+                                            (64, 8, 16, 8192, 8), (5, 1, 128, 4000, 1), (1, 64, 128, 90000, 64)])
+def test_units_share_the_cost_the_plan_states(B, T, H, hi, short, kv):
+    # pieces at what the planner charges for them, and one tile for each row tile past the drafted
+    # tokens (many of them in a row: none of them may fall to one unit)
+    rng = np.random.default_rng(B + T + hi)
+    lens = rng.integers(0, short + 1, B) if short else np.zeros(B, int)
+    seq = rng.integers(0, hi + 1, B) + lens
+    units = 74
+    R = (T * H + 127) // 128
+    p = parse(ops.plan_tree_host(seq, lens, B, T, H, num_sms=2 * units, kv_dtype=kv), B * R, 128)
+    ovh, empty = (3 if kv == "fp8" else 2) + (T > 1), int(T > 1)
+    cost, empties = np.zeros(units), np.zeros(units, int)
+    for u in range(units):
+        for i in range(p["unit_begin"][u], p["unit_begin"][u + 1]):
+            _, t0, t1, _ = p["items"][i]
+            cost[u] += (t1 - t0 + 127) // 128 + ovh if t1 > t0 else empty
+            empties[u] += t1 <= t0
+    # a unit's share, a tile folded in from either side, and the charge of a piece begun elsewhere
+    most = p["per"] + 2 + ovh
+    assert cost.max() <= most
+    if T > 1:
+        assert empties.max() <= most
+    assert empties.sum() == sum(int(lens[b] * H <= t * 128 or seq[b] == 0) for b in range(B) for t in range(R))
