@@ -256,3 +256,48 @@ def test_prefix_read_back_feeds_the_prefill(kv):
     k, v = ops.prefill_decompress(entries, w_uk, w_uv)
     want = torch.einsum("hjc,tc->htj", w_uk.double(), entries[:, :512].double())
     assert bool(((k.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_every_call_does_its_work_on_a_given_stream(kv):
+    # the current stream is busy meanwhile: what a call queued there, or waited for there, would be
+    # missing from its results
+    st = Step(kv, 7)
+    x, s = st.x, torch.cuda.Stream()
+    q_nope = ops.absorb_query(ops.rope(x["q"], st.rpos, st.freqs)[0], st.w_uk).view(B, T, H, 512)
+    q_rope = x["q"][..., 128:].contiguous().view(B, T, H, 64)
+
+    def calls(cache, ws, given, stream=None):
+        g = given
+        p, r = ops.rope(x["q"], st.rpos, st.freqs, mscale=st.mscale, stream=stream)
+        ops.rope(x["q"], st.rpos, st.freqs, out_pass=g["p"], out_rot=g["r"], stream=stream)
+        ops.cache_write(cache, st.bt, st.req, st.slot, x["kv"], freqs=st.freqs, rope_positions=st.rpos,
+                        mscale=st.mscale, norm_weight=st.norm, stream=stream)
+        e = ops.cache_read(cache, st.bt, st.req, g["slot"], stream=stream)
+        ops.cache_read(cache, st.bt, st.req, st.slot, entries=g["e"], stream=stream)
+        ops.plan_tree(ws, st.seq, st.lens, kv_dtype=kv, stream=stream)
+        args = (ws, q_nope, q_rope, cache, st.bt, st.seq, st.lens, st.mask, tree_ref.SCALE)
+        o, l = ops.decode_tree(*args, out_dtype=torch.bfloat16, stream=stream)
+        ops.decode_tree(*args, out=g["o"], lse=g["l"], stream=stream)
+        v = ops.verify_draft(x["target"], x["draft"], x["tok"], x["u"], parents=x["parents"], tree_lens=st.lens, stream=stream)
+        return [p, r, e, o, l, *v, *(g[k] for k in ("p", "r", "e", "o", "l")), cache.view(torch.uint8)]
+
+    def buffers():
+        new = lambda *shape, dtype=torch.bfloat16: torch.full(shape, 7.0, dtype=dtype, device="cuda")
+        return dict(p=new(B * T, H, 128), r=new(B * T, H, 64), e=new(B * T, 576), o=new(B, T, H, 512, dtype=torch.float32),
+                    l=new(B, T, H, dtype=torch.float32), slot=st.slot.clamp(min=0))
+
+    want = calls(st.cache.clone(), ops.TreeWorkspace(B, T, H), buffers())
+    runs = [(st.cache.clone(), ops.TreeWorkspace(B, T, H), buffers()) for _ in range(2)]
+    torch.cuda.synchronize()
+    calls(*runs[0], stream=s)  # (the allocator's blocks for this stream: an allocation may wait for the device)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # some 200 ms of the current stream
+    got = calls(*runs[1], stream=s)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    with torch.cuda.stream(s):
+        same = [torch.equal(a, b) for a, b in zip(got, want)]
+    assert all(same), same
+    torch.cuda.synchronize()
+    assert ops.status(runs[1][1]) == 0
