@@ -334,14 +334,15 @@ mla_status launch_rw(K kernel, const RwArgs &a, int warps, int most, void *strea
                                                                                                        : MLA_ERR_CUDA;
 }
 
-// Arguments the write and the read share; fills `a` with them.
+// Arguments the write and the read share; fills `a` with them (where there are tokens).
 mla_status check_rw(RwArgs *a, const void *cache, mla_kv_dtype kv_dtype, int64_t num_pages,
                     const int32_t *block_table, int num_requests, int max_pages, const int32_t *requests,
                     const int32_t *positions, const void *rows, int64_t stride, int64_t N, int32_t *device_status) {
-    if (N < 0 || num_requests < 1 || max_pages < 1 || num_pages < 1 || stride < kDEntry) return MLA_ERR_INVALID_ARG;
+    if (N < 0 || stride < kDEntry) return MLA_ERR_INVALID_ARG;
     if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
-    if (!cache || !block_table) return MLA_ERR_INVALID_ARG;
-    if (N > 0 && (!positions || !rows)) return MLA_ERR_INVALID_ARG;
+    if (N == 0) return MLA_OK;  // (the caller enqueues nothing; a batch may have no requests, then)
+    if (num_requests < 1 || max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+    if (!cache || !block_table || !positions || !rows) return MLA_ERR_INVALID_ARG;
     if (!requests && N > num_requests) return MLA_ERR_INVALID_ARG;
     if (!aligned16(cache) || !aligned16(rows) || stride % 8 != 0) return MLA_ERR_INVALID_ARG;
     a->cache = (unsigned char *)const_cast<void *>(cache);

@@ -127,3 +127,13 @@ def test_rope_frequencies():
     for kw in (dict(d_rot=63), dict(base=1.0), dict(factor=0.5), dict(scaling="x"), dict(scaling="yarn", beta_fast=1.0)):
         with pytest.raises(ValueError):
             ops.rope_frequencies(**{**dict(d_rot=64, device="cpu"), **kw})
+
+
+def test_no_tokens_are_nothing_to_do_whatever_the_batch():
+    # a step without requests: no table, no pages, no rows
+    none = dict(N=0, cache=0, bt=0, req=0, pos=0, pages=0, B=0, mp=0)
+    assert _write(**none, kv=0) == OK and _write(**none, kv=0, kind=1, w=A, freqs=A) == OK
+    assert _read(**none, e=0) == OK
+    # what does not depend on the batch is checked all the same
+    assert _write(**none, kv=0, kind=2) == INVALID and _write(**none, kv=0, layout=5) == INVALID
+    assert _read(**none, e=0, stride=512) == INVALID
