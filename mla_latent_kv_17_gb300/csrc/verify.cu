@@ -69,7 +69,7 @@ struct Residual {
     __device__ __forceinline__ uint64_t minus(uint64_t left, int k, float qv) const {
         // the first draft is subtracted exactly; later ones are scaled by the mass left (q and the mass
         // as whole multiples of 2^-58, the product cut to one; fp64 units are few on this part)
-        const uint64_t f = fixed58(qv), d = k == 0 ? f : __umul64hi(f << 5, mass[k] << 1);
+        const uint64_t f = fixed58(qv), d = k == 0 ? f : __umul64hi(f, mass[k]) << 6 | (f * mass[k]) >> 58;
         return left > d ? left - d : 0;
     }
     __device__ __forceinline__ uint64_t at(int v) const {

@@ -171,3 +171,19 @@ def test_empty_batch():
     n, d, x = ops.verify_draft(torch.zeros(0, 3, 5, device="cuda"), None,
                                torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, 3, device="cuda"))
     assert n.shape == (0,) and d.shape == (0, 2) and x.shape == (0,)
+
+
+@pytest.mark.parametrize("total", [20.0, 40.0, 60.0])
+def test_siblings_of_rows_that_add_up_to_less_than_64(total):
+    # residuals of more than half the sums' range: what a second sibling covers is its share of all of it
+    B, T, V = 60, 4, 200
+    g = torch.Generator(device="cuda").manual_seed(31)
+    target = torch.rand(B, T + 1, V, generator=g, device="cuda")
+    target = (target / target.sum(-1, keepdim=True) * total).contiguous()
+    draft = (3 * torch.randn(B, T, V, generator=g, device="cuda")).softmax(-1)
+    tok = draft.argmax(-1).to(torch.int32)
+    parents = torch.full((B, T), -1, dtype=torch.int32, device="cuda")
+    u = 0.9 + 0.09 * torch.rand(B, T + 1, generator=g, device="cuda")
+    u[:, T] = torch.rand(B, generator=g, device="cuda")
+    n, _, _ = run(target, draft, tok, u, parents)
+    assert int((n == 0).sum()) > 10  # all four fell
