@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kRwWarps = 8;
 constexpr int kWriteWarps = 32, kWriteMost = 16;  // see launch_rw
+constexpr int kSms = 152;  // a GB300's; only the grids' shapes depend on it
 constexpr unsigned kAll = 0xffffffffu;
 
 struct RwArgs {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 8) read_kernel(RwArgs a) {
 // keep them busy, up to `most`.
 template <typename K>
 mla_status launch_rw(K kernel, const RwArgs &a, int warps, int most, void *stream) {
-    const int64_t want = (a.N + 152 * warps - 1) / (152 * warps);
+    const int64_t want = (a.N + kSms * warps - 1) / (kSms * warps);
     const int per = (int)(want < 1 ? 1 : want > most ? most : want);
     const int64_t ctas = (a.N + (int64_t)per * kRwWarps - 1) / ((int64_t)per * kRwWarps);
     if (ctas > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
@@ -405,7 +406,7 @@ extern "C" mla_status mla_cache_read(const void *cache, mla_kv_dtype kv_dtype, i
                                    positions, entries, entries_stride, N, device_status);
     if (st != MLA_OK) return st;
     if (N == 0) return MLA_OK;
-    const int64_t ctas = (N + kRwWarps - 1) / kRwWarps, resident = 152 * 8;
+    const int64_t ctas = (N + kRwWarps - 1) / kRwWarps, resident = kSms * 8;
     return launch_pdl(kv_dtype == MLA_KV_FP8_E4M3 ? read_kernel<true> : read_kernel<false>,
                       (int)(ctas < resident ? ctas : resident), 32 * kRwWarps, 0, (cudaStream_t)stream,
                       a) == cudaSuccess

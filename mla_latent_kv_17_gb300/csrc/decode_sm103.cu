@@ -823,7 +823,7 @@ struct Fp8Loads {
 // kMode 0: dense bf16 tiles (128 consecutive tokens, two pages, 64-row boxes).
 // kMode 1: DSA sparse tiles (128 index slots gathered row by row, tile::gather4).
 // kMode 2: dense FP8 records: raw e4m3 codes and scales are loaded by two extra warps (one
-//          for the latent-half ring, one for the other-columns stage) and expanded to bf16
+//          for the latent-half ring, one for the other-columns stage) and expanded to fp16
 //          operand tiles by eight warps; RoPE goes in directly.
 // tmap: the cache (kMode 2: its bytes, 128-B boxes of codes; kMode 1: one-row boxes);
 // tmap_sc: FP8 scales (16-B boxes) or, for kMode 1, the cache in 64-row boxes; tmap_rope:
@@ -834,9 +834,9 @@ struct Fp8Loads {
 // ~2.95).  By clock traces its 3,750 cycles are 8 PV operations of 128 x 256 (~1,000) and 36 QK^T
 // operations of 128 x 64 (~80 each, of which the arithmetic is 32), one after the other; shared
 // memory moves 369 KB meanwhile (2,900 cycles of its bandwidth).  With all heads on one GPU
-// (16 requests x 8 tokens x 128 heads, 1,024-8,192 tokens) that bounds the call: 132 us against 66
+// (16 requests x 8 tokens x 128 heads, 1,024-8,192 tokens) that bounds the call: 133 us against 66
 // for its products; one 128-row tile per request (64 x 8 x 16, the same lengths) reads the cache
-// once and takes 99 us against 53.
+// once and takes 100 us against 53.
 template <int kMode, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMode == 2 ? kThreadsFp8 : kMode == 1 ? kThreadsSparse : kThreads, 1)
 decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tmap_sc,
@@ -922,7 +922,7 @@ decode_sm103_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_const
         // Warps 4, 7, 9, 10 and 12-15 (two per SM sub-partition) expand every job, in the order the
         // jobs are consumed: a warp takes part p (codes 128 p .. 128 p + 127) of 16 rows, a lane
         // every other 16-code chunk of a row.  The codes of part p of row r arrive as one 128-B row
-        // of box 2p of the bf16 destination, the box that receives the first half of that part's
+        // of box 2p of the fp16 destination, the box that receives the first half of that part's
         // output (the second half goes to box 2p + 1): a row's two lanes read all their codes before
         // either writes.  (With four warps, the peer page first and a page found between two loads
         // 32 requests x 4 tokens x 128 heads took 2 % more.)

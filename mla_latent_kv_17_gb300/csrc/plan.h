@@ -156,7 +156,8 @@ MLA_HD int piece_overhead(int fp8_records) { return fp8_records ? 3 : 2; }
 // A tree's items are shorter and more (every row tile of a request): one tile more each (16 requests
 // x 8 tokens x 128 heads 1.8 % faster than with none, FP8 records 32 x 4 x 128 0.9 %; with two more
 // 1.1 % faster and 0.3 % slower).  One token is planned as the plain decode plans it, and so gives its
-// very bits.
+// very bits over a bf16 cache (a tree's FP8 records are expanded in packed fp16 arithmetic, which
+// rounds a few values the other way).
 MLA_HD int tree_piece_overhead(int fp8_records, int T) { return piece_overhead(fp8_records) + (T > 1 ? 1 : 0); }
 // An entry without tiles costs nothing, but for a tree's row tiles past the drafted tokens: many of
 // them follow one another, and the zeros they write (64 KB per SM) would all fall to one unit (24 us

@@ -710,7 +710,8 @@ def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens,
     """Tree attention with the plan in ws: q_nope bf16 [B,T,H,512], q_rope bf16 [B,T,H,64]; cache bf16
     [P,64,576] or uint8 FP8 records [P,64,656], holding seq_lens[b] entries of request b, the last
     tree_lens[b] (None: T) of them its drafted tokens'; tree_mask int64 [B,T]: bit j of [b,i] set:
-    token i attends drafted token j.  -> (out fp32 or bf16 [B,T,H,512], lse fp32 [B,T,H] or None)."""
+    token i attends drafted token j.  -> (out fp32 or bf16 [B,T,H,512], lse fp32 [B,T,H] or None);
+    NaN for a token that attends a drafted one whose entry is not finite."""
     B, T, H = ws.B, ws.T, ws.H
     dev = _device_of("q_nope q_rope cache block_table seq_lens tree_lens tree_mask out lse workspace", q_nope, q_rope,
                      cache, block_table, seq_lens, tree_lens, tree_mask, out, lse, ws.buf)
