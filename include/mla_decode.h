@@ -262,7 +262,8 @@ typedef enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 } mla_rope_layout;
  *   (a, b) -> mscale * (a cos theta - b sin theta,  a sin theta + b cos theta),
  * computed in fp32 and rounded once to bf16.  The angle is reduced exactly (64-bit fixed
  * point), so positions up to 2^31 keep fp32 accuracy; freqs is fp64 (radians per position),
- * which is where a long context's scaling goes; a negative position turns backwards.
+ * finite and below 2^52, which is where a long context's scaling goes; a negative position turns
+ * backwards.
  * x, out_pass, out_rot: bf16, values of a row adjacent, rows placed by the given token and
  * head strides (in elements).  out_pass may be NULL (the passing part is not copied), and
  * out_rot may be x's own rotated part (rotation in place; any other overlap is undefined).
