@@ -274,6 +274,19 @@ mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride
                     void *out_pass, int64_t pass_token_stride, int64_t pass_head_stride, void *out_rot,
                     int64_t rot_token_stride, int64_t rot_head_stride, void *stream);
 
+/* Rotary positions with several axes (an image's or a video's tokens: time, height, width): as
+ * mla_rope, but token n stands at num_axes positions, positions[n * position_token_stride +
+ * x * position_axis_stride] on axis x, and pair j of a head turns by its own axis's:
+ *   theta = position(n, axes[j]) * freqs[j].
+ * Where a token's positions are equal on all axes (text), the result is mla_rope's.  positions int32
+ * with any strides (in elements; [N][A] or [A][N]).  axes: HOST array [d_rot / 2], each below
+ * num_axes; read before the call returns.  1 <= num_axes <= 4, d_rot <= 512. */
+mla_status mla_rope_axes(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t N, int H, int d_pass,
+                         int d_rot, mla_rope_layout layout, const int32_t *positions, int64_t position_token_stride,
+                         int64_t position_axis_stride, int num_axes, const uint8_t *axes, const double *freqs,
+                         float mscale, void *out_pass, int64_t pass_token_stride, int64_t pass_head_stride,
+                         void *out_rot, int64_t rot_token_stride, int64_t rot_head_stride, void *stream);
+
 /* Cache write of many tokens (a ragged batch's prompts, or drafted tokens): token n of
  * request requests[n] (NULL: request n) goes to that request's logical position positions[n],
  * page block_table[request][position / 64], row position % 64.  kv bf16 [N][576] with row
@@ -295,6 +308,15 @@ mla_status mla_cache_write(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages
                            const void *kv, int64_t kv_stride, int64_t N, const void *norm_weight, float norm_eps,
                            const double *freqs, const int32_t *rope_positions, mla_rope_layout layout, float mscale,
                            int32_t *device_status, void *stream);
+
+/* mla_cache_write of tokens whose keys turn by several axes, as mla_rope_axes: rope_positions (not
+ * NULL) with the strides and the axes of the 32 pairs given there; freqs is needed. */
+mla_status mla_cache_write_axes(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages, const int32_t *block_table,
+                                int num_requests, int max_pages, const int32_t *requests, const int32_t *positions,
+                                const void *kv, int64_t kv_stride, int64_t N, const void *norm_weight, float norm_eps,
+                                const double *freqs, const int32_t *rope_positions, int64_t position_token_stride,
+                                int64_t position_axis_stride, int num_axes, const uint8_t *axes, mla_rope_layout layout,
+                                float mscale, int32_t *device_status, void *stream);
 
 /* Cache read, the way back: entries[n][0..576) = the entry at logical position positions[n]
  * of request requests[n] (NULL: request n), bf16; an FP8 record is dequantised as
@@ -367,6 +389,37 @@ mla_status mla_verify_draft(const float *target, const float *draft, const int32
                             const int32_t *tree_lens, const float *uniforms, int B, int T, int V,
                             int32_t *num_accepted, int32_t *depths, int32_t *next_token, int32_t *device_status,
                             void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Prompts of text and images that meet states which exist already.  Their queries and keys turn by
+ * several axes (mla_rope_axes, mla_cache_write_axes above); their queries attend key runs of another
+ * length than their own (a prefix read back from the cache, an encoder's states), and their tokens
+ * are scored (mla_token_logprobs).
+ * ------------------------------------------------------------------------------------------ */
+
+/* Log probabilities of given tokens: for each of N rows of logits x [V], with p = softmax(scale x)
+ * over the row,
+ *   logprob[n]  = ln p(tokens[n]),
+ *   entropy[n]  = - sum p ln p,
+ *   rank[n]     = how many tokens come before tokens[n] when the row is sorted by falling logits,
+ *                 equal logits by rising token (0: the best one),
+ *   top_tokens[n][0 .. top), top_logprobs[n][0 .. top) = that order's first tokens and their ln p.
+ * logits: device bf16, fp16 or fp32 rows, row_stride elements apart (0: the same row for every
+ * token), aligned to their type.
+ * -inf masks a token (p = 0, and it is no alternative: where fewer than `top` tokens are left the
+ * lists end with -1 and -inf; of a row with every token masked the log probabilities are -inf and
+ * the entropy 0).  Logits must not be NaN or +inf.  scale (1 /
+ * temperature) in [1e-6, 1e6].  Sums in fp32, in an order that depends on the sizes alone.
+ * tokens int32 [N]; a negative one is no token (a padded row): logprob 0, rank -1, the rest as ever.
+ * One of V or more gives NaN and -1 and records MLA_ERR_INDEX in *device_status (optional).
+ * entropy and rank may be NULL; top in [0, 64] (0: the lists may be NULL).  V <= 2^28.  N = 0 is
+ * valid and enqueues nothing. */
+typedef enum { MLA_LOGITS_BF16 = 0, MLA_LOGITS_FP16 = 1, MLA_LOGITS_FP32 = 2 } mla_logits_dtype;
+
+mla_status mla_token_logprobs(const void *logits, mla_logits_dtype dtype, int64_t row_stride, int64_t N, int V,
+                              const int32_t *tokens, float scale, int top, float *logprob, float *entropy,
+                              int32_t *rank, int32_t *top_tokens, float *top_logprobs, int32_t *device_status,
+                              void *stream);
 
 #ifdef __cplusplus
 }

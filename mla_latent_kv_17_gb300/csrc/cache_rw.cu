@@ -127,15 +127,18 @@ __device__ __forceinline__ float2 quotients(uint64_t x, uint64_t neg_s, uint64_t
 // every lane works on a key, and the four angles a lane computes are the ones its pairs need.
 // Interleaved: the pairs of its own values.  Half layout: lanes l and l ^ 4 hold the first and
 // the second values of the same eight pairs; each computes four of their angles.
-// turns: the 32 frequencies (shared memory).
-__device__ __forceinline__ uint4 rotate_key(uint4 key, const uint64_t *turns, int32_t pos, float mscale, int lane,
-                                            bool interleaved) {
-    const int j = interleaved ? 4 * (lane & 7) : 8 * (lane & 3) + (lane & 4);
+// turns: the 32 frequencies (shared memory); pos: where the lane's four angles stand.
+__device__ __forceinline__ int first_angle(int lane, bool interleaved) {
+    return interleaved ? 4 * (lane & 7) : 8 * (lane & 3) + (lane & 4);
+}
+__device__ __forceinline__ uint4 rotate_key(uint4 key, const uint64_t *turns, const int32_t (&pos)[4], float mscale,
+                                            int lane, bool interleaved) {
+    const int j = first_angle(lane, interleaved);
     float k[8];
     unpack8(key, k);
     float2 cs[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = turn(pos, turns[j + i], mscale);
+    for (int i = 0; i < 4; ++i) cs[i] = turn(pos[i], turns[j + i], mscale);
     if (interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -156,6 +159,17 @@ __device__ __forceinline__ uint4 rotate_key(uint4 key, const uint64_t *turns, in
     return pack8(k);
 }
 
+// Positions of a key's pairs: one for all of them (RwArgs), or one per axis and an axis for each pair.
+struct OnePosition {
+    static constexpr bool kAxes = false;
+};
+struct AxisPositions {
+    static constexpr bool kAxes = true;
+    int64_t token_stride, axis_stride;
+    int num_axes;
+    uint8_t axis[kDRope / 2];
+};
+
 struct Latent {
     uint4 v0, v1;  // lane l: channels 16 l .. 16 l + 15
 };
@@ -167,8 +181,10 @@ __device__ __forceinline__ Latent load_latent(const uint16_t *src, int lane) {
 // A warp takes `per` (<= 32) tokens in a row: lane i resolves the cache row of the i-th one, all
 // at once, and the next token's latent is read while the present one is worked on, so that no
 // token waits for the position -> page -> row chain.
-template <bool kFp8, bool kNorm>
-__global__ void __launch_bounds__(32 * kRwWarps, 4) write_kernel(RwArgs a, int per) {
+template <bool kFp8, bool kNorm, typename Positions>
+__global__ void __launch_bounds__(32 * kRwWarps, 4) write_kernel(RwArgs a, int per,
+                                                                 const __grid_constant__ Positions places) {
+    constexpr bool kAxes = Positions::kAxes;
     __shared__ uint64_t s_turns[32];
     grid_dep_wait();
     grid_dep_launch();
@@ -179,10 +195,23 @@ __global__ void __launch_bounds__(32 * kRwWarps, 4) write_kernel(RwArgs a, int p
     Latent next{};
     if (cnt > 0) next = load_latent(rows, lane);
     int64_t row_l = -1;
-    int32_t at_l = 0;
+    int32_t at_l[kAxes ? kMaxAxes : 1] = {};  // the lane's token's place on each axis
     if (lane < cnt) {
         row_l = cache_row(a, n0 + lane);
-        if (a.freqs) at_l = (a.rope_positions ? a.rope_positions : a.positions)[n0 + lane];
+        if constexpr (kAxes) {
+#pragma unroll
+            for (int x = 0; x < kMaxAxes; ++x)
+                if (x < places.num_axes)
+                    at_l[x] = a.rope_positions[(n0 + lane) * places.token_stride + x * places.axis_stride];
+        } else {
+            if (a.freqs) at_l[0] = (a.rope_positions ? a.rope_positions : a.positions)[n0 + lane];
+        }
+    }
+    uint32_t axis4 = 0;  // the axes of the lane's four angles, a byte each
+    if constexpr (kAxes) {
+        const int j = first_angle(lane, a.interleaved != 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) axis4 |= (uint32_t)places.axis[j + k] << 8 * k;
     }
     const int64_t row_bytes = kFp8 ? kFp8RecordBytes : kDEntry * 2;
     if (a.freqs) {  // the same for the whole grid
@@ -196,7 +225,17 @@ __global__ void __launch_bounds__(32 * kRwWarps, 4) write_kernel(RwArgs a, int p
             uint4 key = make_uint4(0u, 0u, 0u, 0u);
             if (i < cnt) key = reinterpret_cast<const uint4 *>(rows + i * a.stride + kDLatent)[lane & 7];
             const int64_t row = __shfl_sync(kAll, row_l, i & 31);
-            if (a.freqs) key = rotate_key(key, s_turns, __shfl_sync(kAll, at_l, i & 31), a.mscale, lane, a.interleaved != 0);
+            if (a.freqs) {
+                int32_t pos[4];
+#pragma unroll
+                for (int x = 0; x < (kAxes ? kMaxAxes : 1); ++x) {
+                    const int32_t p = __shfl_sync(kAll, at_l[x], i & 31);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (x == 0 || (axis4 >> 8 * k & 0xFFu) == (uint32_t)x) pos[k] = p;
+                }
+                key = rotate_key(key, s_turns, pos, a.mscale, lane, a.interleaved != 0);
+            }
             if (i < cnt && row >= 0)
                 reinterpret_cast<uint4 *>(a.cache + row * row_bytes + (kFp8 ? kDLatent + 16 : kDLatent * 2))[lane & 7] = key;
         }
@@ -325,14 +364,15 @@ __global__ void __launch_bounds__(32 * kRwWarps, 8) read_kernel(RwArgs a) {
 
 // Tokens per warp: one while that still gives every SM at most `warps` warps, then as many as
 // keep them busy, up to `most`.
-template <typename K>
-mla_status launch_rw(K kernel, const RwArgs &a, int warps, int most, void *stream) {
+template <typename K, typename Positions>
+mla_status launch_rw(K kernel, const RwArgs &a, const Positions &places, int warps, int most, void *stream) {
     const int64_t want = (a.N + kSms * warps - 1) / (kSms * warps);
     const int per = (int)(want < 1 ? 1 : want > most ? most : want);
     const int64_t ctas = (a.N + (int64_t)per * kRwWarps - 1) / ((int64_t)per * kRwWarps);
     if (ctas > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
-    return launch_pdl(kernel, (int)ctas, 32 * kRwWarps, 0, (cudaStream_t)stream, a, per) == cudaSuccess ? MLA_OK
-                                                                                                       : MLA_ERR_CUDA;
+    return launch_pdl(kernel, (int)ctas, 32 * kRwWarps, 0, (cudaStream_t)stream, a, per, places) == cudaSuccess
+               ? MLA_OK
+               : MLA_ERR_CUDA;
 }
 
 // Arguments the write and the read share; fills `a` with them (where there are tokens).
@@ -366,17 +406,13 @@ mla_status check_rw(RwArgs *a, const void *cache, mla_kv_dtype kv_dtype, int64_t
     return MLA_OK;
 }
 
-}  // namespace
-}  // namespace mla
-
-using namespace mla;
-
-extern "C" mla_status mla_cache_write(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages,
-                                      const int32_t *block_table, int num_requests, int max_pages,
-                                      const int32_t *requests, const int32_t *positions, const void *kv,
-                                      int64_t kv_stride, int64_t N, const void *norm_weight, float norm_eps,
-                                      const double *freqs, const int32_t *rope_positions, mla_rope_layout layout,
-                                      float mscale, int32_t *device_status, void *stream) {
+// Checks a write's arguments and launches it.
+template <typename Positions>
+mla_status run_write(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages, const int32_t *block_table, int num_requests,
+                     int max_pages, const int32_t *requests, const int32_t *positions, const void *kv, int64_t kv_stride,
+                     int64_t N, const void *norm_weight, float norm_eps, const double *freqs,
+                     const int32_t *rope_positions, const Positions &places, mla_rope_layout layout, float mscale,
+                     int32_t *device_status, void *stream) {
     RwArgs a;
     const mla_status st = check_rw(&a, cache, kv_dtype, num_pages, block_table, num_requests, max_pages, requests,
                                    positions, kv, kv_stride, N, device_status);
@@ -392,9 +428,44 @@ extern "C" mla_status mla_cache_write(void *cache, mla_kv_dtype kv_dtype, int64_
     a.interleaved = layout == MLA_ROPE_INTERLEAVED;
     a.mscale = mscale;
     const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
-    const auto kernel = norm_weight ? (fp8 ? write_kernel<true, true> : write_kernel<false, true>)
-                                    : (fp8 ? write_kernel<true, false> : write_kernel<false, false>);
-    return launch_rw(kernel, a, kWriteWarps, kWriteMost, stream);
+    const auto kernel = norm_weight ? (fp8 ? write_kernel<true, true, Positions> : write_kernel<false, true, Positions>)
+                                    : (fp8 ? write_kernel<true, false, Positions> : write_kernel<false, false, Positions>);
+    return launch_rw(kernel, a, places, kWriteWarps, kWriteMost, stream);
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_cache_write(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages,
+                                      const int32_t *block_table, int num_requests, int max_pages,
+                                      const int32_t *requests, const int32_t *positions, const void *kv,
+                                      int64_t kv_stride, int64_t N, const void *norm_weight, float norm_eps,
+                                      const double *freqs, const int32_t *rope_positions, mla_rope_layout layout,
+                                      float mscale, int32_t *device_status, void *stream) {
+    return run_write(cache, kv_dtype, num_pages, block_table, num_requests, max_pages, requests, positions, kv, kv_stride,
+                     N, norm_weight, norm_eps, freqs, rope_positions, OnePosition{}, layout, mscale, device_status, stream);
+}
+
+extern "C" mla_status mla_cache_write_axes(void *cache, mla_kv_dtype kv_dtype, int64_t num_pages,
+                                           const int32_t *block_table, int num_requests, int max_pages,
+                                           const int32_t *requests, const int32_t *positions, const void *kv,
+                                           int64_t kv_stride, int64_t N, const void *norm_weight, float norm_eps,
+                                           const double *freqs, const int32_t *rope_positions,
+                                           int64_t position_token_stride, int64_t position_axis_stride, int num_axes,
+                                           const uint8_t *axes, mla_rope_layout layout, float mscale,
+                                           int32_t *device_status, void *stream) {
+    if (num_axes < 1 || !axes) return MLA_ERR_INVALID_ARG;
+    if (num_axes > kMaxAxes) return MLA_ERR_UNSUPPORTED;
+    if (N > 0 && (!freqs || !rope_positions)) return MLA_ERR_INVALID_ARG;
+    AxisPositions places;
+    places.token_stride = position_token_stride;
+    places.axis_stride = position_axis_stride;
+    places.num_axes = num_axes;
+    if (!copy_axes(places.axis, axes, kDRope / 2, num_axes)) return MLA_ERR_INVALID_ARG;
+    return run_write(cache, kv_dtype, num_pages, block_table, num_requests, max_pages, requests, positions, kv, kv_stride,
+                     N, norm_weight, norm_eps, freqs, rope_positions, places, layout, mscale, device_status, stream);
 }
 
 extern "C" mla_status mla_cache_read(const void *cache, mla_kv_dtype kv_dtype, int64_t num_pages,

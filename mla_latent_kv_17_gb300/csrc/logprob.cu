@@ -1,0 +1,443 @@
+// Log probabilities of given tokens, with their ranks, the rows' entropies and the best
+// alternatives.  The definition is in include/mla_decode.h (mla_token_logprobs).
+//
+// One pass over a row.  With c = scale log2 e and a reference m, the maximum of xc so far, a thread keeps s = sum 2^(xc - m) and w = sum 2^(xc - m) (xc - m) of its
+// share; when the reference moves by d = m - m', s becomes 2^d s and w becomes 2^d (w + d s).  Then
+//   log p(x) = ln 2 (xc - m - log2 s),   H = ln 2 (log2 s - w / s):
+// both terms of H are >= 0, so nothing cancels.  Sums and references are fp32.
+//
+// The best alternatives come out of the same pass: a thread's share of the row is a stripe of 16-byte
+// units, and it keeps the stripe's maximum.  The k-th largest of those maxima is a lower bound of
+// the k-th best logit, and only stripes that reach it - about k of them - are read again (from L2),
+// a warp per stripe, for the tokens that reach it.  Rows where more than kCandidates do (many equal
+// logits) take one pass for each alternative instead.
+//
+// A CTA takes a row; with few rows a cluster of up to eight CTAs shares one, its parts joined through
+// distributed shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "sm103_ptx.cuh"
+#include "tc_util.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpBatch = 4;         // 16-byte units of a thread in flight together
+constexpr int kLpMaxTop = 64;
+constexpr int kCandidates = 1024;   // at least kLpMaxTop units' values
+constexpr int kLpMaxCluster = 8;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct LogprobArgs {
+    const void *logits;
+    int64_t row_stride;  // in elements
+    int V, parts;        // parts: CTAs per row
+    const int32_t *tokens;
+    float scale, scale_log2;
+    int top;
+    float *logprob, *entropy;
+    int32_t *rank, *top_tokens;
+    float *top_logprobs;
+    int *status;
+};
+
+struct Bf16 {
+    using Raw = uint16_t;
+    static constexpr int kUnit = 8;
+    static constexpr uint32_t kMinusInf = 0xFF80FF80u;
+    static __device__ __forceinline__ float value(Raw r) { return bf16_to_f32(r); }
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
+struct Fp16 {
+    using Raw = uint16_t;
+    static constexpr int kUnit = 8;
+    static constexpr uint32_t kMinusInf = 0xFC00FC00u;
+    static __device__ __forceinline__ float value(Raw r) { return __half2float(__ushort_as_half(r)); }
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu)));
+            f[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+        }
+    }
+};
+struct Fp32 {
+    using Raw = float;
+    static constexpr int kUnit = 4;
+    static constexpr uint32_t kMinusInf = 0xFF800000u;
+    static __device__ __forceinline__ float value(Raw r) { return r; }
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+};
+
+// A row as 16-byte units: unit u holds tokens first + u * kUnit ... (the first and the last unit may
+// reach over the row's ends; what lies there is not read and counts as -inf).
+template <typename T>
+struct Row {
+    const typename T::Raw *p;
+    int first, V, units;
+
+    __device__ __forceinline__ Row(const typename T::Raw *row, int v) : p(row), V(v) {
+        const int past = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(typename T::Raw));
+        first = -past;
+        units = (int)(((int64_t)v + past + T::kUnit - 1) / T::kUnit);
+    }
+    __device__ __forceinline__ int token(int u) const { return first + u * T::kUnit; }
+    __device__ __forceinline__ uint4 load(int u) const {
+        const int e = token(u);
+        if (e >= 0 && e <= V - T::kUnit) return *reinterpret_cast<const uint4 *>(p + e);
+        uint4 v = make_uint4(T::kMinusInf, T::kMinusInf, T::kMinusInf, T::kMinusInf);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < T::kUnit; ++i) {
+            if (e + i < 0 || e + i >= V) continue;
+            if constexpr (sizeof(typename T::Raw) == 4) {
+                w[i] = __float_as_uint(p[e + i]);
+            } else {
+                const uint32_t r = p[e + i];
+                w[i / 2] = i % 2 ? (w[i / 2] & 0xFFFFu) | r << 16 : (w[i / 2] & 0xFFFF0000u) | r;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Whole numbers in the order of the floats (-0 as +0), above 0 for every float but -inf and below.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+// A token's place among the alternatives: larger logits first, then lower tokens.
+__device__ __forceinline__ uint64_t place_key(float x, int token) {
+    return (uint64_t)ordered(x) << 32 | (uint32_t)~token;
+}
+
+struct Part {
+    float m, s, w;  // the largest logit (-inf: nothing yet), sums
+    int ahead;      // tokens before the given one in the order of place_key
+};
+
+// Two parts' sums under the larger of their maxima; c = scale log2 e.
+__device__ __forceinline__ Part join(const Part &a, const Part &b, float c) {
+    Part r;
+    r.ahead = a.ahead + b.ahead;
+    r.m = fmaxf(a.m, b.m);
+    if (r.m == -INFINITY) {
+        r.s = r.w = 0.f;
+        return r;
+    }
+    const float da = fmaxf((a.m - r.m) * c, -200.f), db = fmaxf((b.m - r.m) * c, -200.f);  // (2^-200: 0 in fp32)
+    const float fa = ptx::ex2_approx(da), fb = ptx::ex2_approx(db);
+    r.s = a.s * fa + b.s * fb;
+    r.w = fa * (a.w + a.s * da) + fb * (b.w + b.s * db);
+    return r;
+}
+
+struct Shared {
+    Part warp[kLpWarps];
+    Part cta;                       // read by the cluster's first CTA
+    uint32_t stripe[kLpThreads];    // each stripe's maximum, as ordered()
+    uint32_t limit;
+    int stripes, candidates;
+    int listed[kLpThreads];         // stripes that reach the limit
+    uint64_t key[kCandidates];
+    uint64_t best[kLpMaxTop];       // this CTA's alternatives in order (0: none); read by the first CTA
+    uint64_t warp_key[kLpWarps];
+};
+
+// Puts the `top` largest of the n keys (all different) into best, in order; 0 where there are fewer.
+__device__ __forceinline__ void pick(const uint64_t *key, int n, uint64_t *best, int top) {
+    for (int i = threadIdx.x; i < top; i += kLpThreads)
+        if (i >= n) best[i] = 0;
+    for (int i = threadIdx.x; i < n; i += kLpThreads) {
+        const uint64_t k = key[i];
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += key[j] > k;
+        if (r < top) best[r] = k;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(LogprobArgs a) {
+    __shared__ Shared sh;
+    grid_dep_wait();
+    grid_dep_launch();
+    constexpr int E = T::kUnit;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int parts = a.parts, part = blockIdx.x % parts;  // a row's CTAs are one cluster
+    const int64_t n = blockIdx.x / parts;
+    const Row<T> row(reinterpret_cast<const typename T::Raw *>(a.logits) + n * a.row_stride, a.V);
+    const int per = (row.units + parts - 1) / parts;
+    const int u0 = part * per, u1 = min(row.units, u0 + per);
+    const float c = a.scale_log2;
+    const int token = a.tokens[n];
+    const bool given = token >= 0 && token < a.V;
+    const float mine = given ? T::value(row.p[token]) : INFINITY;
+    const bool masked = mine == -INFINITY;  // all tokens below it are ahead, and those above it that are not masked
+
+    // ---- the pass
+    Part t{-INFINITY, 0.f, 0.f, 0};
+    float top = -INFINITY;  // the stripe's largest logit
+    for (int u = u0 + tid; u < u1; u += kLpBatch * kLpThreads) {
+        uint4 v[kLpBatch];
+#pragma unroll
+        for (int q = 0; q < kLpBatch; ++q) {
+            v[q] = make_uint4(T::kMinusInf, T::kMinusInf, T::kMinusInf, T::kMinusInf);
+            if (u + q * kLpThreads < u1) v[q] = row.load(u + q * kLpThreads);
+        }
+        float f[kLpBatch][E], most = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kLpBatch; ++q) {
+            T::unpack(v[q], f[q]);
+#pragma unroll
+            for (int i = 0; i < E; ++i) most = fmaxf(most, f[q][i]);
+        }
+        top = fmaxf(top, most);
+        if (most == -INFINITY) continue;  // all masked
+        const float m = fmaxf(t.m, most), d = fmaxf((t.m - m) * c, -200.f), g = ptx::ex2_approx(d);
+        t.w = g * (t.w + d * t.s);
+        t.s *= g;
+        t.m = m;
+#pragma unroll
+        for (int q = 0; q < kLpBatch; ++q) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float x = fmaxf((f[q][i] - t.m) * c, -200.f);
+                const float p = ptx::ex2_approx(x);
+                t.s += p;
+                t.w = fmaf(p, x, t.w);
+            }
+        }
+        if (most >= mine) {
+#pragma unroll
+            for (int q = 0; q < kLpBatch; ++q) {
+                const int e = row.token(u + q * kLpThreads);
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    t.ahead += masked ? f[q][i] > mine && e + i > token
+                                      : f[q][i] > mine || (f[q][i] == mine && e + i < token);
+            }
+        }
+    }
+    sh.stripe[tid] = ordered(top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Part b;
+        b.m = __shfl_xor_sync(kFull, t.m, o);
+        b.s = __shfl_xor_sync(kFull, t.s, o);
+        b.w = __shfl_xor_sync(kFull, t.w, o);
+        b.ahead = __shfl_xor_sync(kFull, t.ahead, o);
+        t = join(t, b, c);
+    }
+    if (lane == 0) sh.warp[warp] = t;
+    if (tid == 0) sh.stripes = sh.candidates = 0;
+    __syncthreads();
+    if (tid == 32) {
+        Part r = sh.warp[0];
+        for (int i = 1; i < kLpWarps; ++i) r = join(r, sh.warp[i], c);
+        sh.cta = r;
+    }
+
+    // ---- this CTA's alternatives
+    if (a.top > 0) {
+        if (warp == 0) {
+            // the largest limit that `top` stripes reach, to 16 bits (rounded down)
+            uint32_t k[kLpThreads / 32], limit = 0;
+#pragma unroll
+            for (int i = 0; i < kLpThreads / 32; ++i) k[i] = sh.stripe[lane + 32 * i];
+            for (int bit = 31; bit >= 16; --bit) {
+                const uint32_t l = limit | 1u << bit;
+                int cnt = 0;
+#pragma unroll
+                for (int i = 0; i < kLpThreads / 32; ++i) cnt += k[i] >= l;
+                if (__reduce_add_sync(kFull, cnt) >= a.top) limit = l;
+            }
+            if (lane == 0) sh.limit = max(limit, ordered(-INFINITY) + 1);  // masked tokens are none
+        }
+        __syncthreads();
+        const uint32_t limit = sh.limit;
+        if (sh.stripe[tid] >= limit) sh.listed[atomicAdd(&sh.stripes, 1)] = tid;
+        __syncthreads();
+        const int stripes = sh.stripes;
+        for (int i = warp; i < stripes; i += kLpWarps) {
+            for (int u = u0 + sh.listed[i] + lane * kLpThreads; u < u1; u += 32 * kLpThreads) {
+                float f[E];
+                T::unpack(row.load(u), f);
+                const int e = row.token(u);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    if (ordered(f[j]) >= limit) {
+                        const int at = atomicAdd(&sh.candidates, 1);
+                        if (at < kCandidates) sh.key[at] = place_key(f[j], e + j);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int found = sh.candidates;
+        if (found <= kCandidates) {
+            pick(sh.key, found, sh.best, a.top);
+        } else {
+            // one after the other: the largest key below the last one
+            uint64_t last = ~0ull;
+            for (int k = 0; k < a.top; ++k) {
+                uint64_t mx = 0;
+                for (int u = u0 + tid; u < u1; u += kLpThreads) {
+                    float f[E];
+                    T::unpack(row.load(u), f);
+                    const int e = row.token(u);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        const uint64_t key = place_key(f[j], e + j);
+                        if (key < last && key > mx && ordered(f[j]) >= limit) mx = key;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(kFull, mx, o));
+                if (lane == 0) sh.warp_key[warp] = mx;
+                __syncthreads();
+                for (int i = 0; i < kLpWarps; ++i) mx = max(mx, sh.warp_key[i]);
+                if (tid == 0) sh.best[k] = mx;
+                last = mx;
+                __syncthreads();
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- the row's
+    const uint64_t *best = sh.best;
+    Part r = sh.cta;
+    if (parts > 1) {
+        ptx::cluster_sync();
+        if (part == 0) {
+            const uint32_t here = ptx::smem_u32(&sh);
+            auto peer = [&](int rank, const void *at) {
+                return ptx::mapa(here + (uint32_t)(reinterpret_cast<const char *>(at) - reinterpret_cast<const char *>(&sh)), rank);
+            };
+            auto ld32 = [](uint32_t at) {
+                uint32_t x;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+                return x;
+            };
+            auto ld64 = [](uint32_t at) {
+                uint64_t x;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
+                return x;
+            };
+            for (int q = 1; q < parts; ++q) {
+                const uint32_t at = peer(q, &sh.cta);
+                r = join(r, Part{__uint_as_float(ld32(at)), __uint_as_float(ld32(at + 4)), __uint_as_float(ld32(at + 8)),
+                                 (int)ld32(at + 12)}, c);
+            }
+            if (a.top > 0) {
+                // (the candidates' places are free by now)
+                if (tid == 0) sh.candidates = 0;
+                __syncthreads();
+                for (int i = tid; i < parts * a.top; i += kLpThreads) {
+                    const uint64_t k = ld64(peer(i / a.top, &sh.best[i % a.top]));
+                    if (k) sh.key[atomicAdd(&sh.candidates, 1)] = k;
+                }
+                __syncthreads();
+                pick(sh.key, sh.candidates, sh.best, a.top);
+                __syncthreads();
+            }
+        }
+        ptx::cluster_sync();  // the first CTA has read the others' memory
+        if (part != 0) return;
+    }
+    const float log_s = log2f(r.s) * kLn2;
+    const bool none = r.m == -INFINITY;  // every token masked
+    if (tid == 0) {
+        const float y = none || masked ? -INFINITY : (mine - r.m) * a.scale - log_s;
+        a.logprob[n] = given ? y : token < 0 ? 0.f : NAN;
+        if (a.entropy) a.entropy[n] = none ? 0.f : log_s - r.w / r.s * kLn2;
+        if (a.rank) a.rank[n] = given ? r.ahead + (masked ? token : 0) : -1;
+        if (token >= a.V && a.status) record_error(a.status, MLA_ERR_INDEX);
+    }
+    for (int i = tid; i < a.top; i += kLpThreads) {
+        const uint64_t k = best[i];
+        a.top_tokens[n * a.top + i] = k ? (int32_t)~(uint32_t)k : -1;
+        a.top_logprobs[n * a.top + i] = k ? (unordered((uint32_t)(k >> 32)) - r.m) * a.scale - log_s : -INFINITY;
+    }
+}
+
+template <typename T>
+mla_status launch_logprobs(LogprobArgs a, int64_t N, cudaStream_t stream) {
+    // CTAs per row: as many as the SMs take at once while each still has a batch of units a thread
+    const int64_t units = ((int64_t)a.V + T::kUnit - 1) / T::kUnit;
+    int parts = 1;
+    while (parts < kLpMaxCluster && N * parts * 2 <= 304 && units >= 2 * parts * kLpThreads * kLpBatch) parts *= 2;
+    a.parts = parts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(N * parts), 1, 1);
+    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = parts;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = parts > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, logprob_kernel<T>, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_token_logprobs(const void *logits, mla_logits_dtype dtype, int64_t row_stride, int64_t N, int V,
+                                         const int32_t *tokens, float scale, int top, float *logprob, float *entropy,
+                                         int32_t *rank, int32_t *top_tokens, float *top_logprobs,
+                                         int32_t *device_status, void *stream) {
+    if (dtype != MLA_LOGITS_BF16 && dtype != MLA_LOGITS_FP16 && dtype != MLA_LOGITS_FP32) return MLA_ERR_INVALID_ARG;
+    if (N < 0 || V < 1 || top < 0 || row_stride < 0) return MLA_ERR_INVALID_ARG;
+    if (!(scale >= 1e-6f && scale <= 1e6f)) return MLA_ERR_INVALID_ARG;
+    if (top > kLpMaxTop || V > (1 << 28) || N > (int64_t)1 << 30) return MLA_ERR_UNSUPPORTED;
+    if (N == 0) return MLA_OK;
+    if (!logits || !tokens || !logprob || (top > 0 && (!top_tokens || !top_logprobs))) return MLA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == MLA_LOGITS_FP32 ? 4 : 2)) return MLA_ERR_INVALID_ARG;
+    LogprobArgs a;
+    a.logits = logits;
+    a.row_stride = row_stride;
+    a.V = V;
+    a.tokens = tokens;
+    a.scale = scale;
+    a.scale_log2 = scale * kLog2e;
+    a.top = top;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.rank = rank;
+    a.top_tokens = top_tokens;
+    a.top_logprobs = top_logprobs;
+    a.status = (int *)device_status;
+    cudaStream_t s = (cudaStream_t)stream;
+    return dtype == MLA_LOGITS_BF16   ? launch_logprobs<Bf16>(a, N, s)
+           : dtype == MLA_LOGITS_FP16 ? launch_logprobs<Fp16>(a, N, s)
+                                      : launch_logprobs<Fp32>(a, N, s);
+}

@@ -24,6 +24,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeRows = 4;                // rows per thread, in flight together
 constexpr int kRopeCtas = 3;                // CTAs per SM (registers)
 constexpr int kRopeTableBytes = 16 * 1024;  // shared memory for the CTA's (cos, sin) pairs, at most
+constexpr int kMaxAxisPairs = 256;          // pairs of a head with several axes (their axes are a kernel parameter)
 
 struct RopeArgs {
     const uint16_t *x;
@@ -32,13 +33,24 @@ struct RopeArgs {
     int64_t p_ts, p_hs;
     uint16_t *out_rot;
     int64_t r_ts, r_hs;
-    const int32_t *positions;
     const double *freqs;
     float mscale;
     int64_t N;
     int H, d_pass, d_rot, interleaved;
     int tokens;  // tokens per CTA
     int heads;   // heads per CTA (all of them when tokens > 1)
+};
+
+// Where a token stands: one position for all pairs, or one per axis and an axis for each pair.
+struct OnePosition {
+    const int32_t *p;
+    __device__ __forceinline__ int32_t at(int64_t n, int) const { return p[n]; }
+};
+struct AxisPositions {
+    const int32_t *p;
+    int64_t token_stride, axis_stride;
+    uint8_t axis[kMaxAxisPairs];
+    __device__ __forceinline__ int32_t at(int64_t n, int pair) const { return p[n * token_stride + axis[pair] * axis_stride]; }
 };
 
 template <int kVec>
@@ -100,8 +112,8 @@ __device__ __forceinline__ void rotate(Vec<kVec> &va, Vec<kVec> &vb, const float
 }
 
 // kOne: the CTA's rows are heads of one token (rows at a fixed distance, no division).
-template <int kVec, bool kOne>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeArgs a) {
+template <int kVec, bool kOne, typename Positions>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeArgs a, const __grid_constant__ Positions pos) {
     extern __shared__ float2 s_cs[];  // [tokens][d_rot / 2]
     grid_dep_wait();
     grid_dep_launch();
@@ -137,8 +149,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeArgs 
             }
             if (first) {
                 for (int i = tid; i < nt * half; i += nthreads) {
-                    const int t = kOne ? 0 : i / half;
-                    s_cs[i] = turn(a.positions[n0 + t], turns_fixed(a.freqs[i - t * half]), a.mscale);
+                    const int t = kOne ? 0 : i / half, p = i - t * half;
+                    s_cs[i] = turn(pos.at(n0 + t, p), turns_fixed(a.freqs[p]), a.mscale);
                 }
                 __syncthreads();
                 first = false;
@@ -161,8 +173,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeArgs 
     }
 }
 
-template <int kVec>
-mla_status launch_rope(RopeArgs a, cudaStream_t stream) {
+template <int kVec, typename Positions>
+mla_status launch_rope(RopeArgs a, const Positions &pos, cudaStream_t stream) {
     const int units = (a.out_pass ? (a.d_pass / kVec + 1) / 2 : 0) + a.d_rot / 2 / kVec;
     const int bx = units < kRopeThreads ? units : kRopeThreads;
     int by = 1;  // a power of two, like most head counts
@@ -192,21 +204,19 @@ mla_status launch_rope(RopeArgs a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, a.tokens == 1 ? rope_kernel<kVec, true> : rope_kernel<kVec, false>, a) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, a.tokens == 1 ? rope_kernel<kVec, true, Positions> : rope_kernel<kVec, false, Positions>,
+                              a, pos) == cudaSuccess
                ? MLA_OK
                : MLA_ERR_CUDA;
 }
 
-}  // namespace
-}  // namespace mla
+// Checks the arguments that do not depend on where the positions stand, and launches.
+template <typename Positions>
+mla_status run_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t N, int H, int d_pass, int d_rot,
+                    mla_rope_layout layout, const Positions &pos, const double *freqs, float mscale, void *out_pass,
+                    int64_t pass_token_stride, int64_t pass_head_stride, void *out_rot, int64_t rot_token_stride,
+                    int64_t rot_head_stride, void *stream) {
 
-using namespace mla;
-
-extern "C" mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t N, int H,
-                               int d_pass, int d_rot, mla_rope_layout layout, const int32_t *positions,
-                               const double *freqs, float mscale, void *out_pass, int64_t pass_token_stride,
-                               int64_t pass_head_stride, void *out_rot, int64_t rot_token_stride,
-                               int64_t rot_head_stride, void *stream) {
     if (N < 0 || H < 1 || d_pass < 0 || d_rot < 2 || d_rot % 2 != 0) return MLA_ERR_INVALID_ARG;
     if (layout != MLA_ROPE_INTERLEAVED && layout != MLA_ROPE_HALF) return MLA_ERR_INVALID_ARG;
     if (!isfinite(mscale)) return MLA_ERR_INVALID_ARG;
@@ -214,7 +224,7 @@ extern "C" mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_
     if (N == 0) return MLA_OK;
     if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out_rot) | reinterpret_cast<uintptr_t>(out_pass)) % 2)
         return MLA_ERR_INVALID_ARG;  // no bf16 values
-    if (!x || !positions || !freqs || !out_rot) return MLA_ERR_INVALID_ARG;
+    if (!x || !pos.p || !freqs || !out_rot) return MLA_ERR_INVALID_ARG;
     RopeArgs a;
     a.x = (const uint16_t *)x;
     a.x_ts = x_token_stride;
@@ -225,7 +235,6 @@ extern "C" mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_
     a.out_rot = (uint16_t *)out_rot;
     a.r_ts = rot_token_stride;
     a.r_hs = rot_head_stride;
-    a.positions = positions;
     a.freqs = freqs;
     a.mscale = mscale;
     a.N = N;
@@ -239,5 +248,36 @@ extern "C" mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_
     bool vec = aligned16(x) && aligned16(out_rot) && d_pass % 8 == 0 && d_rot % 16 == 0 &&
                (x_token_stride | x_head_stride | rot_token_stride | rot_head_stride) % 8 == 0;
     if (a.out_pass) vec = vec && aligned16(out_pass) && (pass_token_stride | pass_head_stride) % 8 == 0;
-    return vec ? launch_rope<8>(a, (cudaStream_t)stream) : launch_rope<1>(a, (cudaStream_t)stream);
+    return vec ? launch_rope<8>(a, pos, (cudaStream_t)stream) : launch_rope<1>(a, pos, (cudaStream_t)stream);
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t N, int H,
+                               int d_pass, int d_rot, mla_rope_layout layout, const int32_t *positions,
+                               const double *freqs, float mscale, void *out_pass, int64_t pass_token_stride,
+                               int64_t pass_head_stride, void *out_rot, int64_t rot_token_stride,
+                               int64_t rot_head_stride, void *stream) {
+    return run_rope(x, x_token_stride, x_head_stride, N, H, d_pass, d_rot, layout, OnePosition{positions}, freqs, mscale,
+                    out_pass, pass_token_stride, pass_head_stride, out_rot, rot_token_stride, rot_head_stride, stream);
+}
+
+extern "C" mla_status mla_rope_axes(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t N, int H,
+                                    int d_pass, int d_rot, mla_rope_layout layout, const int32_t *positions,
+                                    int64_t position_token_stride, int64_t position_axis_stride, int num_axes,
+                                    const uint8_t *axes, const double *freqs, float mscale, void *out_pass,
+                                    int64_t pass_token_stride, int64_t pass_head_stride, void *out_rot,
+                                    int64_t rot_token_stride, int64_t rot_head_stride, void *stream) {
+    if (d_rot < 2 || num_axes < 1 || !axes) return MLA_ERR_INVALID_ARG;
+    if (num_axes > kMaxAxes || d_rot / 2 > kMaxAxisPairs) return MLA_ERR_UNSUPPORTED;
+    AxisPositions pos;
+    pos.p = positions;
+    pos.token_stride = position_token_stride;
+    pos.axis_stride = position_axis_stride;
+    if (!copy_axes(pos.axis, axes, d_rot / 2, num_axes)) return MLA_ERR_INVALID_ARG;
+    return run_rope(x, x_token_stride, x_head_stride, N, H, d_pass, d_rot, layout, pos, freqs, mscale, out_pass,
+                    pass_token_stride, pass_head_stride, out_rot, rot_token_stride, rot_head_stride, stream);
 }

@@ -33,4 +33,15 @@ __device__ __forceinline__ float2 turn(int32_t pos, uint64_t turns, float mscale
     return make_float2(c * mscale, s * mscale);
 }
 
+constexpr int kMaxAxes = 4;  // axes of a position (time, height, width and one more)
+
+// The axes of a head's pairs, from the caller's host array; false where one of them does not exist.
+inline bool copy_axes(uint8_t *to, const uint8_t *axes, int pairs, int num_axes) {
+    for (int j = 0; j < pairs; ++j) {
+        if (axes[j] >= num_axes) return false;
+        to[j] = axes[j];
+    }
+    return true;
+}
+
 }  // namespace mla

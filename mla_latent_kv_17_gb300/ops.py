@@ -72,6 +72,11 @@ def lib():
             L.mla_project_output.restype = I
             L.mla_rope.argtypes = [P, I64, I64, I64, I, I, I, I, P, P, F, P, I64, I64, P, I64, I64, P]
             L.mla_rope.restype = I
+            L.mla_rope_axes.argtypes = [P, I64, I64, I64, I, I, I, I, P, I64, I64, I, P, P, F, P, I64, I64, P, I64, I64, P]
+            L.mla_rope_axes.restype = I
+            L.mla_cache_write_axes.argtypes = [P, I, I64, P, I, I, P, P, P, I64, I64, P, F, P, P, I64, I64, I, P, I, F, P,
+                                               P]
+            L.mla_cache_write_axes.restype = I
             L.mla_cache_write.argtypes = [P, I, I64, P, I, I, P, P, P, I64, I64, P, F, P, P, I, F, P, P]
             L.mla_cache_write.restype = I
             L.mla_cache_read.argtypes = [P, I, I64, P, I, I, P, P, I64, P, I64, P, P]
@@ -86,6 +91,8 @@ def lib():
             L.mla_decode_tree.restype = I
             L.mla_verify_draft.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P, P]
             L.mla_verify_draft.restype = I
+            L.mla_token_logprobs.argtypes = [P, I, I64, I64, I, P, F, I, P, P, P, P, P, P, P]
+            L.mla_token_logprobs.restype = I
             L.mla_decode_status.argtypes = [P, SZ, P]
             L.mla_decode_status.restype = I
             L.mla_decode_inject_stall.argtypes = [I]
@@ -532,12 +539,38 @@ def rope_frequencies(d_rot: int = 64, base: float = 10000.0, scaling: str = "non
     return f.to(device if device is not None else "cuda"), mscale
 
 
+def rope_axes(sections, order: str = "blocks") -> bytes:
+    """The axis of each pair of a rotated part, for rope() and cache_write() of tokens with a position per
+    axis: sections[x] pairs turn by axis x (time, height, width, ...; 1 to 4 axes, len(freqs) pairs in
+    all).  order 'blocks': one axis's pairs after the other's; 'interleaved': a pair of each axis in turn
+    as long as the axis has pairs left."""
+    counts = [int(n) for n in sections]
+    if not 1 <= len(counts) <= 4 or any(n != m or n < 0 for n, m in zip(counts, sections)) or sum(counts) < 1:
+        raise ValueError("sections must be 1 to 4 whole numbers of pairs, not all of them 0")
+    if order == "blocks":
+        return bytes(x for x, n in enumerate(counts) for _ in range(n))
+    if order == "interleaved":
+        return bytes(x for i in range(max(counts)) for x, n in enumerate(counts) if i < n)
+    raise ValueError(f"order must be 'blocks' or 'interleaved', not {order!r}")
+
+
+def _axis_places(positions, axes, N, pairs, name):
+    """The number of axes after checks of positions [N,A] and of the pairs' axes."""
+    if type(axes) is not bytes or len(axes) != pairs:
+        raise ValueError(f"axes must be the bytes that rope_axes gives, of {pairs} pairs")
+    if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] != N or positions.shape[1] < 1:
+        raise ValueError(f"{name} must be int32 [{N},axes]")
+    return positions.shape[1]
+
+
 def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pass=None, out_rot=None,
-         copy_pass: bool = True, stream=None):
+         copy_pass: bool = True, stream=None, axes=None):
     """Rotary positions of the last 2 len(freqs) values of every head: x bf16 [N,H,D] (rows of any
     stride, values adjacent), positions int32 [N], freqs float64 -> (x[..., :D-d] copied, the rotated
     part), bf16 [N,H,D-d] and [N,H,d]; None for the first part where it is empty or copy_pass=False
-    leaves it out.  out_rot may be x[..., D-d:] itself (rotation in place)."""
+    leaves it out.  out_rot may be x[..., D-d:] itself (rotation in place).  With axes (from rope_axes)
+    a token has a position per axis, positions int32 [N,A] (any strides), and pair j turns by that of
+    axes[j]."""
     if x.dtype != torch.bfloat16 or x.dim() != 3:
         raise ValueError("x must be bf16 [N,H,D]")
     N, H, D = x.shape
@@ -546,7 +579,10 @@ def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pas
     if d_rot < 2 or d_pass < 0:
         raise ValueError(f"x has {D} values per head, freqs turns {d_rot}")
     dev = _device_of("x positions freqs out_pass out_rot", x, positions, freqs, out_pass, out_rot)
-    _ints(positions, (N,), "positions")
+    if axes is None:
+        _ints(positions, (N,), "positions")
+    else:
+        num_axes = _axis_places(positions, axes, N, d_rot // 2, "positions")
     _freqs(freqs, d_rot)
     code = _layout(layout)
     with _on(dev):
@@ -571,11 +607,17 @@ def rope(x, positions, freqs, layout="interleaved", mscale: float = 1.0, out_pas
             return out_pass, out_rot
         if (xs[2] != 1 and D > 1) or rs[2] != 1 or (ps[2] != 1 and d_pass > 1):
             raise ValueError("x, out_pass and out_rot must have unit stride within a row")
-        st = lib().mla_rope(x.data_ptr(), xs[0], xs[1], N, H, d_pass, d_rot, code, positions.data_ptr(),
-                            freqs.data_ptr(), mscale, _at(out_pass), ps[0], ps[1], out_rot.data_ptr(), rs[0], rs[1],
-                            _raw(stream, dev))
+        if axes is None:
+            st = lib().mla_rope(x.data_ptr(), xs[0], xs[1], N, H, d_pass, d_rot, code, positions.data_ptr(),
+                                freqs.data_ptr(), mscale, _at(out_pass), ps[0], ps[1], out_rot.data_ptr(), rs[0],
+                                rs[1], _raw(stream, dev))
+        else:
+            at = positions.stride()
+            st = lib().mla_rope_axes(x.data_ptr(), xs[0], xs[1], N, H, d_pass, d_rot, code, positions.data_ptr(), at[0],
+                                     at[1], num_axes, axes, freqs.data_ptr(), mscale, _at(out_pass), ps[0], ps[1],
+                                     out_rot.data_ptr(), rs[0], rs[1], _raw(stream, dev))
     if st:
-        _check("mla_rope", st)
+        _check("mla_rope" if axes is None else "mla_rope_axes", st)
     return out_pass, out_rot
 
 
@@ -614,12 +656,14 @@ def _entry_rows(t, N, name):
 
 def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_positions=None,
                 layout="interleaved", mscale: float = 1.0, norm_weight=None, norm_eps: float = 1e-6,
-                device_status=None, stream=None):
+                device_status=None, stream=None, axes=None):
     """Writes many tokens' entries: token n (kv bf16 [N,576]: latent | key) goes to position
     positions[n] (< 0 skips) of request requests[n] (None: request n) of the paged cache, bf16
     [P,64,576] or uint8 FP8 records [P,64,656] (quantised on the way in).  With norm_weight
     (bf16 [512]) the latent is RMS-normalised first; with freqs (float64 [32]) the key is rotated
-    at rope_positions (None: positions).  device_status: optional int32 [1] for MLA_ERR_INDEX."""
+    at rope_positions (None: positions).  With axes (from rope_axes, 32 pairs) as well, rope_positions
+    is int32 [N,A], a position per axis (any strides).  device_status: optional int32 [1] for
+    MLA_ERR_INDEX."""
     dev = _device_of("cache block_table requests positions kv freqs rope_positions norm_weight device_status", cache,
                      block_table, requests, positions, kv, freqs, rope_positions, norm_weight, device_status)
     kind = _cache_kind(cache)
@@ -627,7 +671,11 @@ def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_po
     stride = _entry_rows(kv, N, "kv")
     if freqs is not None:
         _freqs(freqs, 64)
-    if rope_positions is not None:
+    if axes is not None:
+        if freqs is None or rope_positions is None:
+            raise ValueError("axes without freqs or without rope_positions")
+        num_axes = _axis_places(rope_positions, axes, N, 32, "rope_positions")
+    elif rope_positions is not None:
         if freqs is None:
             raise ValueError("rope_positions without freqs")
         _ints(rope_positions, (N,), "rope_positions")
@@ -637,12 +685,20 @@ def cache_write(cache, block_table, requests, positions, kv, freqs=None, rope_po
     _status_word(device_status)
     code = _layout(layout)
     with _on(dev):
-        st = lib().mla_cache_write(
-            cache.data_ptr(), kind, cache.shape[0], block_table.data_ptr(), block_table.shape[0],
-            block_table.shape[1], _at(requests), positions.data_ptr(), kv.data_ptr(), stride, N, _at(norm_weight),
-            norm_eps, _at(freqs), _at(rope_positions), code, mscale, _at(device_status), _raw(stream, dev))
+        if axes is None:
+            st = lib().mla_cache_write(
+                cache.data_ptr(), kind, cache.shape[0], block_table.data_ptr(), block_table.shape[0],
+                block_table.shape[1], _at(requests), positions.data_ptr(), kv.data_ptr(), stride, N, _at(norm_weight),
+                norm_eps, _at(freqs), _at(rope_positions), code, mscale, _at(device_status), _raw(stream, dev))
+        else:
+            at = rope_positions.stride()
+            st = lib().mla_cache_write_axes(
+                cache.data_ptr(), kind, cache.shape[0], block_table.data_ptr(), block_table.shape[0],
+                block_table.shape[1], _at(requests), positions.data_ptr(), kv.data_ptr(), stride, N, _at(norm_weight),
+                norm_eps, freqs.data_ptr(), rope_positions.data_ptr(), at[0], at[1], num_axes, axes, code, mscale,
+                _at(device_status), _raw(stream, dev))
     if st:
-        _check("mla_cache_write", st)
+        _check("mla_cache_write" if axes is None else "mla_cache_write_axes", st)
     return cache
 
 
@@ -785,6 +841,40 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
     if st:
         _check("mla_verify_draft", st)
     return num, depths, nxt
+
+
+_LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def token_logprobs(logits, tokens, top: int = 0, scale: float = 1.0, device_status=None, stream=None):
+    """Scores of given tokens: logits bf16, fp16 or fp32 [N,V] (rows of any stride; -inf masks a token),
+    tokens int32 [N] (negative: none), scale = 1 / temperature -> (logprob fp32 [N], entropy fp32 [N],
+    rank int32 [N]: 0 for the best, top_tokens int32 [N,top] best first, top_logprobs fp32 [N,top]; None
+    for the last two where top is 0).  device_status: optional int32 [1] for MLA_ERR_INDEX."""
+    dev = _device_of("logits tokens device_status", logits, tokens, device_status)
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        raise ValueError("logits must be bf16, fp16 or fp32 [N,V]")
+    N, V = logits.shape
+    row, col = logits.stride()
+    if col != 1 and V > 1:
+        raise ValueError("logits must have unit stride within a row")
+    _ints(tokens, (N,), "tokens")
+    _status_word(device_status)
+    with _on(dev):
+        logprob = _new(logits, (N,), torch.float32, stream)
+        entropy = _new(logits, (N,), torch.float32, stream)
+        rank = _new(logits, (N,), torch.int32, stream)
+        ids = alt = None
+        if top > 0:
+            ids = _new(logits, (N, top), torch.int32, stream)
+            alt = _new(logits, (N, top), torch.float32, stream)
+        st = lib().mla_token_logprobs(
+            logits.data_ptr(), kind, row, N, V, tokens.data_ptr(), scale, top, logprob.data_ptr(), entropy.data_ptr(),
+            rank.data_ptr(), _at(ids), _at(alt), _at(device_status), _raw(stream, dev))
+    if st:
+        _check("mla_token_logprobs", st)
+    return logprob, entropy, rank, ids, alt
 
 
 def plan_tree_host(seq_lens, tree_lens, B: int, T: int, H: int, num_sms: int = 148, kv_dtype="bf16"):
