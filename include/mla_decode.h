@@ -397,6 +397,43 @@ mla_status mla_verify_draft(const float *target, const float *draft, const int32
  * are scored (mla_token_logprobs).
  * ------------------------------------------------------------------------------------------ */
 
+/* Attention of a ragged batch of query runs to key runs of another length, non-absorbed (192-wide
+ * keys, 128-wide values, as mla_prefill_attention): the queries of run b are rows cu_q[b] ..
+ * cu_q[b + 1] of [total_q], its keys rows cu_k[b] .. cu_k[b + 1] of [total_k] (device int32 [B + 1],
+ * not falling, within [0, total_q] and [0, total_k]).  Query i of a run's n attends to all of its m
+ * keys (an encoder's states; a prefix brought back by mla_cache_read and decompressed), or, causal, to
+ * keys t <= m - n + i (a chunk over its prefix and itself: the last query sees every key):
+ *   s_t = softmax_scale * (q_nope . k_nope[h][t] + q_rope . k_R[t]),
+ *   out = sum_t softmax(s)_t v[h][t],   lse = ln sum_t e^{s_t}.
+ * q_nope bf16 [total_q][H][128], q_rope bf16 [total_q][H][64], entries bf16 [total_k][576] (k_R is
+ * columns 512 .. 575), k_nope and v bf16 [H][total_k][128] as mla_prefill_decompress writes them.
+ * q_rope and entries may both be NULL: scores without a part for positions.
+ * before_out fp32 [total_q][H][128] and before_lse fp32 [total_q][H] (both or neither) hold the result
+ * over an earlier part of the keys; the call's is joined with it:
+ *   L = ln(e^{before_lse} + e^{lse}),  out = e^{before_lse - L} before_out + e^{lse - L} out,  lse = L
+ * (a before_lse of -inf: nothing so far, before_out may hold anything there).  They may be out
+ * (fp32) and lse themselves, otherwise they must not overlap them.
+ * out fp32 or bf16 (rounded once), lse fp32 [total_q][H] or NULL.  A query that sees no key gets
+ * out = 0 and lse = -inf (or the earlier part's result).  Rows of out and lse outside every run stay
+ * as they were, and rows of q, entries, k_nope and v outside every run may hold anything; values
+ * inside the runs must be finite.  Scores and softmax in fp32, probabilities rounded to bf16 for their
+ * product with the values, fp32 accumulation; a call's result depends on its sizes alone.
+ * The plan reads cu_q and cu_k on the device; it serves any number of calls (layers) until they
+ * change, one call at a time, and holds the work list, partial results and the status word, which
+ * mla_decode_status reads: runs that fall or lie outside are moved up or in and recorded as
+ * MLA_ERR_INDEX.  After MLA_ERR_TIMEOUT the plan has to be made again.  num_sms as for
+ * mla_decode_plan, the same in both calls.  1 <= B <= 2^20, total_q <= 2^24, 1 <= H <= 128; workspace
+ * and tensors 16-byte aligned. */
+size_t mla_cross_workspace_size(int B, int H, int64_t total_q, int num_sms);
+
+mla_status mla_cross_plan(const int32_t *cu_q, const int32_t *cu_k, int B, int H, int64_t total_q, int64_t total_k,
+                          int causal, int num_sms, void *workspace, size_t ws_bytes, void *stream);
+
+mla_status mla_cross_attention(void *workspace, size_t ws_bytes, const void *q_nope, const void *q_rope,
+                               const void *entries, const void *k_nope, const void *v, int B, int H, int64_t total_q,
+                               int64_t total_k, float softmax_scale, const float *before_out, const float *before_lse,
+                               void *out, mla_out_dtype out_dtype, float *lse, void *stream);
+
 /* Log probabilities of given tokens: for each of N rows of logits x [V], with p = softmax(scale x)
  * over the row,
  *   logprob[n]  = ln p(tokens[n]),

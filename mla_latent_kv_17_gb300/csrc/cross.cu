@@ -1,0 +1,957 @@
+// Attention of a ragged batch of query runs to key runs of another length (an encoder's states, a
+// cached prefix, a chunk over its prefix and itself).  The definition is in include/mla_decode.h
+// (mla_cross_attention).
+//
+// cross_plan_kernel: one CTA cuts the batch into items - a tile of 128 or 256 query rows of a run
+// with the key tiles (of 128) it sees - and items whose keys would keep one SM much longer than
+// the others' share into pieces, and orders the pieces by falling length.  The list is the same for
+// every head.
+//
+// cross_kernel: a persistent CTA per SM takes units (a piece and a head) from a counter, longest
+// pieces first, groups of eight heads in turn so that the keys and values in use stay in L2.  Per
+// unit, as in the causal prefill: S = Q K^T on tcgen05 into TMEM, online softmax with one thread per
+// query row, P as bf16 over its scores in TMEM, O += P V.  The loads and first scores of the next unit
+// run under the last softmax and the epilogue of the present one.
+//   256 rows: two query tiles share the keys and take turns on the tensor pipe.
+//   128 rows: one query tile, scores and values double-buffered, for short runs, where the keys'
+//   and values' way from memory bounds the call.
+// The pieces of an item leave normalised partial results; the one that comes last (a ticket per item,
+// head and tile) joins them, in the pieces' order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "mla_decode.h"
+#include "sm103_ptx.cuh"
+#include "tc_util.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+
+constexpr int kCrDh = 128;
+constexpr int kCrTile = 128;            // query rows of a tile (TMEM lanes), keys of a tile
+constexpr int kCrHeadGroup = 8;
+constexpr int kCrMinPiece = 4;          // key tiles
+constexpr int kCrShare = 3;             // pieces an SM's share is made of, at least, before items stay whole
+constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
+constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
+constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
+
+struct CrossHeader {
+    uint32_t magic;
+    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, partial_rows, reserved[5];
+};
+static_assert(sizeof(CrossHeader) == 64, "plan header is 64 bytes");
+
+// Key tiles [g0, g1) of the run's nk keys (from row k0 on) for query rows q0 .. q0 + nrows; a causal
+// plan's row r sees the keys below see0 + r (0 and less: none), any other's all of them.
+struct CrossPiece {
+    int32_t q0, nrows, k0, nk, see0, g0, g1;
+    int32_t part, parts;     // this piece of the item's
+    int32_t row0;            // the item's first partial row (part p: + p nrows)
+    int32_t split;           // the item's number among those cut
+    int32_t head;            // (filled in where a unit is taken)
+};
+
+struct CrossLayout {
+    size_t pieces, order, seqs, item_off, tickets, part_lse, part_o, total;
+    int max_pieces, max_splits;
+    int64_t max_rows;
+};
+
+constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it
+constexpr size_t kCrCounters = 192;  // next unit, CTAs that are done
+
+MLA_HD int cross_rows(int B, int64_t total_q) { return total_q > (int64_t)kCrTile * B ? 2 * kCrTile : kCrTile; }
+
+MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {
+    CrossLayout L;
+    const int rows = cross_rows(B, total_q);
+    // An item of t tiles is cut into n = ceil(t / target) > 1 pieces, and the target is at least the batch's
+    // cost / `cuts`: at most `cuts` items are cut, into 2 `cuts` pieces together and `cuts` + 1 each.
+    const int64_t cuts = (int64_t)kCrShare * sms / H + 1, items = total_q / rows + B;
+    L.max_pieces = (int)(items + cuts);
+    L.max_splits = (int)cuts;
+    const int64_t by_pieces = 2 * cuts * rows, by_rows = (cuts + 1) * total_q;
+    L.max_rows = by_pieces < by_rows ? by_pieces : by_rows;
+    size_t o = 256;
+    L.pieces = o;
+    o = align_up(o + sizeof(CrossPiece) * (size_t)L.max_pieces, 256);
+    L.order = o;
+    o = align_up(o + sizeof(int32_t) * (size_t)L.max_pieces, 256);
+    L.seqs = o;
+    o = align_up(o + sizeof(int4) * (size_t)B, 256);
+    L.item_off = o;
+    o = align_up(o + sizeof(int32_t) * (size_t)(B + 1), 256);
+    L.tickets = o;
+    o = align_up(o + sizeof(int32_t) * (size_t)L.max_splits * H * 2, 256);
+    L.part_lse = o;
+    o = align_up(o + sizeof(float) * (size_t)L.max_rows * H, 256);
+    L.part_o = o;
+    o = align_up(o + sizeof(float) * (size_t)L.max_rows * H * kCrDh, 256);
+    L.total = o;
+    return L;
+}
+
+// ------------------------------------------------------------------ the plan
+constexpr int kCpThreads = 512;
+constexpr int kCpWarps = kCpThreads / 32;
+constexpr int kCpSort = 2048;  // pieces that are put in order (more of them even out by themselves)
+
+struct Add {
+    __device__ __forceinline__ int64_t operator()(int64_t a, int64_t b) const { return a + b; }
+};
+struct Max {
+    __device__ __forceinline__ int64_t operator()(int64_t a, int64_t b) const { return a > b ? a : b; }
+};
+
+// Inclusive scan of v over the block; *all receives the whole.  sh: kCpWarps values.
+template <typename Op>
+__device__ int64_t block_scan(int64_t v, Op op, int64_t *all, int64_t *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = op(v, y);
+    }
+    if (lane == 31) sh[warp] = v;
+    __syncthreads();
+    int64_t before = 0, whole = sh[0];
+    for (int i = 0; i < kCpWarps; ++i) {
+        if (i == warp && i > 0) v = op(v, before);
+        before = i == 0 ? sh[0] : op(before, sh[i]);
+        whole = before;
+    }
+    *all = whole;
+    __syncthreads();
+    return v;
+}
+
+struct CrossPlanArgs {
+    const int32_t *cu_q, *cu_k;
+    int B, H, total_q, total_k, causal, rows, sms;
+    unsigned char *ws;
+    CrossLayout L;
+};
+
+// Keys that the item's rows up to `end` (of nq) see.
+__device__ __forceinline__ int seen_by(int end, int nq, int nk, int causal) {
+    if (!causal) return nk;
+    const int s = nk - nq + end;
+    return s < 0 ? 0 : s;
+}
+__device__ __forceinline__ int key_tiles(int keys) { return (keys + kCrTile - 1) / kCrTile; }
+
+__global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const CrossPlanArgs a) {
+    __shared__ int64_t s_scan[kCpWarps];
+    __shared__ uint32_t s_key[kCpSort];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x;
+    int4 *seqs = reinterpret_cast<int4 *>(a.ws + a.L.seqs);
+    int32_t *item_off = reinterpret_cast<int32_t *>(a.ws + a.L.item_off);
+    CrossPiece *pieces = reinterpret_cast<CrossPiece *>(a.ws + a.L.pieces);
+    int32_t *order = reinterpret_cast<int32_t *>(a.ws + a.L.order);
+    int32_t *tickets = reinterpret_cast<int32_t *>(a.ws + a.L.tickets);
+    int *status = reinterpret_cast<int *>(a.ws + kCrStatus);
+
+    // the runs: starts that fall or lie outside are moved up or in (and recorded), so that runs never
+    // overlap and the items fit their places
+    int64_t q_upto = 0, k_upto = 0, items = 0, cost = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kCpThreads) {
+        const int b = b0 + tid;
+        int64_t q = 0, q2 = 0, k = 0, k2 = 0;
+        if (b < a.B) {
+            const int32_t r[4] = {a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]};
+            q = min(max(r[0], 0), a.total_q);
+            q2 = min(max(r[1], 0), a.total_q);
+            k = min(max(r[2], 0), a.total_k);
+            k2 = min(max(r[3], 0), a.total_k);
+            if (r[0] != q || r[1] != q2 || r[2] != k || r[3] != k2 || r[0] > r[1] || r[2] > r[3])
+                record_error(status, MLA_ERR_INDEX);
+        }
+        int64_t all;
+        // ends so far, this run's own among them; a run starts no earlier than they do before it
+        const int64_t qe = max(q_upto, block_scan(max(q, q2), Max(), &all, s_scan));
+        const int64_t q_all = max(q_upto, all);
+        const int64_t ke = max(k_upto, block_scan(max(k, k2), Max(), &all, s_scan));
+        const int64_t k_all = max(k_upto, all);
+        // (the start: the maximum of everything before cu[b + 1])
+        const int64_t qs = max(q_upto, block_scan(q, Max(), &all, s_scan));
+        const int64_t ks = max(k_upto, block_scan(k, Max(), &all, s_scan));
+        const int nq = b < a.B ? (int)(qe - qs) : 0, nk = b < a.B ? (int)(ke - ks) : 0;
+        const int tiles = (nq + a.rows - 1) / a.rows;
+        int64_t c = 0;
+        for (int j = 0; j < tiles; ++j)
+            c += kCrItemCost + key_tiles(seen_by(min(nq, (j + 1) * a.rows), nq, nk, a.causal));
+        const int64_t upto = items + block_scan(tiles, Add(), &all, s_scan);
+        items += all;
+        block_scan(c, Add(), &all, s_scan);
+        cost += all;
+        if (b < a.B) {
+            seqs[b] = make_int4((int)qs, nq, (int)ks, nk);
+            item_off[b] = (int32_t)(upto - tiles);
+        }
+        q_upto = q_all;
+        k_upto = k_all;
+    }
+    __syncthreads();
+
+    // the items, and those of more than a part of an SM's share in pieces
+    const int64_t shares = (int64_t)kCrShare * a.sms;
+    const int64_t share = (cost * a.H + shares - 1) / shares;
+    const int target = (int)(share > kCrMinPiece ? share : kCrMinPiece);
+    int64_t n_pieces = 0, n_splits = 0, n_rows = 0;
+    for (int64_t i0 = 0; i0 < items; i0 += kCpThreads) {
+        const int64_t i = i0 + tid;
+        int n = 0;
+        CrossPiece p = {};
+        int tiles = 0;
+        if (i < items) {
+            int lo = 0, hi = a.B - 1;  // the last run that starts at or before item i (empty runs share a start)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (item_off[mid] <= i)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int4 s = seqs[lo];
+            const int r0 = (int)(i - item_off[lo]) * a.rows;
+            p.nrows = min(a.rows, s.y - r0);
+            p.q0 = s.x + r0;
+            p.k0 = s.z;
+            p.nk = s.w;
+            p.see0 = s.w - s.y + r0 + 1;
+            tiles = key_tiles(seen_by(r0 + p.nrows, s.y, s.w, a.causal));
+            n = tiles > target ? (tiles + target - 1) / target : 1;
+        }
+        int64_t all;
+        const int64_t at = n_pieces + block_scan(n, Add(), &all, s_scan) - n;
+        n_pieces += all;
+        const int64_t sp = n_splits + block_scan(n > 1, Add(), &all, s_scan) - (n > 1);
+        n_splits += all;
+        const int64_t rows = n > 1 ? (int64_t)n * p.nrows : 0;
+        const int64_t row0 = n_rows + block_scan(rows, Add(), &all, s_scan) - rows;
+        n_rows += all;
+        for (int k = 0; k < n; ++k) {
+            p.g0 = (int)((int64_t)tiles * k / n);
+            p.g1 = (int)((int64_t)tiles * (k + 1) / n);
+            p.part = k;
+            p.parts = n;
+            p.row0 = (int)row0;
+            p.split = (int)sp;
+            pieces[at + k] = p;
+            if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(p.g1 - p.g0, 0xFFFF)) << 16 | (uint32_t)(at + k);
+        }
+    }
+    for (int64_t i = tid; i < n_splits * a.H * 2; i += kCpThreads) tickets[i] = 0;
+    __syncthreads();
+
+    // longest first
+    if (n_pieces > 1 && n_pieces <= kCpSort) {
+        int n = 2;
+        while (n < n_pieces) n *= 2;
+        for (int i = (int)n_pieces + tid; i < n; i += kCpThreads) s_key[i] = 0xFFFFFFFFu;
+        __syncthreads();
+        for (int w = 2; w <= n; w *= 2) {
+            for (int d = w / 2; d > 0; d /= 2) {
+                for (int i = tid; i < n / 2; i += kCpThreads) {
+                    const int x = 2 * d * (i / d) + i % d, y = x + d;
+                    const uint32_t u = s_key[x], v = s_key[y];
+                    if ((u > v) == ((x & w) == 0)) {
+                        s_key[x] = v;
+                        s_key[y] = u;
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        for (int i = tid; i < n_pieces; i += kCpThreads) order[i] = (int32_t)(s_key[i] & 0xFFFFu);
+    } else {
+        for (int64_t i = tid; i < n_pieces; i += kCpThreads) order[i] = (int32_t)i;
+    }
+    if (tid == 0) {
+        int *counters = reinterpret_cast<int *>(a.ws + kCrCounters);
+        counters[0] = counters[1] = 0;
+        CrossHeader h = {};
+        h.magic = kCrossMagic;
+        h.B = a.B;
+        h.H = a.H;
+        h.total_q = a.total_q;
+        h.total_k = a.total_k;
+        h.causal = a.causal;
+        h.rows = a.rows;
+        h.sms = a.sms;
+        h.pieces = (int32_t)n_pieces;
+        h.splits = (int32_t)n_splits;
+        h.partial_rows = (int32_t)n_rows;
+        *reinterpret_cast<CrossHeader *>(a.ws) = h;
+    }
+}
+
+// ------------------------------------------------------------------ the attention
+constexpr uint32_t kCrBox = 64 * kCrTile * 2;  // 64 columns x 128 rows, bf16
+
+template <int kTiles>
+struct Shape {
+    static constexpr int kWarpsSoft = 4 * kTiles;
+    static constexpr int kThreads = 32 * (kWarpsSoft + 4);  // + keys, MMAs, values, units
+    static constexpr int kK = 2, kV = kTiles == 1 ? 2 : 1;  // buffers
+    static constexpr uint32_t kOffK = 3 * kCrBox * kTiles, kOffV = kOffK + 3 * kCrBox * kK;
+    static constexpr uint32_t kOffBar = kOffV + 2 * kCrBox * kV;
+    static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
+};
+
+struct CrossArgs {
+    unsigned char *ws;
+    size_t ws_bytes;
+    int B, H, total_q, total_k, rows;
+    float scale_log2;
+    int positions;
+    const float *before_out, *before_lse;
+    float *out;       // one of the two
+    uint16_t *out16;
+    float *lse;       // or null
+};
+
+// The result's row: the new part (o, of sum e^{lse}) joined with an earlier one.
+struct Share {
+    float mine, before, lse;
+};
+__device__ __forceinline__ Share share_of(float lse, const float *before, int64_t row) {
+    Share s{1.f, 0.f, lse};
+    if (before) {
+        const float b = before[row], m = fmaxf(lse, b);
+        if (m == -INFINITY) return s;
+        const float e0 = expf(b - m), e1 = expf(lse - m), sum = e0 + e1;
+        s.mine = e1 / sum;
+        s.before = e0 / sum;
+        s.lse = m + logf(sum);
+    }
+    return s;
+}
+__device__ __forceinline__ void store4(const CrossArgs &a, int64_t at, float4 o, const Share &s) {
+    o.x *= s.mine;
+    o.y *= s.mine;
+    o.z *= s.mine;
+    o.w *= s.mine;
+    if (s.before != 0.f) {  // (what has no weight may hold anything)
+        const float4 b = *reinterpret_cast<const float4 *>(a.before_out + at);
+        o.x = fmaf(b.x, s.before, o.x);
+        o.y = fmaf(b.y, s.before, o.y);
+        o.z = fmaf(b.z, s.before, o.z);
+        o.w = fmaf(b.w, s.before, o.w);
+    }
+    if (a.out)
+        *reinterpret_cast<float4 *>(a.out + at) = o;
+    else
+        *reinterpret_cast<uint2 *>(a.out16 + at) = make_uint2(bf16x2_bits(o.x, o.y), bf16x2_bits(o.z, o.w));
+}
+
+template <int kTiles>
+__global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
+    cross_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qr,
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CrossArgs a) {
+    using S = Shape<kTiles>;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char *gbase = smem_raw + (base - raw);
+    const uint32_t bars = base + S::kOffBar;
+    // barriers: the queries: q_full, q_empty; per key buffer k_full, k_empty; per value buffer v_full,
+    // v_empty, and v_landed for a run's last tile; per score buffer s_full, p_full (one arrival per
+    // softmax warp), pv_done; per query tile o_free; per unit slot u_full, u_empty.  (pv_done per score
+    // buffer: with two of them a tile's scores say nothing about the PV before the last one, and a wait
+    // for the last one's phase would pass while a common barrier is still two phases back.)
+    const uint32_t q_full = bars, q_empty = bars + 8;
+    auto k_full = [&](int b) { return bars + 16u + 8u * b; };
+    auto k_empty = [&](int b) { return bars + 32u + 8u * b; };
+    auto v_full = [&](int b) { return bars + 48u + 8u * b; };
+    auto v_empty = [&](int b) { return bars + 64u + 8u * b; };
+    const uint32_t v_landed = bars + 80;
+    auto s_full = [&](int j) { return bars + 88u + 8u * j; };
+    auto p_full = [&](int j) { return bars + 104u + 8u * j; };
+    auto pv_done = [&](int j) { return bars + 120u + 8u * j; };
+    auto o_free = [&](int x) { return bars + 136u + 8u * x; };
+    auto u_full = [&](int j) { return bars + 152u + 8u * j; };
+    auto u_empty = [&](int j) { return bars + 168u + 8u * j; };
+    CrossPiece *slots = reinterpret_cast<CrossPiece *>(gbase + S::kOffBar + 192);  // two of 48 bytes
+    int *abort_flag = reinterpret_cast<int *>(gbase + S::kOffBar + 288);
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(gbase + S::kOffBar + 296);
+    volatile int *last_in = reinterpret_cast<volatile int *>(gbase + S::kOffBar + 304);  // per query tile
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_init(q_full, 1);
+            mbar_init(q_empty, 1);
+            mbar_init(v_landed, 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(k_full(b), 1);
+                mbar_init(k_empty(b), 1);
+                mbar_init(v_full(b), 1);
+                mbar_init(v_empty(b), 1);
+                mbar_init(s_full(b), 1);
+                mbar_init(p_full(b), 4);
+                mbar_init(pv_done(b), 1);
+                mbar_init(o_free(b), 4);
+                mbar_init(u_full(b), 1);
+                mbar_init(u_empty(b), 3 + S::kWarpsSoft);
+            }
+            *abort_flag = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(tslot)), 512);
+        tmem_relinquish();
+    }
+    grid_dep_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    int *status = reinterpret_cast<int *>(a.ws + kCrStatus);
+    int *counters = reinterpret_cast<int *>(a.ws + kCrCounters);
+    CrossHeader *hd = reinterpret_cast<CrossHeader *>(a.ws);
+    const bool match = hd->magic == kCrossMagic && hd->B == a.B && hd->H == a.H && hd->total_q == a.total_q &&
+                       hd->total_k == a.total_k && hd->rows == a.rows && hd->sms > 0 &&
+                       cross_layout(a.B, a.H, a.total_q, hd->sms).total <= a.ws_bytes;
+    if (!match && threadIdx.x == 0) record_error(status, MLA_ERR_WORKSPACE);
+    const int step = hd->causal ? 1 : 0;
+    bool ok = true;
+
+    // The next unit's piece, from its slot (the whole warp); false: there is none, or a wait ran out.
+    int taken = 0;
+    CrossPiece p;
+    auto next_unit = [&]() -> bool {
+        if (!ok) return false;
+        const int j = taken & 1;
+        ok = __all_sync(0xffffffffu, wait_bounded(u_full(j), (taken >> 1) & 1, abort_flag));
+        if (!ok) return false;
+        p = slots[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty(j));
+        ++taken;
+        return p.head >= 0;
+    };
+    // Keys that row r of the item sees, and key tiles of query tile x within the piece.
+    auto seen = [&](int r) { return step ? min(p.nk, p.see0 + r) : p.nk; };
+    auto tiles_of = [&](int x) -> int {
+        const int rows = min(p.nrows - x * kCrTile, kCrTile);
+        if (rows <= 0) return 0;
+        const int keys = max(seen(x * kCrTile + rows - 1), 0);
+        return max(min(p.g1, (keys + kCrTile - 1) / kCrTile) - p.g0, 0);
+    };
+    // (of two query tiles the second sees as many keys as the first, or more, where it has rows)
+    auto tiles_loaded = [&]() -> int { return kTiles == 2 ? max(tiles_of(0), tiles_of(1)) : tiles_of(0); };
+    const int w = warp - S::kWarpsSoft;
+
+    if (!match) {
+        // nothing to do
+    } else if (w == 3) {
+        // ---------------------------------------------------------------- units
+        if (lane == 0) {
+            const CrossLayout L = cross_layout(a.B, a.H, a.total_q, hd->sms);
+            const CrossPiece *pieces = reinterpret_cast<const CrossPiece *>(a.ws + L.pieces);
+            const int32_t *order = reinterpret_cast<const int32_t *>(a.ws + L.order);
+            const int n = hd->pieces;
+            for (int i = 0; ok; ++i) {
+                const int j = i & 1;
+                if (i >= 2) ok = wait_bounded(u_empty(j), ((i >> 1) - 1) & 1, abort_flag);
+                if (!ok) break;
+                const int u = atomicAdd(&counters[0], 1);
+                CrossPiece d;
+                d.head = -1;
+                if (u < n * a.H) {
+                    // a group of heads: each piece for all of them, in the pieces' order
+                    const int h0 = u / (kCrHeadGroup * n) * kCrHeadGroup, hg = min(kCrHeadGroup, a.H - h0);
+                    const int r = u - h0 * n;
+                    d = pieces[order[r / hg]];
+                    d.head = h0 + r % hg;
+                }
+                slots[j] = d;
+                mbar_arrive(u_full(j));
+                if (d.head < 0) break;
+            }
+        }
+    } else if (w == 0) {
+        // ---------------------------------------------------------------- queries and keys
+        const uint32_t boxes = a.positions ? 3 : 2;
+        int units = 0, t = 0;
+        while (next_unit()) {
+            const int ntot = tiles_loaded();
+            if (ntot == 0) continue;
+            if (lane == 0) {
+                const int nx = kTiles == 2 && p.nrows > kCrTile ? 2 : 1;
+                if (units > 0) ok = wait_bounded(q_empty, (units - 1) & 1, abort_flag);
+                if (ok) {
+                    mbar_arrive_expect_tx(q_full, nx * boxes * kCrBox);
+                    for (int x = 0; x < nx; ++x) {
+                        const uint32_t qd = base + 3 * kCrBox * x;
+                        const int q0 = p.q0 + x * kCrTile;
+                        tma_load_3d(qd, &tm_qn, 0, p.head, q0, q_full);
+                        tma_load_3d(qd + kCrBox, &tm_qn, 64, p.head, q0, q_full);
+                        if (a.positions) tma_load_3d(qd + 2 * kCrBox, &tm_qr, 0, p.head, q0, q_full);
+                    }
+                }
+                for (int g = 0; g < ntot && ok; ++g) {
+                    const int b = (t + g) % S::kK, use = (t + g) / S::kK;
+                    if (use > 0) ok = wait_bounded(k_empty(b), (use - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const uint32_t kd = base + S::kOffK + b * 3 * kCrBox;
+                    const int k0 = p.k0 + (p.g0 + g) * kCrTile;
+                    mbar_arrive_expect_tx(k_full(b), boxes * kCrBox);
+                    tma_load_3d(kd, &tm_k, 0, k0, p.head, k_full(b));
+                    tma_load_3d(kd + kCrBox, &tm_k, 64, k0, p.head, k_full(b));
+                    if (a.positions) tma_load_2d(kd + 2 * kCrBox, &tm_kr, kDLatent, k0, k_full(b));
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            ++units;
+            t += ntot;
+        }
+    } else if (w == 2) {
+        // ---------------------------------------------------------------- values
+        int t = 0, landed = 0;
+        while (next_unit()) {
+            const int ntot = tiles_loaded();
+            for (int g = 0; g < ntot && ok; ++g, ++t) {
+                const int b = t % S::kV, use = t / S::kV;
+                if (use > 0) ok = __all_sync(0xffffffffu, wait_bounded(v_empty(b), (use - 1) & 1, abort_flag));
+                if (!ok) break;
+                const uint32_t vd = base + S::kOffV + b * 2 * kCrBox;
+                const int t0 = (p.g0 + g) * kCrTile, valid = p.nk - t0;
+                // What lies behind the run's last key is another run's, or anything: its weights are 0, but
+                // 0 x NaN is not, so those rows are zeroed before PV reads them.
+                const uint32_t bar = valid < kCrTile ? v_landed : v_full(b);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, 2 * kCrBox);
+                    tma_load_3d(vd, &tm_v, 0, p.k0 + t0, p.head, bar);
+                    tma_load_3d(vd + kCrBox, &tm_v, 64, p.k0 + t0, p.head, bar);
+                }
+                if (valid < kCrTile) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(v_landed, landed & 1, abort_flag));
+                    ++landed;
+                    if (!ok) break;
+                    const int chunks = (kCrTile - valid) * 8;  // 16 bytes each, of either box
+                    uint4 *rows = reinterpret_cast<uint4 *>(gbase + S::kOffV + b * 2 * kCrBox + valid * 128);
+                    for (int i = lane; i < chunks; i += 32) {
+                        rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                        rows[kCrBox / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_full(b));
+                }
+            }
+        }
+    } else if (w == 1) {
+        // ---------------------------------------------------------------- MMAs
+        // the whole warp runs the issue loop (its waits made warp-uniform); one elected lane issues
+        auto wait_w = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_quick(bar, parity, abort_flag));
+        };
+        constexpr uint32_t idesc_s = idesc_bf16_major(128, kCrTile, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16_major(128, kCrDh, false, true);
+        const int steps = a.positions ? 12 : 8;
+        int units = 0, t = 0;              // units with keys, and their key tiles, so far
+        int su[2] = {0, 0}, ou[2] = {0, 0};  // uses of each score buffer, units of each query tile, so far
+        while (next_unit()) {
+            const int n0 = tiles_of(0), n1 = kTiles == 2 ? tiles_of(1) : 0, ntot = max(n0, n1);
+            if (ntot == 0) continue;
+            // Scores of query tile x with key tile g; the key buffer goes back after the last query tile
+            // that reads it, the queries after the unit's last scores.
+            auto qk = [&](int x, int g) -> bool {
+                const int b = (t + g) % S::kK, j = kTiles == 2 ? x : (t + g) & 1;
+                if (!wait_w(k_full(b), ((t + g) / S::kK) & 1)) return false;
+                tc_fence_after();
+                const uint32_t kd = base + S::kOffK + b * 3 * kCrBox, qd = base + 3 * kCrBox * x;
+                const uint32_t cs = tmem + (kTiles == 2 ? 256u * x : 128u * j);
+                for (int k = 0; k < steps; ++k) {
+                    const uint32_t off = (k >> 2) * kCrBox + (k & 3) * 32u;
+                    mma_ss_warp(cs, smem_desc_sw128(qd + off, 16u, 1024u), smem_desc_sw128(kd + off, 16u, 1024u), idesc_s,
+                                k > 0 ? 1u : 0u);
+                }
+                mma_commit_warp(s_full(j));
+                if (x == (g < n1 ? 1 : 0)) {
+                    mma_commit_warp(k_empty(b));
+                    if (g == ntot - 1) mma_commit_warp(q_empty);
+                }
+                return true;
+            };
+            // O_x += P_x(g) V(g); the value buffer goes back after the last query tile's.
+            auto pv = [&](int x, int g) -> bool {
+                const int j = kTiles == 2 ? x : (t + g) & 1, b = (t + g) % S::kV;
+                if (g == 0 && ou[x] > 0 && !wait_w(o_free(x), (ou[x] - 1) & 1)) return false;
+                if (!wait_w(p_full(j), su[j] & 1) || !wait_w(v_full(b), ((t + g) / S::kV) & 1)) return false;
+                tc_fence_after();
+                ++su[j];
+                const uint32_t cp = tmem + (kTiles == 2 ? 256u * x : 128u * j);
+                const uint32_t co = tmem + (kTiles == 2 ? 256u * x + 128u : 256u);
+                for (int k = 0; k < kCrTile / 16; ++k) {
+                    const uint64_t bd = smem_desc_sw128(base + S::kOffV + b * 2 * kCrBox + k * 2048u, kCrBox, 1024u);
+                    mma_ts_warp(co, cp + 8u * k, bd, idesc_o, (g > 0 || k > 0) ? 1u : 0u);
+                }
+                mma_commit_warp(pv_done(j));
+                if (x == (g < n1 ? 1 : 0)) mma_commit_warp(v_empty(b));
+                return true;
+            };
+            ok = wait_w(q_full, units & 1);
+            if constexpr (kTiles == 2) {
+                ok = ok && (n0 == 0 || qk(0, 0)) && (n1 == 0 || qk(1, 0));
+                for (int g = 0; g < ntot && ok; ++g) {
+                    if (g < n0) ok = pv(0, g) && (g + 1 >= n0 || qk(0, g + 1));
+                    if (ok && g < n1) ok = pv(1, g) && (g + 1 >= n1 || qk(1, g + 1));
+                }
+            } else {
+                ok = ok && qk(0, 0);
+                for (int g = 0; g < ntot && ok; ++g) ok = (g + 1 >= ntot || qk(0, g + 1)) && pv(0, g);
+            }
+            if (n0 > 0) ++ou[0];
+            if (n1 > 0) ++ou[1];
+            ++units;
+            t += ntot;
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        // warps 4x .. 4x + 3: query tile x, rows 32 (w % 4) .. (its TMEM lanes), one thread per row
+        const CrossLayout L = cross_layout(a.B, a.H, a.total_q, hd->sms);
+        float *part_lse = reinterpret_cast<float *>(a.ws + L.part_lse);
+        float *part_o = reinterpret_cast<float *>(a.ws + L.part_o);
+        int32_t *tickets = reinterpret_cast<int32_t *>(a.ws + L.tickets);
+        const int x = warp >> 2, quad = warp & 3;
+        const int r = x * kCrTile + 32 * quad + lane;  // the item's row
+        const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
+        const uint32_t cO = tmem + lane_base + (kTiles == 2 ? 256u * x + 128u : 256u);
+        int t = 0;  // key tiles of this query tile so far
+        auto wait_pv = [&](int n) {
+            return wait_bounded(pv_done(kTiles == 2 ? x : n & 1), (kTiles == 2 ? n : n >> 1) & 1, abort_flag);
+        };
+        while (next_unit()) {
+            const int nt = tiles_of(x);
+            // (rows past the item's compute something nobody reads)
+            const int see = r < p.nrows ? seen(r) : p.nk;
+            float m = -INFINITY, l = 0.f;  // reference maximum (log2 units), running sum
+            for (int g = 0; g < nt; ++g) {
+                const int n = t + g, j = kTiles == 2 ? x : n & 1;
+                ok = wait_bounded(s_full(j), (kTiles == 2 ? n : n >> 1) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t cS = tmem + lane_base + (kTiles == 2 ? 256u * x : 128u * j);
+                float s[kCrTile];
+#pragma unroll
+                for (int c = 0; c < kCrTile / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(cS + 32u * c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(v[i]);
+                }
+                const int lim = see - (p.g0 + g) * kCrTile;  // columns c < lim are seen
+                if (__any_sync(0xffffffffu, lim < kCrTile)) {
+#pragma unroll
+                    for (int c = 0; c < kCrTile; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+                }
+                float mxs[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) mxs[c] = s[c];
+#pragma unroll
+                for (int c = 8; c < kCrTile; ++c) mxs[c & 7] = fmaxf(mxs[c & 7], s[c]);
+                const float mx = fmaxf(m, a.scale_log2 * fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
+                                                               fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7]))));
+                // the reference moves only when exceeded by 2^8 (probabilities stay <= 2^8), so most tiles leave
+                // O alone; a row that has seen no key yet keeps -inf, probabilities of 0 and an O of 0
+                const float mref = (m == -INFINITY || mx > m + kCrRescale) ? mx : m;
+                const float alpha = m == -INFINITY ? 1.f : ex2_approx(m - mref);
+                const float sub = mref == -INFINITY ? 0.f : -mref;
+                float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = ex2_approx(fmaf(s[64 * c + 2 * i], a.scale_log2, sub));
+                        const float p1 = ex2_approx(fmaf(s[64 * c + 2 * i + 1], a.scale_log2, sub));
+                        sums[i & 3] += p0 + p1;
+                        pk[i] = bf16x2_bits(p0, p1);
+                    }
+                    tmem_st32(cS + 32u * c, pk);
+                }
+                l = l * alpha + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
+                m = mref;
+                // O is rescaled (rarely) once the previous PV has finished; the next waits for this P
+                if (g > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    ok = wait_pv(n - 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kCrDh / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(cO + 32u * c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                        tmem_st32(cO + 32u * c, v);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(j));
+            }
+            if (!ok) break;
+            t += nt;
+            // the result's row, normalised
+            float o[kCrDh];
+#pragma unroll
+            for (int c = 0; c < kCrDh; ++c) o[c] = 0.f;
+            if (nt > 0) {
+                ok = wait_pv(t - 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int c = 0; c < kCrDh / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(cO + 32u * c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[32 * c + i] = __uint_as_float(v[i]) * inv;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_free(x));
+            }
+            const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+            if (p.parts == 1) {
+                if (r < p.nrows) {
+                    const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
+                    const Share sh = share_of(lse2 * kLn2, a.before_lse, row);
+#pragma unroll
+                    for (int c = 0; c < kCrDh; c += 4)
+                        store4(a, row * kCrDh + c, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]), sh);
+                    if (a.lse) a.lse[row] = sh.lse;
+                }
+                continue;
+            }
+            if (x * kCrTile >= p.nrows) continue;  // (the same for the query tile's warps)
+            if (r < p.nrows) {
+                const int64_t row = ((int64_t)p.row0 + (int64_t)p.part * p.nrows + r) * a.H + p.head;
+                float4 *dst = reinterpret_cast<float4 *>(part_o + row * kCrDh);
+#pragma unroll
+                for (int c = 0; c < kCrDh / 4; ++c)
+                    dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                part_lse[row] = lse2;
+            }
+            __threadfence();
+            named_bar_sync(1 + x, 128);
+            if (quad == 0 && lane == 0) {
+                int32_t *ticket = &tickets[((int64_t)p.split * a.H + p.head) * 2 + x];
+                const bool last = atomicAdd(ticket, 1) == p.parts - 1;
+                if (last) *ticket = 0;
+                last_in[x] = last;
+            }
+            named_bar_sync(1 + x, 128);
+            const bool last = last_in[x];
+            named_bar_sync(1 + x, 128);  // (last_in is free again)
+            if (!last) continue;
+            __threadfence();
+            // this warp's rows, a row at a time: lane i has columns 4 i ..
+            for (int i = 0; i < 32; ++i) {
+                const int rr = x * kCrTile + 32 * quad + i;
+                if (rr >= p.nrows) break;
+                const int64_t first = ((int64_t)p.row0 + rr) * a.H + p.head, pitch = (int64_t)p.nrows * a.H;
+                float top = -INFINITY;
+                for (int k = lane; k < p.parts; k += 32) top = fmaxf(top, __ldcg(part_lse + first + k * pitch));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float sum = 0.f;
+                if (top != -INFINITY) {
+                    for (int k = 0; k < p.parts; ++k) {
+                        const float f = ex2_approx(__ldcg(part_lse + first + k * pitch) - top);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_o + (first + k * pitch) * kCrDh) + lane);
+                        sum += f;
+                        acc.x = fmaf(f, v.x, acc.x);
+                        acc.y = fmaf(f, v.y, acc.y);
+                        acc.z = fmaf(f, v.z, acc.z);
+                        acc.w = fmaf(f, v.w, acc.w);
+                    }
+                    const float inv = 1.f / sum;
+                    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                }
+                const int64_t row = (int64_t)(p.q0 + rr) * a.H + p.head;
+                const Share sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse, row);
+                store4(a, row * kCrDh + 4 * lane, acc, sh);
+                __syncwarp();  // (lse may be before_lse itself)
+                if (a.lse && lane == 0) a.lse[row] = sh.lse;
+            }
+        }
+    }
+    grid_dep_launch();
+    if (!__syncthreads_and(ok ? 1 : 0)) {
+        if (threadIdx.x == 0) {
+            record_error(status, MLA_ERR_TIMEOUT);
+            hd->magic = 0;  // tickets and units are where they were left: the plan has to be made again
+        }
+        drain_pause();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    // the last CTA to leave sets the unit counter back for the plan's next call
+    if (match && threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(&counters[1], 1) == (int)gridDim.x - 1) counters[0] = counters[1] = 0;
+    }
+}
+
+bool tmap_bf16(CUtensorMap *m, const void *p, int rank, const uint64_t *d, const uint64_t *s, const uint32_t *b) {
+    return tmap_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rank, d, s, b);
+}
+
+// SMs of the current device (0: none), its cross kernels' shared memory granted.
+int cross_device() {
+    static int sms[64] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (sms[dev] > 0) return sms[dev];
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(cross_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<1>::kSmem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(cross_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<2>::kSmem) !=
+            cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    sms[dev] = n;
+    return n;
+}
+
+int device_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// Units and partial rows fit 32 bits.
+bool cross_shape_ok(int B, int H, int64_t total_q) {
+    return B <= (1 << 20) && H <= kMaxHeads && total_q <= (1 << 24);
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" size_t mla_cross_workspace_size(int B, int H, int64_t total_q, int num_sms) {
+    if (B < 1 || H < 1 || total_q < 0 || num_sms < 0 || num_sms > 4096 || !cross_shape_ok(B, H, total_q)) return 0;
+    if (num_sms == 0) num_sms = device_sms();
+    if (num_sms <= 0) return 0;
+    return cross_layout(B, H, total_q, num_sms).total;
+}
+
+extern "C" mla_status mla_cross_plan(const int32_t *cu_q, const int32_t *cu_k, int B, int H, int64_t total_q,
+                                     int64_t total_k, int causal, int num_sms, void *workspace, size_t ws_bytes,
+                                     void *stream) {
+    if (!workspace || !cu_q || !cu_k || B < 1 || H < 1 || total_q < 0 || total_k < 0 || num_sms < 0 || num_sms > 4096)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+    if (!cross_shape_ok(B, H, total_q) || total_k > INT32_MAX - kCrTile) return MLA_ERR_UNSUPPORTED;
+    if (num_sms == 0) num_sms = device_sms();
+    if (num_sms <= 0) return MLA_ERR_CUDA;
+    CrossPlanArgs a;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.B = B;
+    a.H = H;
+    a.total_q = (int)total_q;
+    a.total_k = (int)total_k;
+    a.causal = causal ? 1 : 0;
+    a.rows = cross_rows(B, total_q);
+    a.sms = num_sms;
+    a.ws = (unsigned char *)workspace;
+    a.L = cross_layout(B, H, total_q, num_sms);
+    if (ws_bytes < a.L.total) return MLA_ERR_WORKSPACE;
+    return launch_pdl(cross_plan_kernel, 1, kCpThreads, 0, (cudaStream_t)stream, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, const void *q_nope, const void *q_rope,
+                                          const void *entries, const void *k_nope, const void *v, int B, int H,
+                                          int64_t total_q, int64_t total_k, float softmax_scale, const float *before_out,
+                                          const float *before_lse, void *out, mla_out_dtype out_dtype, float *lse,
+                                          void *stream) {
+    if (!workspace || B < 1 || H < 1 || total_q < 0 || total_k < 0) return MLA_ERR_INVALID_ARG;
+    if (out_dtype != MLA_OUT_FP32 && out_dtype != MLA_OUT_BF16) return MLA_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || softmax_scale == INFINITY) return MLA_ERR_INVALID_ARG;
+    if ((q_rope == nullptr) != (entries == nullptr) && total_q > 0 && total_k > 0) return MLA_ERR_INVALID_ARG;
+    if ((before_out == nullptr) != (before_lse == nullptr)) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || !aligned16(q_nope) || !aligned16(q_rope) || !aligned16(entries) || !aligned16(k_nope) ||
+        !aligned16(v) || !aligned16(out) || !aligned16(before_out))
+        return MLA_ERR_INVALID_ARG;
+    if (!cross_shape_ok(B, H, total_q) || total_k > INT32_MAX - kCrTile) return MLA_ERR_UNSUPPORTED;
+    if (total_q == 0) return MLA_OK;
+    if (!q_nope || !out || (total_k > 0 && (!k_nope || !v))) return MLA_ERR_INVALID_ARG;
+    if (ws_bytes < cross_layout(B, H, total_q, 1).total) return MLA_ERR_WORKSPACE;
+    const int sms = cross_device();
+    if (sms <= 0) return MLA_ERR_CUDA;
+    // (without any key the maps stand for something that is never read)
+    const uint64_t nk = total_k > 0 ? (uint64_t)total_k : 1;
+    if (total_k == 0) k_nope = v = entries = q_rope = nullptr;
+    if (!k_nope) k_nope = v = q_nope;
+    const bool positions = q_rope != nullptr;
+    CUtensorMap tqn, tqr, tk, tkr, tv;
+    // q nope [total_q][H][128], q rope [total_q][H][64]: (cols, h, query); boxes of 64 columns x 128 queries
+    const uint64_t dqn[3] = {kCrDh, (uint64_t)H, (uint64_t)total_q}, sqn[2] = {kCrDh * 2, (uint64_t)kCrDh * 2 * H};
+    const uint64_t dqr[3] = {kDRope, (uint64_t)H, (uint64_t)total_q}, sqr[2] = {kDRope * 2, (uint64_t)kDRope * 2 * H};
+    const uint32_t bq[3] = {64, 1, kCrTile};
+    // k nope, v [H][total_k][128]: (cols, key, h); boxes of 64 columns x 128 keys
+    const uint64_t dkv[3] = {kCrDh, nk, total_k > 0 ? (uint64_t)H : 1}, skv[2] = {kCrDh * 2, (uint64_t)kCrDh * 2 * nk};
+    const uint32_t bkv[3] = {64, kCrTile, 1};
+    // RoPE keys: columns 512 .. 575 of the [total_k][576] entries
+    const uint64_t de[2] = {kDEntry, nk}, se[1] = {kDEntry * 2};
+    const uint32_t be[2] = {64, kCrTile};
+    if (!tmap_bf16(&tqn, q_nope, 3, dqn, sqn, bq) || !tmap_bf16(&tk, k_nope, 3, dkv, skv, bkv) ||
+        !tmap_bf16(&tv, v, 3, dkv, skv, bkv))
+        return MLA_ERR_CUDA;
+    tqr = tqn;
+    tkr = tk;
+    if (positions && (!tmap_bf16(&tqr, q_rope, 3, dqr, sqr, bq) || !tmap_bf16(&tkr, entries, 2, de, se, be)))
+        return MLA_ERR_CUDA;
+    CrossArgs a;
+    a.ws = (unsigned char *)workspace;
+    a.ws_bytes = ws_bytes;
+    a.B = B;
+    a.H = H;
+    a.total_q = (int)total_q;
+    a.total_k = (int)total_k;
+    a.rows = cross_rows(B, total_q);
+    a.scale_log2 = softmax_scale * kLog2e;
+    a.positions = positions;
+    a.before_out = before_out;
+    a.before_lse = before_lse;
+    a.out = out_dtype == MLA_OUT_FP32 ? (float *)out : nullptr;
+    a.out16 = out_dtype == MLA_OUT_BF16 ? (uint16_t *)out : nullptr;
+    a.lse = lse;
+    const cudaError_t e =
+        a.rows == kCrTile
+            ? launch_pdl(cross_kernel<1>, sms, Shape<1>::kThreads, Shape<1>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a)
+            : launch_pdl(cross_kernel<2>, sms, Shape<2>::kThreads, Shape<2>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a);
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}

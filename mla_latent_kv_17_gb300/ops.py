@@ -91,6 +91,12 @@ def lib():
             L.mla_decode_tree.restype = I
             L.mla_verify_draft.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P, P]
             L.mla_verify_draft.restype = I
+            L.mla_cross_workspace_size.argtypes = [I, I, I64, I]
+            L.mla_cross_workspace_size.restype = SZ
+            L.mla_cross_plan.argtypes = [P, P, I, I, I64, I64, I, I, P, SZ, P]
+            L.mla_cross_plan.restype = I
+            L.mla_cross_attention.argtypes = [P, SZ, P, P, P, P, P, I, I, I64, I64, F, P, P, P, I, P, P]
+            L.mla_cross_attention.restype = I
             L.mla_token_logprobs.argtypes = [P, I, I64, I64, I, P, F, I, P, P, P, P, P, P, P]
             L.mla_token_logprobs.restype = I
             L.mla_decode_status.argtypes = [P, SZ, P]
@@ -841,6 +847,90 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
     if st:
         _check("mla_verify_draft", st)
     return num, depths, nxt
+
+
+class CrossWorkspace:
+    """Device workspace of a cross attention of B query runs of H heads, total_q query rows in all: its
+    plan, partial results and status word (status() reads it)."""
+
+    def __init__(self, B: int, H: int, total_q: int, num_sms: int = 0, device=None):
+        self.B, self.H, self.total_q, self.num_sms = int(B), int(H), int(total_q), int(num_sms)
+        self.total_k = None
+        dev = torch.device(device if device is not None else "cuda")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        with _on(dev.index):
+            self.nbytes = int(lib().mla_cross_workspace_size(self.B, self.H, self.total_q, self.num_sms))
+            if self.nbytes == 0:
+                raise MlaError("mla_cross_workspace_size", 1, "invalid arguments")
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+            self.buf[:256].zero_()  # no plan yet, no error
+
+    def ptr(self):
+        return _ptr(self.buf)
+
+
+def plan_cross(ws: CrossWorkspace, cu_q, cu_k, total_k: int, causal: bool = False, stream=None):
+    """Builds the plan of cross_attention: run b's queries are rows cu_q[b] .. cu_q[b+1] of ws.total_q, its
+    keys rows cu_k[b] .. cu_k[b+1] of total_k (device int32 [B+1]); causal: a run's queries are its
+    last keys (the last one sees all of them, the one before all but the last)."""
+    dev = _device_of("cu_q cu_k workspace", cu_q, cu_k, ws.buf)
+    _ints(cu_q, (ws.B + 1,), "cu_q")
+    _ints(cu_k, (ws.B + 1,), "cu_k")
+    with _on(dev):
+        st = lib().mla_cross_plan(cu_q.data_ptr(), cu_k.data_ptr(), ws.B, ws.H, ws.total_q, total_k, 1 if causal else 0,
+                                  ws.num_sms, ws.buf.data_ptr(), ws.nbytes, _raw(stream, dev))
+    if st:
+        _check("mla_cross_plan", st)
+    ws.total_k = total_k
+    return ws
+
+
+def cross_attention(ws: CrossWorkspace, q_nope, q_rope, entries, k_nope, v, softmax_scale: float, before=None, out=None,
+                    lse=None, out_dtype=torch.float32, with_lse: bool = True, stream=None):
+    """Attention of the planned query runs to their key runs: q_nope bf16 [Nq,H,128], q_rope bf16
+    [Nq,H,64] and entries bf16 [Nk,576] (the keys' RoPE part; None for both: no positions), k_nope and v
+    bf16 [H,Nk,128] (as prefill_decompress gives them).  before = (out fp32, lse fp32): an earlier
+    result over other keys, which this one is joined with (they may be `out` and `lse` themselves).
+    -> (out fp32 or bf16 [Nq,H,128], lse fp32 [Nq,H] or None); rows outside every run are left as
+    they were (undefined where out is allocated here)."""
+    before_out, before_lse = before if before is not None else (None, None)
+    H, Nq = ws.H, ws.total_q
+    dev = _device_of("q_nope q_rope entries k_nope v before before_lse out lse workspace", q_nope, q_rope, entries, k_nope,
+                     v, before_out, before_lse, out, lse, ws.buf)
+    Nk = ws.total_k
+    if Nk is None:
+        raise ValueError("the workspace holds no plan (plan_cross)")
+    bf16, fp32 = torch.bfloat16, torch.float32
+    for t, shape, dtype, name in (
+            (q_nope, (Nq, H, 128), bf16, "q_nope"), (q_rope, (Nq, H, 64), bf16, "q_rope"),
+            (entries, (Nk, 576), bf16, "entries"), (k_nope, (H, Nk, 128), bf16, "k_nope"), (v, (H, Nk, 128), bf16, "v"),
+            (before_out, (Nq, H, 128), fp32, "before's out"), (before_lse, (Nq, H), fp32, "before's lse")):
+        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {'bf16' if dtype == bf16 else 'fp32'} {list(shape)}")
+    if (q_rope is None) != (entries is None):
+        raise ValueError("q_rope and entries: both or neither")
+    if (before_out is None) != (before_lse is None):
+        raise ValueError("before must hold out and lse")
+    with _on(dev):
+        if out is not None:
+            out_dtype = out.dtype
+        if out_dtype not in (fp32, bf16) or out is not None and (out.shape != (Nq, H, 128) or not out.is_contiguous()):
+            raise ValueError(f"out must be contiguous fp32 or bf16 [{Nq},{H},128]")
+        if out is None:
+            out = _new(q_nope, (Nq, H, 128), out_dtype, stream)
+        if lse is None:
+            if with_lse:
+                lse = _new(q_nope, (Nq, H), fp32, stream)
+        elif lse.dtype != fp32 or lse.shape != (Nq, H) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous fp32 [{Nq},{H}]")
+        st = lib().mla_cross_attention(
+            ws.buf.data_ptr(), ws.nbytes, q_nope.data_ptr(), _at(q_rope), _at(entries), k_nope.data_ptr(), v.data_ptr(),
+            ws.B, H, Nq, Nk, softmax_scale, _at(before_out), _at(before_lse), out.data_ptr(),
+            1 if out_dtype == bf16 else 0, _at(lse), _raw(stream, dev))
+    if st:
+        _check("mla_cross_attention", st)
+    return out, lse
 
 
 _LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}

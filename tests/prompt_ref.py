@@ -63,3 +63,41 @@ def logprobs(x, tokens, scale, top):
     alt[none] = -np.inf
     ids[:, :k][np.take_along_axis(x, order[:, :k], 1) == -np.inf] = -1
     return logprob, entropy, rank, ids, alt, below, logs
+
+
+def cross(q, k, v, cu_q, cu_k, scale, causal, before=None):
+    """q [Nq, H, d], k [H, Nk, d], v [H, Nk, 128] float64 -> out [Nq, H, 128], lse [Nq, H], the mean of
+    |v| under the weights [Nq, H, 128], and the largest sum_d |q_d k_d| of a row's keys [Nq, H]
+    (NaN in rows outside every run)."""
+    Nq, H = q.shape[:2]
+    out, lse = np.full((Nq, H, 128), np.nan), np.full((Nq, H), np.nan)
+    mean, dot = out.copy(), lse.copy()
+    for b in range(len(cu_q) - 1):
+        i0, i1, j0, j1 = cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1]
+        n, m = i1 - i0, j1 - j0
+        for h in range(H):
+            qs, ks, vs = q[i0:i1, h], k[h, j0:j1], v[h, j0:j1]
+            s = scale * qs @ ks.T
+            if causal:
+                s = np.where(np.arange(m)[None, :] <= np.arange(n)[:, None] + m - n, s, -np.inf)
+            top = s.max(1, initial=-np.inf, keepdims=True)
+            e = np.exp(s - np.where(top == -np.inf, 0.0, top))
+            total = e.sum(1, keepdims=True)
+            some = total > 0
+            w = np.where(some, e / np.where(some, total, 1.0), 0.0)
+            with np.errstate(divide="ignore"):
+                lse[i0:i1, h] = (np.log(total) + top)[:, 0]
+            out[i0:i1, h], mean[i0:i1, h] = w @ vs, w @ np.abs(vs)
+            seen = np.isfinite(s)
+            dot[i0:i1, h] = np.where(seen, np.abs(qs) @ np.abs(ks).T, 0.0).max(1, initial=0.0)
+    if before is not None:
+        o1, l1 = before
+        for b in range(len(cu_q) - 1):
+            r = slice(cu_q[b], cu_q[b + 1])
+            with np.errstate(invalid="ignore"):
+                both = np.logaddexp(l1[r], lse[r])
+                a1 = np.where(l1[r] == -np.inf, 0.0, np.exp(l1[r] - both))[..., None]
+                a2 = np.where(lse[r] == -np.inf, 0.0, np.exp(lse[r] - both))[..., None]
+            first = np.where(a1 > 0, o1[r], 0.0)
+            out[r], mean[r], lse[r] = a1 * first + a2 * out[r], a1 * np.abs(first) + a2 * mean[r], both
+    return out, lse, mean, dot

@@ -1,0 +1,294 @@
+"""Attention to key runs of another length on the GPU against a 64-bit restatement.
+
+Bounds (u = 2^-24).  A score is a sum of d = 128 or 192 exact products in fp32: off by at most
+d u scale sum |q k| =: e (absolute, in nats), and by 3 u of itself more for its factors.  A weight is
+off by 2 e + 2^-21 relative (its score, the row's maximum, the exponential) and by the rounding of
+the probability to bf16, 2^-8; the sum of weights by the same without the rounding, and by
+(128 / 4 + 8 + tiles) u for its additions.  So out is off by 2^-8 E|v| + (4 e + 2^-20 + K u) E|v| with
+E|v| the mean of |v| under the weights and K = 60 + keys (PV's additions), and lse by e + (K u + 2^-20),
+and 4 u |lse|.  A part in bf16 output adds 2^-8 |out|."""
+import numpy as np
+import pytest
+import torch
+
+from guards import Guarded
+from mla_latent_kv_17_gb300 import ops
+import prompt_ref
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from mla_latent_kv_17_gb300 import build
+    build.build()
+    ops.lib()
+
+
+class Case:
+    """Packed runs; rows before, between and behind them hold NaN (q, k, entries, v)."""
+
+    def __init__(self, q_lens, k_lens, H, positions, seed, spread=1.0, pad=0, before=False):
+        g = torch.Generator().manual_seed(seed)
+        randn = lambda *s: torch.randn(*s, generator=g).to(BF)
+        self.B, self.H, self.positions = len(q_lens), H, positions
+        self.cu_q = np.concatenate([[pad], pad + np.cumsum(q_lens)]).astype(np.int32)
+        self.cu_k = np.concatenate([[pad], pad + np.cumsum(k_lens)]).astype(np.int32)
+        self.nq, self.nk = int(self.cu_q[-1]) + pad, int(self.cu_k[-1]) + pad
+        self.q_nope, self.q_rope = randn(self.nq, H, 128), randn(self.nq, H, 64)
+        self.q_nope, self.q_rope = (t * spread for t in (self.q_nope, self.q_rope))
+        self.k_nope, self.v, self.entries = randn(H, self.nk, 128), randn(H, self.nk, 128), randn(self.nk, 576)
+        self.scale = float(np.float32(1 / np.sqrt(192 if positions else 128)))
+        self.before = None
+        if before:
+            lse = 2 + 2 * torch.randn(self.nq, H, generator=g)
+            out = torch.randn(self.nq, H, 128, generator=g)
+            gone = torch.rand(self.nq, H, generator=g) < 0.2
+            lse[gone] = -torch.inf
+            out[gone] = torch.nan
+            self.before = (out, lse)
+        if pad:
+            for t in (self.q_nope, self.q_rope):
+                t[:pad], t[-pad:] = torch.nan, torch.nan
+            self.entries[:pad], self.entries[-pad:] = torch.nan, torch.nan
+            for t in (self.k_nope, self.v):
+                t[:, :pad], t[:, -pad:] = torch.nan, torch.nan
+
+    def cuda(self):
+        for n in ("q_nope", "q_rope", "k_nope", "v", "entries"):
+            setattr(self, n, getattr(self, n).cuda())
+        self.d_cu = torch.from_numpy(self.cu_q).cuda(), torch.from_numpy(self.cu_k).cuda()
+        if self.before is not None:
+            self.before = tuple(t.cuda() for t in self.before)
+        return self
+
+    def run(self, causal=False, ws=None, **kw):
+        if ws is None:
+            ws = ops.CrossWorkspace(self.B, self.H, self.nq)
+        ops.plan_cross(ws, *self.d_cu, self.nk, causal=causal, stream=kw.get("stream"))
+        q_rope, entries = (self.q_rope, self.entries) if self.positions else (None, None)
+        got = ops.cross_attention(ws, self.q_nope, q_rope, entries, self.k_nope, self.v, self.scale, before=self.before, **kw)
+        self.ws = ws
+        return got
+
+    def check(self, got, causal=False):
+        assert ops.status(self.ws) == 0
+        num = lambda t: t.double().cpu().numpy()
+        q, k = num(self.q_nope), num(self.k_nope)
+        if self.positions:
+            q = np.concatenate([q, num(self.q_rope)], -1)
+            k = np.concatenate([k, np.broadcast_to(num(self.entries)[None, :, 512:], (self.H, self.nk, 64))], -1)
+        before = None if self.before is None else tuple(num(t) for t in self.before)
+        out, lse, mean, dot = prompt_ref.cross(q, k, num(self.v), self.cu_q, self.cu_k, self.scale, causal, before)
+        r = slice(self.cu_q[0], self.cu_q[-1])
+        out, lse, mean, dot = out[r], lse[r], mean[r], dot[r]
+        e = q.shape[-1] * U * self.scale * dot
+        K = 60 + int(np.diff(self.cu_k).max(initial=0))
+        go, gl = num(got[0])[r], got[1] if got[1] is None else num(got[1])[r]
+        bound = (2.0 ** -8 + 4 * e[..., None] + 2.0 ** -20 + K * U) * mean
+        if got[0].dtype == BF:
+            bound = bound + 2.0 ** -8 * (np.abs(out) + bound)
+        assert np.isfinite(go).all()
+        err = np.abs(go - out)
+        assert (err <= bound + 1e-30).all(), ("out", (err - bound).max(), np.argwhere(err > bound)[:4])
+        if gl is not None:
+            same = (gl == lse)
+            with np.errstate(invalid="ignore"):
+                ok = same | (np.abs(gl - lse) <= e + K * U + 2.0 ** -20 + 4 * U * np.abs(lse))
+            assert ok.all(), ("lse", gl[~ok][:4], lse[~ok][:4])
+
+
+@pytest.mark.parametrize("positions", [True, False])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,H", [
+    ([1], [1], 1), ([5], [3], 2), ([1], [300], 3), ([1, 1, 1], [128, 129, 127], 16), ([128], [128], 2),
+    ([129], [257], 2), ([256, 256], [512, 100], 3), ([257], [640], 9), ([300, 1, 77], [1000, 50, 129], 4),
+    ([700], [701], 10), ([0, 5, 0, 130], [40, 0, 0, 260], 3), ([40, 0], [0, 0], 2), ([3] * 20, list(range(0, 400, 20)), 5)])
+def test_cross(q_lens, k_lens, H, causal, positions):
+    c = Case(q_lens, k_lens, H, positions, sum(q_lens) + sum(k_lens) + H).cuda()
+    c.check(c.run(causal), causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("positions", [True, False])
+@pytest.mark.parametrize("q_len,k_lo,k_hi,B,H", [(1, 1, 700, 40, 16), (3, 130, 300, 64, 16), (150, 1, 500, 9, 128),
+                                                 (90, 100, 200, 10, 64)])
+def test_many_units_for_each_sm(q_len, k_lo, k_hi, B, H, causal, positions):
+    k_lens = [k_lo + (k_hi - k_lo) * ((i * 37) % B) // (B - 1) for i in range(B)]
+    c = Case([q_len] * B, k_lens, H, positions, B).cuda()
+    got = c.run(causal)
+    c.check(got, causal)
+    for _ in range(4):
+        again = c.run(causal, ws=c.ws)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,H", [
+    ([1], [20000], 1), ([1], [9000], 8), ([2, 1, 7], [100, 5000, 30], 4), ([130], [6000], 2), ([257], [9001], 1),
+    ([1, 1], [64, 16384], 3), ([400, 3], [3000, 7000], 2)])
+def test_keys_cut_into_pieces(q_lens, k_lens, H, causal):
+    c = Case(q_lens, k_lens, H, True, sum(k_lens)).cuda()
+    got = c.run(causal)
+    assert int(c.ws.buf[36:40].view(torch.int32)) > 0  # some item is cut
+    c.check(got, causal)
+    again = c.run(causal, ws=c.ws)  # tickets and units are back where they were
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,H", [([5, 3], [100, 61], 3), ([1, 200], [7000, 333], 2), ([300, 260], [0, 500], 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_joined_with_an_earlier_part(q_lens, k_lens, H, causal, dtype):
+    c = Case(q_lens, k_lens, H, True, 17 + H, before=True).cuda()
+    got = c.run(causal, out_dtype=dtype)
+    c.check(got, causal)
+    if dtype == torch.float32:  # in place
+        want = got
+        out, lse = c.before
+        got = c.run(causal, out=out, lse=lse)
+        assert got[0].data_ptr() == out.data_ptr()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_parts_of_the_keys_one_after_the_other():
+    # keys in three calls, each joined with those before, against one call: the same formula's bounds
+    c = Case([150, 20], [900, 300], 4, True, 5).cuda()
+    cuts = [np.array([0, 0]), np.array([100, 300]), np.array([500, 300]), np.array([900, 300])]
+    state = None
+    for lo, hi in zip(cuts, cuts[1:]):
+        part = Case([150, 20], list(hi - lo), 4, True, 5)
+        pick = np.concatenate([np.arange(a, b) + off for a, b, off in zip(lo, hi, (0, 900))])
+        for n in ("k_nope", "v"):
+            setattr(part, n, getattr(c, n)[:, pick].contiguous())
+        part.entries, part.q_nope, part.q_rope = c.entries[pick].contiguous(), c.q_nope, c.q_rope
+        part.before = state
+        state = part.cuda().run()
+    c.ws = part.ws
+    c.check(state)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_rows_outside_the_runs(dtype):
+    # what lies before and behind the runs holds NaN and is neither used nor written
+    for q_lens, k_lens in (([3, 9], [70, 200]), ([300, 40], [150, 5])):
+        c = Case(q_lens, k_lens, 3, True, 8, pad=37).cuda()
+        out = torch.full((c.nq, 3, 128), 5.0, dtype=dtype, device="cuda")
+        lse = torch.full((c.nq, 3), 5.0, device="cuda")
+        c.check(c.run(out=out, lse=lse))
+        for t in (out, lse):
+            assert bool((t[:37] == 5).all()) and bool((t[-37:] == 5).all())
+
+
+def test_peaked_scores_and_no_lse():
+    c = Case([200, 6], [3000, 900], 3, True, 12, spread=8.0).cuda()
+    got = c.run(True, with_lse=False, out_dtype=BF)
+    assert got[1] is None
+    c.check(got, True)
+    rising = Case([140], [1500], 2, False, 13).cuda()  # scores that grow along the keys: the reference moves
+    rising.q_nope.fill_(0.25)
+    rising.k_nope.copy_((torch.arange(1500, device="cuda") / 40.0).view(1, -1, 1).expand(2, 1500, 128).to(BF))
+    rising.check(rising.run())
+
+
+def test_no_write_outside_the_arrays():
+    for q_lens, k_lens, H in (([1, 2], [9000, 30], 3), ([300], [700], 2)):
+        c = Case(q_lens, k_lens, H, True, 3).cuda()
+        ws = ops.CrossWorkspace(c.B, H, c.nq)
+        g = [Guarded(ws.nbytes), Guarded(c.nq * H * 512), Guarded(c.nq * H * 4)]
+        ws.buf = g[0].inner
+        got = c.run(ws=ws, out=g[1].inner.view(torch.float32).view(c.nq, H, 128), lse=g[2].inner.view(torch.float32).view(c.nq, H))
+        c.check(got)
+        for b in g:
+            b.check("cross attention")
+
+
+def test_plan_serves_several_calls_and_a_captured_one():
+    c = Case([5, 300, 1], [400, 900, 4000], 4, True, 31).cuda()
+    want = c.run()
+    c.check(want)
+    call = lambda: ops.cross_attention(c.ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale)
+    for _ in range(3):
+        got = call()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.plan_cross(c.ws, *c.d_cu, c.nk)
+        got = call()
+    # other runs of the same rows, replayed
+    for q_lens, k_lens in (([5, 300, 1], [400, 900, 4000]), ([100, 0, 206], [5000, 300, 0]), ([306, 0, 0], [1, 2, 5297])):
+        c.cu_q = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+        c.cu_k = np.concatenate([[0], np.cumsum(k_lens)]).astype(np.int32)
+        c.d_cu[0].copy_(torch.from_numpy(c.cu_q))
+        c.d_cu[1].copy_(torch.from_numpy(c.cu_k))
+        graph.replay()
+        c.check(got)
+
+
+def test_two_streams():
+    a, b = Case([4, 260], [3000, 512], 4, True, 1).cuda(), Case([1, 1], [8000, 90], 16, False, 2).cuda()
+    want = [c.run() for c in (a, b)]  # (workspaces are made, and zeroed, on the current stream)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        gb = b.run(ws=b.ws, stream=side)
+        ga = a.run(ws=a.ws)
+        torch.cuda.synchronize()
+        for got, w in zip((ga, gb), want):
+            assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+
+
+def test_runs_that_fall_or_lie_outside_are_recorded():
+    c = Case([50, 60], [90, 100], 2, True, 3).cuda()
+    for cu_q, cu_k in (([0, 50, 40], [0, 90, 190]), ([-3, 50, 110], [0, 90, 190]), ([0, 50, 400], [0, 90, 190]),
+                       ([0, 50, 110], [0, 90, 5000]), ([0, 2 ** 31 - 1, -2 ** 31], [2 ** 31 - 1, -5, 190]),
+                       ([110, 0, 110], [190, 0, 190])):
+        ws = ops.CrossWorkspace(2, 2, c.nq)
+        ops.plan_cross(ws, torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+                       torch.tensor(cu_k, dtype=torch.int32, device="cuda"), c.nk)
+        ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale)
+        assert ops.status(ws) == 5
+    c.check(c.run())
+
+
+def test_a_workspace_without_a_matching_plan():
+    c = Case([50, 60], [90, 100], 2, True, 3).cuda()
+    ws = ops.CrossWorkspace(2, 2, c.nq)
+    with pytest.raises(ValueError, match="no plan"):
+        ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale)
+    ws.total_k = c.nk
+    ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale)
+    assert ops.status(ws) == 3
+    ops.plan_cross(ws, *c.d_cu, c.nk + 1)
+    ws.total_k = c.nk
+    ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale)
+    assert ops.status(ws) == 3
+
+
+def test_empty_and_refusals():
+    c = Case([50, 60], [90, 100], 2, True, 3).cuda()
+    ws = ops.CrossWorkspace(2, 2, 0)
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ops.plan_cross(ws, zero, c.d_cu[1], c.nk)
+    out, lse = ops.cross_attention(ws, c.q_nope[:0], c.q_rope[:0], c.entries, c.k_nope, c.v, c.scale)
+    assert out.shape == (0, 2, 128) and ops.status(ws) == 0
+    ws = ops.CrossWorkspace(2, 2, c.nq)  # no key at all
+    ops.plan_cross(ws, c.d_cu[0], zero, 0, causal=True)
+    out, lse = ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries[:0], c.k_nope[:, :0].contiguous(),
+                                   c.v[:, :0].contiguous(), c.scale)
+    assert bool((out == 0).all()) and bool((lse == -torch.inf).all()) and ops.status(ws) == 0
+    c.run()
+    good = dict(q_nope=c.q_nope, q_rope=c.q_rope, entries=c.entries, k_nope=c.k_nope, v=c.v, softmax_scale=c.scale)
+    o32, l32 = torch.zeros(c.nq, 2, 128, device="cuda"), torch.zeros(c.nq, 2, device="cuda")
+    for bad in (dict(q_rope=None), dict(entries=None), dict(q_nope=c.q_nope.float()), dict(v=c.v[:, :-1]),
+                dict(k_nope=c.k_nope.transpose(0, 1)), dict(softmax_scale=0.0), dict(softmax_scale=float("inf")),
+                dict(before=(o32, None)), dict(before=(o32.to(BF), l32)), dict(before=(o32, l32[:-1])),
+                dict(out=o32.half()), dict(out=o32[:-1]), dict(lse=l32.to(BF)), dict(out_dtype=torch.float16),
+                dict(q_nope=c.q_nope.cpu())):
+        with pytest.raises((ValueError, ops.MlaError)):
+            ops.cross_attention(c.ws, **{**good, **bad})
+    for bad in ((c.d_cu[0][:-1], c.d_cu[1]), (c.d_cu[0].long(), c.d_cu[1]), (c.d_cu[0].cpu(), c.d_cu[1])):
+        with pytest.raises(ValueError):
+            ops.plan_cross(c.ws, *bad, c.nk)

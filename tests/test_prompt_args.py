@@ -102,3 +102,48 @@ def test_token_logprobs_refuses(kw):
 def test_token_logprobs_limits():
     assert _score(top=65) == UNSUPPORTED and _score(V=(1 << 28) + 1) == UNSUPPORTED
     assert _score(N=0, x=0, tok=0, lp=0) == OK
+
+
+def _plan(**kw):
+    d = dict(q=A, k=A, B=2, H=4, nq=10, nk=20, causal=0, sms=152, ws=A, bytes=1 << 40)
+    d.update(kw)
+    return ops.lib().mla_cross_plan(P(d["q"]), P(d["k"]), d["B"], d["H"], d["nq"], d["nk"], d["causal"], d["sms"], P(d["ws"]),
+                                    d["bytes"], P(0))
+
+
+@pytest.mark.parametrize("kw", [dict(q=0), dict(k=0), dict(B=0), dict(H=0), dict(nq=-1), dict(nk=-1), dict(sms=-1),
+                                dict(sms=5000), dict(ws=0), dict(ws=A + 4)])
+def test_cross_plan_refuses(kw):
+    assert _plan(**kw) == INVALID
+
+
+def test_cross_plan_limits():
+    assert _plan(H=129) == UNSUPPORTED and _plan(B=(1 << 20) + 1) == UNSUPPORTED
+    assert _plan(nq=(1 << 24) + 1) == UNSUPPORTED and _plan(nk=2 ** 31) == UNSUPPORTED
+    need = ops.lib().mla_cross_workspace_size(2, 4, 10, 152)
+    assert need > 0 and _plan(bytes=need - 1) == 3  # MLA_ERR_WORKSPACE
+    for bad in ((0, 4, 10, 152), (2, 0, 10, 152), (2, 129, 10, 152), (2, 4, -1, 152), (2, 4, 10, -1), (2, 4, 1 << 25, 152)):
+        assert ops.lib().mla_cross_workspace_size(*bad) == 0
+
+
+def _cross(**kw):
+    d = dict(ws=A, bytes=1 << 40, qn=A, qr=A, e=A, k=A, v=A, B=2, H=4, nq=10, nk=20, scale=0.1, bo=0, bl=0, out=A, dt=0, lse=A)
+    d.update(kw)
+    return ops.lib().mla_cross_attention(P(d["ws"]), d["bytes"], P(d["qn"]), P(d["qr"]), P(d["e"]), P(d["k"]), P(d["v"]),
+                                         d["B"], d["H"], d["nq"], d["nk"], d["scale"], P(d["bo"]), P(d["bl"]), P(d["out"]),
+                                         d["dt"], P(d["lse"]), P(0))
+
+
+@pytest.mark.parametrize("kw", [dict(ws=0), dict(qn=0), dict(qr=0), dict(e=0), dict(k=0), dict(v=0), dict(B=0), dict(H=0),
+                                dict(nq=-1), dict(nk=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
+                                dict(scale=math.inf), dict(bo=A), dict(bl=A), dict(out=0), dict(dt=2), dict(qn=A + 2),
+                                dict(k=A + 8), dict(v=A + 4), dict(e=A + 2), dict(out=A + 4), dict(ws=A + 8),
+                                dict(bo=A + 4, bl=A)])
+def test_cross_attention_refuses(kw):
+    assert _cross(**kw) == INVALID
+
+
+def test_cross_attention_limits():
+    assert _cross(H=129) == UNSUPPORTED and _cross(nk=2 ** 31) == UNSUPPORTED
+    assert _cross(bytes=256) == 3
+    assert _cross(nq=0, qn=0, out=0) == OK
