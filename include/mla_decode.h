@@ -422,8 +422,8 @@ mla_status mla_verify_draft(const float *target, const float *draft, const int32
  * change, one call at a time, and holds the work list, partial results and the status word, which
  * mla_decode_status reads: runs that fall or lie outside are moved up or in and recorded as
  * MLA_ERR_INDEX.  After MLA_ERR_TIMEOUT the plan has to be made again.  num_sms as for
- * mla_decode_plan, the same in both calls.  1 <= B <= 2^20, total_q <= 2^24, 1 <= H <= 128; workspace
- * and tensors 16-byte aligned. */
+ * mla_decode_plan, the same in the first two calls.  1 <= B <= 2^20, total_q <= 2^24, 1 <= H <= 128;
+ * workspace and inputs 16-byte aligned, out and before_out 32-byte. */
 size_t mla_cross_workspace_size(int B, int H, int64_t total_q, int num_sms);
 
 mla_status mla_cross_plan(const int32_t *cu_q, const int32_t *cu_k, int B, int H, int64_t total_q, int64_t total_k,

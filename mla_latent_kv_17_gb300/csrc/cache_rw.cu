@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "rotary.cuh"
 #include "tc_util.cuh"
 
@@ -78,27 +79,6 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
     return d;
 }
 
-// Pairs of fp32 values in one 64-bit register pair, for the packed fp32 instructions.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ float2 halves(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 __device__ __forceinline__ void unpack_pairs(uint4 v, uint64_t *f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -15,8 +15,7 @@
 //   256 rows: two query tiles share the keys and take turns on the tensor pipe.
 //   128 rows: one query tile, scores and values double-buffered, for short runs, where the keys'
 //   and values' way from memory bounds the call.
-// The pieces of an item leave normalised partial results; the one that comes last (a ticket per item,
-// head and tile) joins them, in the pieces' order.
+// The pieces of an item leave normalised partial results, which cross_merge_kernel joins.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,6 +23,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "mla_decode.h"
 #include "sm103_ptx.cuh"
 #include "tc_util.cuh"
@@ -44,7 +44,7 @@ constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
 
 struct CrossHeader {
     uint32_t magic;
-    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, partial_rows, reserved[5];
+    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, split_rows, reserved[5];
 };
 static_assert(sizeof(CrossHeader) == 64, "plan header is 64 bytes");
 
@@ -52,14 +52,18 @@ static_assert(sizeof(CrossHeader) == 64, "plan header is 64 bytes");
 // plan's row r sees the keys below see0 + r (0 and less: none), any other's all of them.
 struct CrossPiece {
     int32_t q0, nrows, k0, nk, see0, g0, g1;
-    int32_t part, parts;     // this piece of the item's
-    int32_t row0;            // the item's first partial row (part p: + p nrows)
-    int32_t split;           // the item's number among those cut
-    int32_t head;            // (filled in where a unit is taken)
+    int32_t row0;  // the piece's first partial row (-1: the item's only piece, its rows are the result)
+    int32_t head;  // (filled in where a unit is taken)
+    int32_t reserved[3];
+};
+// An item that is cut: its query rows, its parts' partial rows (part p: row0 + p nrows ..), and how many
+// rows the cut items before it have.
+struct CrossSplit {
+    int32_t q0, nrows, row0, parts, before;
 };
 
 struct CrossLayout {
-    size_t pieces, order, seqs, item_off, tickets, part_lse, part_o, total;
+    size_t pieces, order, splits, seqs, item_off, part_lse, part_o, total;
     int max_pieces, max_splits;
     int64_t max_rows;
 };
@@ -84,12 +88,12 @@ MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {
     o = align_up(o + sizeof(CrossPiece) * (size_t)L.max_pieces, 256);
     L.order = o;
     o = align_up(o + sizeof(int32_t) * (size_t)L.max_pieces, 256);
+    L.splits = o;
+    o = align_up(o + sizeof(CrossSplit) * (size_t)L.max_splits, 256);
     L.seqs = o;
     o = align_up(o + sizeof(int4) * (size_t)B, 256);
     L.item_off = o;
     o = align_up(o + sizeof(int32_t) * (size_t)(B + 1), 256);
-    L.tickets = o;
-    o = align_up(o + sizeof(int32_t) * (size_t)L.max_splits * H * 2, 256);
     L.part_lse = o;
     o = align_up(o + sizeof(float) * (size_t)L.max_rows * H, 256);
     L.part_o = o;
@@ -102,34 +106,50 @@ MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {
 constexpr int kCpThreads = 512;
 constexpr int kCpWarps = kCpThreads / 32;
 constexpr int kCpSort = 2048;  // pieces that are put in order (more of them even out by themselves)
+constexpr int kCpKeep = 1024;  // runs whose starts stay in shared memory
 
-struct Add {
-    __device__ __forceinline__ int64_t operator()(int64_t a, int64_t b) const { return a + b; }
+// Four values a thread, scanned together: sums, or maxima.
+struct Four {
+    int64_t v[4];
 };
-struct Max {
-    __device__ __forceinline__ int64_t operator()(int64_t a, int64_t b) const { return a > b ? a : b; }
-};
-
-// Inclusive scan of v over the block; *all receives the whole.  sh: kCpWarps values.
-template <typename Op>
-__device__ int64_t block_scan(int64_t v, Op op, int64_t *all, int64_t *sh) {
+template <bool kMax>
+__device__ __forceinline__ Four both(Four a, const Four &b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.v[i] = kMax ? (a.v[i] > b.v[i] ? a.v[i] : b.v[i]) : a.v[i] + b.v[i];
+    return a;
+}
+// Inclusive scan of the first kN of x over the block; *all receives the whole.  sh: kCpWarps places.
+template <bool kMax, int kN>
+__device__ Four block_scan(Four x, Four *all, Four *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = op(v, y);
+        Four y = x;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) y.v[i] = __shfl_up_sync(0xffffffffu, x.v[i], o);
+        if (lane >= o) x = both<kMax>(x, y);
     }
-    if (lane == 31) sh[warp] = v;
+    if (lane == 31) sh[warp] = x;
     __syncthreads();
-    int64_t before = 0, whole = sh[0];
-    for (int i = 0; i < kCpWarps; ++i) {
-        if (i == warp && i > 0) v = op(v, before);
-        before = i == 0 ? sh[0] : op(before, sh[i]);
-        whole = before;
+    // (a lane per warp: every warp scans the warps' wholes for itself)
+    Four t = sh[lane < kCpWarps ? lane : 0];
+    if (lane >= kCpWarps) t = Four{};
+#pragma unroll
+    for (int o = 1; o < kCpWarps; o <<= 1) {
+        Four y = t;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) y.v[i] = __shfl_up_sync(0xffffffffu, t.v[i], o);
+        if (lane >= o) t = both<kMax>(t, y);
     }
-    *all = whole;
+    Four before = x;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        before.v[i] = __shfl_sync(0xffffffffu, t.v[i], warp > 0 ? warp - 1 : 0);
+        all->v[i] = __shfl_sync(0xffffffffu, t.v[i], kCpWarps - 1);
+    }
+    if (warp > 0) x = both<kMax>(x, before);
     __syncthreads();
-    return v;
+    return x;
 }
 
 struct CrossPlanArgs {
@@ -139,7 +159,7 @@ struct CrossPlanArgs {
     CrossLayout L;
 };
 
-// Keys that the item's rows up to `end` (of nq) see.
+// Keys that the rows up to `end` (of nq) see.
 __device__ __forceinline__ int seen_by(int end, int nq, int nk, int causal) {
     if (!causal) return nk;
     const int s = nk - nq + end;
@@ -147,58 +167,67 @@ __device__ __forceinline__ int seen_by(int end, int nq, int nk, int causal) {
 }
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + kCrTile - 1) / kCrTile; }
 
-__global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const CrossPlanArgs a) {
-    __shared__ int64_t s_scan[kCpWarps];
-    __shared__ uint32_t s_key[kCpSort];
+__global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_constant__ CrossPlanArgs a) {
+    __shared__ Four s_scan[kCpWarps];
+    __shared__ __align__(16) uint32_t s_key[kCpSort];
+    __shared__ int4 s_seq[kCpKeep];
+    __shared__ int32_t s_off[kCpKeep];
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
-    int4 *seqs = reinterpret_cast<int4 *>(a.ws + a.L.seqs);
-    int32_t *item_off = reinterpret_cast<int32_t *>(a.ws + a.L.item_off);
+    const bool keep = a.B <= kCpKeep;
+    int4 *seqs = keep ? s_seq : reinterpret_cast<int4 *>(a.ws + a.L.seqs);
+    int32_t *item_off = keep ? s_off : reinterpret_cast<int32_t *>(a.ws + a.L.item_off);
     CrossPiece *pieces = reinterpret_cast<CrossPiece *>(a.ws + a.L.pieces);
+    CrossSplit *splits = reinterpret_cast<CrossSplit *>(a.ws + a.L.splits);
     int32_t *order = reinterpret_cast<int32_t *>(a.ws + a.L.order);
-    int32_t *tickets = reinterpret_cast<int32_t *>(a.ws + a.L.tickets);
     int *status = reinterpret_cast<int *>(a.ws + kCrStatus);
 
     // the runs: starts that fall or lie outside are moved up or in (and recorded), so that runs never
     // overlap and the items fit their places
-    int64_t q_upto = 0, k_upto = 0, items = 0, cost = 0;
+    Four upto{}, all;  // ends of the queries and keys so far
+    int64_t items = 0, cost = 0;
     for (int b0 = 0; b0 < a.B; b0 += kCpThreads) {
         const int b = b0 + tid;
-        int64_t q = 0, q2 = 0, k = 0, k2 = 0;
+        int qs = 0, qe = 0, ks = 0, ke = 0;
+        bool bad = false;
         if (b < a.B) {
             const int32_t r[4] = {a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]};
-            q = min(max(r[0], 0), a.total_q);
-            q2 = min(max(r[1], 0), a.total_q);
-            k = min(max(r[2], 0), a.total_k);
-            k2 = min(max(r[3], 0), a.total_k);
-            if (r[0] != q || r[1] != q2 || r[2] != k || r[3] != k2 || r[0] > r[1] || r[2] > r[3])
-                record_error(status, MLA_ERR_INDEX);
+            qs = min(max(r[0], 0), a.total_q);
+            qe = min(max(r[1], 0), a.total_q);
+            ks = min(max(r[2], 0), a.total_k);
+            ke = min(max(r[3], 0), a.total_k);
+            bad = r[0] != qs || r[1] != qe || r[2] != ks || r[3] != ke || qs > qe || ks > ke;
+            if (bad) record_error(status, MLA_ERR_INDEX);
         }
-        int64_t all;
-        // ends so far, this run's own among them; a run starts no earlier than they do before it
-        const int64_t qe = max(q_upto, block_scan(max(q, q2), Max(), &all, s_scan));
-        const int64_t q_all = max(q_upto, all);
-        const int64_t ke = max(k_upto, block_scan(max(k, k2), Max(), &all, s_scan));
-        const int64_t k_all = max(k_upto, all);
-        // (the start: the maximum of everything before cu[b + 1])
-        const int64_t qs = max(q_upto, block_scan(q, Max(), &all, s_scan));
-        const int64_t ks = max(k_upto, block_scan(k, Max(), &all, s_scan));
-        const int nq = b < a.B ? (int)(qe - qs) : 0, nk = b < a.B ? (int)(ke - ks) : 0;
+        if (__syncthreads_or(bad) || upto.v[1] > 0 || upto.v[3] > 0) {
+            // a run starts no earlier than the largest start before it, and ends no earlier
+            const Four x = block_scan<true, 4>(Four{{qs, max(qs, qe), ks, max(ks, ke)}}, &all, s_scan);
+            qs = (int)max(upto.v[1], x.v[0]);
+            qe = (int)max(upto.v[1], x.v[1]);
+            ks = (int)max(upto.v[3], x.v[2]);
+            ke = (int)max(upto.v[3], x.v[3]);
+            upto = both<true>(upto, all);
+        } else if (a.B > kCpThreads) {
+            block_scan<true, 4>(Four{{qs, qe, ks, ke}}, &all, s_scan);
+            upto = all;
+        }
+        const int nq = b < a.B ? qe - qs : 0, nk = b < a.B ? ke - ks : 0;
         const int tiles = (nq + a.rows - 1) / a.rows;
         int64_t c = 0;
-        for (int j = 0; j < tiles; ++j)
-            c += kCrItemCost + key_tiles(seen_by(min(nq, (j + 1) * a.rows), nq, nk, a.causal));
-        const int64_t upto = items + block_scan(tiles, Add(), &all, s_scan);
-        items += all;
-        block_scan(c, Add(), &all, s_scan);
-        cost += all;
-        if (b < a.B) {
-            seqs[b] = make_int4((int)qs, nq, (int)ks, nk);
-            item_off[b] = (int32_t)(upto - tiles);
+        if (!a.causal) {
+            c = (int64_t)tiles * (kCrItemCost + key_tiles(nk));
+        } else {
+            for (int j = 0; j < tiles; ++j)
+                c += kCrItemCost + key_tiles(seen_by(min(nq, (j + 1) * a.rows), nq, nk, 1));
         }
-        q_upto = q_all;
-        k_upto = k_all;
+        const Four x = block_scan<false, 2>(Four{{tiles, c, 0, 0}}, &all, s_scan);
+        if (b < a.B) {
+            seqs[b] = make_int4(qs, nq, ks, nk);
+            item_off[b] = (int32_t)(items + x.v[0] - tiles);
+        }
+        items += all.v[0];
+        cost += all.v[1];
     }
     __syncthreads();
 
@@ -206,12 +235,11 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const CrossPlanA
     const int64_t shares = (int64_t)kCrShare * a.sms;
     const int64_t share = (cost * a.H + shares - 1) / shares;
     const int target = (int)(share > kCrMinPiece ? share : kCrMinPiece);
-    int64_t n_pieces = 0, n_splits = 0, n_rows = 0;
-    for (int64_t i0 = 0; i0 < items; i0 += kCpThreads) {
-        const int64_t i = i0 + tid;
-        int n = 0;
+    Four done{};  // pieces, cut items, their partial rows, their rows
+    for (int i0 = 0; i0 < items; i0 += kCpThreads) {
+        const int i = i0 + tid;
+        int n = 0, tiles = 0;
         CrossPiece p = {};
-        int tiles = 0;
         if (i < items) {
             int lo = 0, hi = a.B - 1;  // the last run that starts at or before item i (empty runs share a start)
             while (lo < hi) {
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const CrossPlanA
                     hi = mid - 1;
             }
             const int4 s = seqs[lo];
-            const int r0 = (int)(i - item_off[lo]) * a.rows;
+            const int r0 = (i - item_off[lo]) * a.rows;
             p.nrows = min(a.rows, s.y - r0);
             p.q0 = s.x + r0;
             p.k0 = s.z;
@@ -231,50 +259,49 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const CrossPlanA
             tiles = key_tiles(seen_by(r0 + p.nrows, s.y, s.w, a.causal));
             n = tiles > target ? (tiles + target - 1) / target : 1;
         }
-        int64_t all;
-        const int64_t at = n_pieces + block_scan(n, Add(), &all, s_scan) - n;
-        n_pieces += all;
-        const int64_t sp = n_splits + block_scan(n > 1, Add(), &all, s_scan) - (n > 1);
-        n_splits += all;
-        const int64_t rows = n > 1 ? (int64_t)n * p.nrows : 0;
-        const int64_t row0 = n_rows + block_scan(rows, Add(), &all, s_scan) - rows;
-        n_rows += all;
+        int at = i;  // (nothing cut: each item is a piece)
+        int64_t row0 = -1;
+        if (__syncthreads_or(n > 1) || done.v[1] > 0) {
+            const int cut = n > 1;
+            const Four mine{{n, cut, cut ? (int64_t)n * p.nrows : 0, cut ? p.nrows : 0}};
+            const Four x = block_scan<false, 4>(mine, &all, s_scan);
+            at = (int)(done.v[0] + x.v[0] - n);
+            if (cut) {
+                row0 = done.v[2] + x.v[2] - mine.v[2];
+                splits[done.v[1] + x.v[1] - 1] = CrossSplit{p.q0, p.nrows, (int32_t)row0, n,
+                                                            (int32_t)(done.v[3] + x.v[3] - mine.v[3])};
+            }
+            done = both<false>(done, all);
+        } else {
+            done.v[0] += min((int64_t)kCpThreads, items - i0);
+        }
         for (int k = 0; k < n; ++k) {
             p.g0 = (int)((int64_t)tiles * k / n);
             p.g1 = (int)((int64_t)tiles * (k + 1) / n);
-            p.part = k;
-            p.parts = n;
-            p.row0 = (int)row0;
-            p.split = (int)sp;
+            p.row0 = n > 1 ? (int)(row0 + (int64_t)k * p.nrows) : -1;
             pieces[at + k] = p;
             if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(p.g1 - p.g0, 0xFFFF)) << 16 | (uint32_t)(at + k);
         }
     }
-    for (int64_t i = tid; i < n_splits * a.H * 2; i += kCpThreads) tickets[i] = 0;
     __syncthreads();
 
-    // longest first
-    if (n_pieces > 1 && n_pieces <= kCpSort) {
-        int n = 2;
-        while (n < n_pieces) n *= 2;
-        for (int i = (int)n_pieces + tid; i < n; i += kCpThreads) s_key[i] = 0xFFFFFFFFu;
+    // longest first: a piece's place is the number of smaller keys (all different)
+    const int np = (int)done.v[0];
+    if (np <= kCpSort) {
+        const int whole = (np + 3) & ~3;
+        if (tid < whole - np) s_key[np + tid] = 0xFFFFFFFFu;
         __syncthreads();
-        for (int w = 2; w <= n; w *= 2) {
-            for (int d = w / 2; d > 0; d /= 2) {
-                for (int i = tid; i < n / 2; i += kCpThreads) {
-                    const int x = 2 * d * (i / d) + i % d, y = x + d;
-                    const uint32_t u = s_key[x], v = s_key[y];
-                    if ((u > v) == ((x & w) == 0)) {
-                        s_key[x] = v;
-                        s_key[y] = u;
-                    }
-                }
-                __syncthreads();
+        for (int i = tid; i < np; i += kCpThreads) {
+            const uint32_t key = s_key[i];
+            int place = 0;
+            for (int j = 0; j < whole; j += 4) {
+                const uint4 k4 = *reinterpret_cast<const uint4 *>(s_key + j);
+                place += (k4.x < key) + (k4.y < key) + (k4.z < key) + (k4.w < key);
             }
+            order[place] = i;
         }
-        for (int i = tid; i < n_pieces; i += kCpThreads) order[i] = (int32_t)(s_key[i] & 0xFFFFu);
     } else {
-        for (int64_t i = tid; i < n_pieces; i += kCpThreads) order[i] = (int32_t)i;
+        for (int i = tid; i < np; i += kCpThreads) order[i] = i;
     }
     if (tid == 0) {
         int *counters = reinterpret_cast<int *>(a.ws + kCrCounters);
@@ -288,9 +315,9 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const CrossPlanA
         h.causal = a.causal;
         h.rows = a.rows;
         h.sms = a.sms;
-        h.pieces = (int32_t)n_pieces;
-        h.splits = (int32_t)n_splits;
-        h.partial_rows = (int32_t)n_rows;
+        h.pieces = np;
+        h.splits = (int32_t)done.v[1];
+        h.split_rows = (int32_t)done.v[3];
         *reinterpret_cast<CrossHeader *>(a.ws) = h;
     }
 }
@@ -336,22 +363,67 @@ __device__ __forceinline__ Share share_of(float lse, const float *before, int64_
     }
     return s;
 }
-__device__ __forceinline__ void store4(const CrossArgs &a, int64_t at, float4 o, const Share &s) {
-    o.x *= s.mine;
-    o.y *= s.mine;
-    o.z *= s.mine;
-    o.w *= s.mine;
+// 32 bytes at once (both directions; a row's thread then touches each sector once).
+__device__ __forceinline__ void ld_global8(const float *p, float (&v)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void st_global8(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// 32 values of the result's row from element `at` on: f times o, and the earlier part's share.
+__device__ __forceinline__ void store32(const CrossArgs &a, int64_t at, const uint32_t (&o)[32], float f, const Share &s) {
+    float y[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * f;
     if (s.before != 0.f) {  // (what has no weight may hold anything)
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+            float v[8];
+            ld_global8(a.before_out + at + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[c + i] = fmaf(v[i], s.before, y[c + i]);
+        }
+    }
+    if (a.out) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(y[c + i]);
+            st_global8(a.out + at + c, w);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(y[c + 2 * i], y[c + 2 * i + 1]);
+            st_global8(a.out16 + at + c, w);
+        }
+    }
+}
+// The same for four values, scaled already.
+__device__ __forceinline__ void store4(const CrossArgs &a, int64_t at, float4 o, float before) {
+    if (before != 0.f) {
         const float4 b = *reinterpret_cast<const float4 *>(a.before_out + at);
-        o.x = fmaf(b.x, s.before, o.x);
-        o.y = fmaf(b.y, s.before, o.y);
-        o.z = fmaf(b.z, s.before, o.z);
-        o.w = fmaf(b.w, s.before, o.w);
+        o = make_float4(fmaf(b.x, before, o.x), fmaf(b.y, before, o.y), fmaf(b.z, before, o.z), fmaf(b.w, before, o.w));
     }
     if (a.out)
         *reinterpret_cast<float4 *>(a.out + at) = o;
     else
         *reinterpret_cast<uint2 *>(a.out16 + at) = make_uint2(bf16x2_bits(o.x, o.y), bf16x2_bits(o.z, o.w));
+}
+
+// True when the workspace holds a plan made for this call.
+__device__ __forceinline__ bool plan_fits(const CrossArgs &a, const CrossHeader *hd) {
+    return hd->magic == kCrossMagic && hd->B == a.B && hd->H == a.H && hd->total_q == a.total_q &&
+           hd->total_k == a.total_k && hd->rows == a.rows && hd->sms > 0 &&
+           cross_layout(a.B, a.H, a.total_q, hd->sms).total <= a.ws_bytes;
 }
 
 template <int kTiles>
@@ -385,7 +457,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     CrossPiece *slots = reinterpret_cast<CrossPiece *>(gbase + S::kOffBar + 192);  // two of 48 bytes
     int *abort_flag = reinterpret_cast<int *>(gbase + S::kOffBar + 288);
     volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(gbase + S::kOffBar + 296);
-    volatile int *last_in = reinterpret_cast<volatile int *>(gbase + S::kOffBar + 304);  // per query tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0) {
@@ -420,9 +491,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int *status = reinterpret_cast<int *>(a.ws + kCrStatus);
     int *counters = reinterpret_cast<int *>(a.ws + kCrCounters);
     CrossHeader *hd = reinterpret_cast<CrossHeader *>(a.ws);
-    const bool match = hd->magic == kCrossMagic && hd->B == a.B && hd->H == a.H && hd->total_q == a.total_q &&
-                       hd->total_k == a.total_k && hd->rows == a.rows && hd->sms > 0 &&
-                       cross_layout(a.B, a.H, a.total_q, hd->sms).total <= a.ws_bytes;
+    const bool match = plan_fits(a, hd);
     if (!match && threadIdx.x == 0) record_error(status, MLA_ERR_WORKSPACE);
     const int step = hd->causal ? 1 : 0;
     bool ok = true;
@@ -625,7 +694,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         const CrossLayout L = cross_layout(a.B, a.H, a.total_q, hd->sms);
         float *part_lse = reinterpret_cast<float *>(a.ws + L.part_lse);
         float *part_o = reinterpret_cast<float *>(a.ws + L.part_o);
-        int32_t *tickets = reinterpret_cast<int32_t *>(a.ws + L.tickets);
         const int x = warp >> 2, quad = warp & 3;
         const int r = x * kCrTile + 32 * quad + lane;  // the item's row
         const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
@@ -647,45 +715,49 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 tc_fence_after();
                 const uint32_t cS = tmem + lane_base + (kTiles == 2 ? 256u * x : 128u * j);
                 float s[kCrTile];
+                {
+                    uint32_t v[4][32];
 #pragma unroll
-                for (int c = 0; c < kCrTile / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(cS + 32u * c, v);
+                    for (int c = 0; c < 4; ++c) tmem_ld32(cS + 32u * c, v[c]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(v[i]);
+                    for (int c = 0; c < kCrTile; ++c) s[c] = __uint_as_float(v[c / 32][c % 32]);
                 }
                 const int lim = see - (p.g0 + g) * kCrTile;  // columns c < lim are seen
                 if (__any_sync(0xffffffffu, lim < kCrTile)) {
 #pragma unroll
                     for (int c = 0; c < kCrTile; ++c) s[c] = c < lim ? s[c] : -INFINITY;
                 }
-                float mxs[8];
+                float mxs[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int c = 0; c < 8; ++c) mxs[c] = s[c];
+                for (int c = 4; c + 8 <= kCrTile; c += 8) {
 #pragma unroll
-                for (int c = 8; c < kCrTile; ++c) mxs[c & 7] = fmaxf(mxs[c & 7], s[c]);
-                const float mx = fmaxf(m, a.scale_log2 * fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
-                                                               fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7]))));
+                    for (int k = 0; k < 4; ++k) mxs[k] = max3(mxs[k], s[c + k], s[c + 4 + k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mxs[k] = fmaxf(mxs[k], s[kCrTile - 4 + k]);
+                const float mx = fmaxf(m, a.scale_log2 * max3(mxs[0], mxs[1], fmaxf(mxs[2], mxs[3])));
                 // the reference moves only when exceeded by 2^8 (probabilities stay <= 2^8), so most tiles leave
                 // O alone; a row that has seen no key yet keeps -inf, probabilities of 0 and an O of 0
                 const float mref = (m == -INFINITY || mx > m + kCrRescale) ? mx : m;
                 const float alpha = m == -INFINITY ? 1.f : ex2_approx(m - mref);
                 const float sub = mref == -INFINITY ? 0.f : -mref;
-                float sums[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = pair(a.scale_log2, a.scale_log2), sub2 = pair(sub, sub);
+                uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float p0 = ex2_approx(fmaf(s[64 * c + 2 * i], a.scale_log2, sub));
-                        const float p1 = ex2_approx(fmaf(s[64 * c + 2 * i + 1], a.scale_log2, sub));
-                        sums[i & 3] += p0 + p1;
+                        const float2 y = halves(fma2(pair(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), c2, sub2));
+                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                        sums[i & 3] = add2(sums[i & 3], pair(p0, p1));
                         pk[i] = bf16x2_bits(p0, p1);
                     }
                     tmem_st32(cS + 32u * c, pk);
                 }
-                l = l * alpha + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
+                const float2 sum = halves(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+                l = l * alpha + (sum.x + sum.y);
                 m = mref;
                 // O is rescaled (rarely) once the previous PV has finished; the next waits for this P
                 if (g > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -710,99 +782,56 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             if (!ok) break;
             t += nt;
-            // the result's row, normalised
-            float o[kCrDh];
-#pragma unroll
-            for (int c = 0; c < kCrDh; ++c) o[c] = 0.f;
+            // the row's result, 32 columns at a time, normalised: the whole of it, or a piece's part
+            const float lse2 = l == 0.f ? -INFINITY : m + log2f(l), inv = l == 0.f ? 0.f : 1.f / l;
+            const bool whole = p.row0 < 0, mine = r < p.nrows;
+            const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
+            const int64_t part_row = (int64_t)(p.row0 + r) * a.H + p.head;
+            Share sh{1.f, 0.f, 0.f};
+            if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse, row);
             if (nt > 0) {
                 ok = wait_pv(t - 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                for (int c = 0; c < kCrDh / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(cO + 32u * c, v);
+            }
+#pragma unroll 1
+            for (int c = 0; c < kCrDh; c += 32) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tmem_ld32(cO + c, o);
                     tmem_wait_ld();
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[32 * c + i] = __uint_as_float(v[i]) * inv;
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
+                if (!mine) continue;
+                if (whole) {
+                    store32(a, row * kCrDh + c, o, inv * sh.mine, sh);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(o[k + i]) * inv);
+                        st_global8(part_o + part_row * kCrDh + c + k, v);
+                    }
+                }
+            }
+            if (nt > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_free(x));
             }
-            const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-            if (p.parts == 1) {
-                if (r < p.nrows) {
-                    const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
-                    const Share sh = share_of(lse2 * kLn2, a.before_lse, row);
-#pragma unroll
-                    for (int c = 0; c < kCrDh; c += 4)
-                        store4(a, row * kCrDh + c, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]), sh);
-                    if (a.lse) a.lse[row] = sh.lse;
-                }
-                continue;
-            }
-            if (x * kCrTile >= p.nrows) continue;  // (the same for the query tile's warps)
-            if (r < p.nrows) {
-                const int64_t row = ((int64_t)p.row0 + (int64_t)p.part * p.nrows + r) * a.H + p.head;
-                float4 *dst = reinterpret_cast<float4 *>(part_o + row * kCrDh);
-#pragma unroll
-                for (int c = 0; c < kCrDh / 4; ++c)
-                    dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                part_lse[row] = lse2;
-            }
-            __threadfence();
-            named_bar_sync(1 + x, 128);
-            if (quad == 0 && lane == 0) {
-                int32_t *ticket = &tickets[((int64_t)p.split * a.H + p.head) * 2 + x];
-                const bool last = atomicAdd(ticket, 1) == p.parts - 1;
-                if (last) *ticket = 0;
-                last_in[x] = last;
-            }
-            named_bar_sync(1 + x, 128);
-            const bool last = last_in[x];
-            named_bar_sync(1 + x, 128);  // (last_in is free again)
-            if (!last) continue;
-            __threadfence();
-            // this warp's rows, a row at a time: lane i has columns 4 i ..
-            for (int i = 0; i < 32; ++i) {
-                const int rr = x * kCrTile + 32 * quad + i;
-                if (rr >= p.nrows) break;
-                const int64_t first = ((int64_t)p.row0 + rr) * a.H + p.head, pitch = (int64_t)p.nrows * a.H;
-                float top = -INFINITY;
-                for (int k = lane; k < p.parts; k += 32) top = fmaxf(top, __ldcg(part_lse + first + k * pitch));
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float sum = 0.f;
-                if (top != -INFINITY) {
-                    for (int k = 0; k < p.parts; ++k) {
-                        const float f = ex2_approx(__ldcg(part_lse + first + k * pitch) - top);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_o + (first + k * pitch) * kCrDh) + lane);
-                        sum += f;
-                        acc.x = fmaf(f, v.x, acc.x);
-                        acc.y = fmaf(f, v.y, acc.y);
-                        acc.z = fmaf(f, v.z, acc.z);
-                        acc.w = fmaf(f, v.w, acc.w);
-                    }
-                    const float inv = 1.f / sum;
-                    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                }
-                const int64_t row = (int64_t)(p.q0 + rr) * a.H + p.head;
-                const Share sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse, row);
-                store4(a, row * kCrDh + 4 * lane, acc, sh);
-                __syncwarp();  // (lse may be before_lse itself)
-                if (a.lse && lane == 0) a.lse[row] = sh.lse;
-            }
+            if (mine && whole && a.lse) a.lse[row] = sh.lse;
+            if (mine && !whole) part_lse[part_row] = lse2;
         }
     }
     grid_dep_launch();
     if (!__syncthreads_and(ok ? 1 : 0)) {
         if (threadIdx.x == 0) {
             record_error(status, MLA_ERR_TIMEOUT);
-            hd->magic = 0;  // tickets and units are where they were left: the plan has to be made again
+            hd->magic = 0;  // units are where they were left: the plan has to be made again
         }
         drain_pause();
     }
@@ -816,6 +845,71 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     if (match && threadIdx.x == 0) {
         __threadfence();
         if (atomicAdd(&counters[1], 1) == (int)gridDim.x - 1) counters[0] = counters[1] = 0;
+    }
+}
+
+// The items that were cut: a warp joins the parts of a row of one head (lane i: columns 4 i .. 4 i + 3),
+// all of them in the parts' order.
+constexpr int kCmThreads = 256;
+constexpr int kCmCtasPerSm = 4;
+constexpr int kCmParts = 8;  // in flight together
+__global__ void __launch_bounds__(kCmThreads) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const CrossHeader *hd = reinterpret_cast<const CrossHeader *>(a.ws);
+    if (!plan_fits(a, hd) || hd->splits == 0) return;
+    const CrossLayout L = cross_layout(a.B, a.H, a.total_q, hd->sms);
+    const CrossSplit *splits = reinterpret_cast<const CrossSplit *>(a.ws + L.splits);
+    const float *part_lse = reinterpret_cast<const float *>(a.ws + L.part_lse);
+    const float *part_o = reinterpret_cast<const float *>(a.ws + L.part_o);
+    const int lane = threadIdx.x & 31, n_splits = hd->splits;
+    const int64_t tasks = (int64_t)hd->split_rows * a.H, warps = (int64_t)gridDim.x * (kCmThreads / 32);
+    for (int64_t t = (int64_t)blockIdx.x * (kCmThreads / 32) + (threadIdx.x >> 5); t < tasks; t += warps) {
+        const int at = (int)(t / a.H), h = (int)(t - (int64_t)at * a.H);
+        int lo = 0, hi = n_splits - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (splits[mid].before <= at)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const CrossSplit s = splits[lo];
+        const int64_t first = (int64_t)(s.row0 + at - s.before) * a.H + h, pitch = (int64_t)s.nrows * a.H;
+        const int64_t row = (int64_t)(s.q0 + at - s.before) * a.H + h;
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < s.parts; k0 += kCmParts) {
+            float l[kCmParts];
+            float4 v[kCmParts];
+#pragma unroll
+            for (int k = 0; k < kCmParts; ++k) {
+                const bool is = k0 + k < s.parts;
+                l[k] = is ? part_lse[first + (k0 + k) * pitch] : -INFINITY;
+                v[k] = is ? reinterpret_cast<const float4 *>(part_o + (first + (k0 + k) * pitch) * kCrDh)[lane]
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float m = top;
+#pragma unroll
+            for (int k = 0; k < kCmParts; ++k) m = fmaxf(m, l[k]);
+            if (m == -INFINITY) continue;  // no key seen so far
+            const float f = ex2_approx(top - m);
+            sum *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int k = 0; k < kCmParts; ++k) {
+                const float w = ex2_approx(l[k] - m);
+                sum += w;
+                acc = make_float4(fmaf(w, v[k].x, acc.x), fmaf(w, v[k].y, acc.y), fmaf(w, v[k].z, acc.z),
+                                  fmaf(w, v[k].w, acc.w));
+            }
+            top = m;
+        }
+        const Share sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse, row);
+        const float f = sum == 0.f ? 0.f : sh.mine / sum;
+        store4(a, row * kCrDh + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), sh.before);
+        __syncwarp();  // (lse may be before_lse itself)
+        if (a.lse && lane == 0) a.lse[row] = sh.lse;
     }
 }
 
@@ -903,7 +997,8 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     if ((q_rope == nullptr) != (entries == nullptr) && total_q > 0 && total_k > 0) return MLA_ERR_INVALID_ARG;
     if ((before_out == nullptr) != (before_lse == nullptr)) return MLA_ERR_INVALID_ARG;
     if (!aligned16(workspace) || !aligned16(q_nope) || !aligned16(q_rope) || !aligned16(entries) || !aligned16(k_nope) ||
-        !aligned16(v) || !aligned16(out) || !aligned16(before_out))
+        !aligned16(v) ||
+        (reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(before_out)) % 32 != 0)
         return MLA_ERR_INVALID_ARG;
     if (!cross_shape_ok(B, H, total_q) || total_k > INT32_MAX - kCrTile) return MLA_ERR_UNSUPPORTED;
     if (total_q == 0) return MLA_OK;
@@ -949,9 +1044,10 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     a.out = out_dtype == MLA_OUT_FP32 ? (float *)out : nullptr;
     a.out16 = out_dtype == MLA_OUT_BF16 ? (uint16_t *)out : nullptr;
     a.lse = lse;
-    const cudaError_t e =
+    cudaError_t e =
         a.rows == kCrTile
             ? launch_pdl(cross_kernel<1>, sms, Shape<1>::kThreads, Shape<1>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a)
             : launch_pdl(cross_kernel<2>, sms, Shape<2>::kThreads, Shape<2>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a);
+    if (e == cudaSuccess) e = launch_pdl(cross_merge_kernel, kCmCtasPerSm * sms, kCmThreads, 0, (cudaStream_t)stream, a);
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

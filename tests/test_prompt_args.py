@@ -138,7 +138,7 @@ def _cross(**kw):
                                 dict(nq=-1), dict(nk=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
                                 dict(scale=math.inf), dict(bo=A), dict(bl=A), dict(out=0), dict(dt=2), dict(qn=A + 2),
                                 dict(k=A + 8), dict(v=A + 4), dict(e=A + 2), dict(out=A + 4), dict(ws=A + 8),
-                                dict(bo=A + 4, bl=A)])
+                                dict(bo=A + 16, bl=A), dict(out=A + 16)])
 def test_cross_attention_refuses(kw):
     assert _cross(**kw) == INVALID
 
