@@ -13,8 +13,11 @@
 // query row, P as bf16 over its scores in TMEM, O += P V.  The loads and first scores of the next unit
 // run under the last softmax and the epilogue of the present one.
 //   256 rows: two query tiles share the keys and take turns on the tensor pipe.
-//   128 rows: one query tile, scores and values double-buffered, for short runs, where the keys'
-//   and values' way from memory bounds the call.
+//   128 rows, for short runs: one query tile with two score buffers, more of the shared memory for keys and
+//   values, whose way from memory bounds the call.
+// Keys and values go round one ring of 16-KB boxes in the order of their first use: with a key buffer twice and
+// a value buffer once instead, the values came a load's latency late for the first of two query tiles (3,800
+// cycles a key tile).
 // The pieces of an item leave normalised partial results, which cross_merge_kernel joins.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -328,10 +331,9 @@ constexpr uint32_t kCrBox = 64 * kCrTile * 2;  // 64 columns x 128 rows, bf16
 template <int kTiles>
 struct Shape {
     static constexpr int kWarpsSoft = 4 * kTiles;
-    static constexpr int kThreads = 32 * (kWarpsSoft + 4);  // + keys, MMAs, values, units
-    static constexpr int kK = 2, kV = kTiles == 1 ? 2 : 1;  // buffers
-    static constexpr uint32_t kOffK = 3 * kCrBox * kTiles, kOffV = kOffK + 3 * kCrBox * kK;
-    static constexpr uint32_t kOffBar = kOffV + 2 * kCrBox * kV;
+    static constexpr int kThreads = 32 * (kWarpsSoft + 4);  // + loads, MMAs, tails, units
+    static constexpr int kRing = 14 - 3 * kTiles;           // boxes of keys and values
+    static constexpr uint32_t kOffRing = 3 * kCrBox * kTiles, kOffBar = 14 * kCrBox;
     static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
 };
 
@@ -437,45 +439,47 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char *gbase = smem_raw + (base - raw);
     const uint32_t bars = base + S::kOffBar;
-    // barriers: the queries: q_full, q_empty; per key buffer k_full, k_empty; per value buffer v_full,
-    // v_empty, and v_landed for a run's last tile; per score buffer s_full, p_full (one arrival per
-    // softmax warp), pv_done; per query tile o_free; per unit slot u_full, u_empty.  (pv_done per score
-    // buffer: with two of them a tile's scores say nothing about the PV before the last one, and a wait
-    // for the last one's phase would pass while a common barrier is still two phases back.)
-    const uint32_t q_full = bars, q_empty = bars + 8;
-    auto k_full = [&](int b) { return bars + 16u + 8u * b; };
-    auto k_empty = [&](int b) { return bars + 32u + 8u * b; };
-    auto v_full = [&](int b) { return bars + 48u + 8u * b; };
-    auto v_empty = [&](int b) { return bars + 64u + 8u * b; };
-    const uint32_t v_landed = bars + 80;
-    auto s_full = [&](int j) { return bars + 88u + 8u * j; };
-    auto p_full = [&](int j) { return bars + 104u + 8u * j; };
-    auto pv_done = [&](int j) { return bars + 120u + 8u * j; };
-    auto o_free = [&](int x) { return bars + 136u + 8u * x; };
-    auto u_full = [&](int j) { return bars + 152u + 8u * j; };
-    auto u_empty = [&](int j) { return bars + 168u + 8u * j; };
-    CrossPiece *slots = reinterpret_cast<CrossPiece *>(gbase + S::kOffBar + 192);  // two of 48 bytes
-    int *abort_flag = reinterpret_cast<int *>(gbase + S::kOffBar + 288);
-    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(gbase + S::kOffBar + 296);
+    // barriers: the ring's items (keys and values of a tile in turn, eight barriers each): full, empty, and
+    // landed for the values of a run's last tile; per use of a score buffer s_full, p_full (one arrival per
+    // softmax warp) and pv_done; per query tile o_free; per unit slot u_full, u_empty; the queries: q_full,
+    // q_empty.  A score buffer has one set of barriers for two query tiles (0, 1) and another for one query
+    // tile that uses both (2, 3): the second tile's warps take no part in such units, run ahead of them, and
+    // would find a common barrier two phases back.  For the same reason pv_done is one per buffer: where one
+    // query tile uses both, its scores say nothing about the PV before the last one.
+    auto full = [&](int i) { return bars + 8u * (i & 7); };
+    auto empty = [&](int i) { return bars + 64u + 8u * (i & 7); };
+    auto landed = [&](int i) { return bars + 128u + 8u * (i & 3); };
+    auto s_full = [&](int i) { return bars + 160u + 8u * i; };
+    auto p_full = [&](int i) { return bars + 192u + 8u * i; };
+    auto pv_done = [&](int i) { return bars + 224u + 8u * i; };
+    auto o_free = [&](int x) { return bars + 256u + 8u * x; };
+    auto u_full = [&](int j) { return bars + 272u + 8u * j; };
+    auto u_empty = [&](int j) { return bars + 288u + 8u * j; };
+    const uint32_t q_full = bars + 304, q_empty = bars + 312;
+    CrossPiece *slots = reinterpret_cast<CrossPiece *>(gbase + S::kOffBar + 320);  // two of 48 bytes
+    int *abort_flag = reinterpret_cast<int *>(gbase + S::kOffBar + 416);
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(gbase + S::kOffBar + 424);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0) {
         if (lane == 0) {
+            for (int i = 0; i < 8; ++i) {
+                mbar_init(full(i), 1);
+                mbar_init(empty(i), 1);
+            }
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(landed(i), 1);
+                mbar_init(s_full(i), 1);
+                mbar_init(p_full(i), 4);
+                mbar_init(pv_done(i), 1);
+            }
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(o_free(j), 4);
+                mbar_init(u_full(j), 1);
+                mbar_init(u_empty(j), 3 + S::kWarpsSoft);
+            }
             mbar_init(q_full, 1);
             mbar_init(q_empty, 1);
-            mbar_init(v_landed, 1);
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(k_full(b), 1);
-                mbar_init(k_empty(b), 1);
-                mbar_init(v_full(b), 1);
-                mbar_init(v_empty(b), 1);
-                mbar_init(s_full(b), 1);
-                mbar_init(p_full(b), 4);
-                mbar_init(pv_done(b), 1);
-                mbar_init(o_free(b), 4);
-                mbar_init(u_full(b), 1);
-                mbar_init(u_empty(b), 3 + S::kWarpsSoft);
-            }
             *abort_flag = 0;
             fence_mbar_init();
         }
@@ -520,6 +524,24 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     };
     // (of two query tiles the second sees as many keys as the first, or more, where it has rows)
     auto tiles_loaded = [&]() -> int { return kTiles == 2 ? max(tiles_of(0), tiles_of(1)) : tiles_of(0); };
+    // One query tile takes both score buffers in turn, so that the next scores are computed under its
+    // softmax; two have one each.  use0 .. use3: how often each set of barriers has been used before the unit,
+    // which says which phase is next, in every role that takes part.
+    auto single = [&]() { return kTiles == 1 || p.nrows <= kCrTile; };
+    int use0 = 0, use1 = 0, use2 = 0, use3 = 0;
+    auto used = [&](int n0, int n1) {
+        if (single()) {
+            use2 += (n0 + 1) / 2;
+            use3 += n0 / 2;
+        } else {
+            use0 += n0;
+            use1 += n1;
+        }
+    };
+    // The ring: key tile t (counted over the units) has `kw` boxes of 128 keys x 64 columns, and its values,
+    // behind them, two of 64 keys x 128 columns (two column halves of 8 KB).
+    const int kw = a.positions ? 3 : 2;
+    auto box = [&](int t, int i) { return base + S::kOffRing + (uint32_t)((t * (kw + 2) + i) % S::kRing) * kCrBox; };
     const int w = warp - S::kWarpsSoft;
 
     if (!match) {
@@ -551,17 +573,27 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
         }
     } else if (w == 0) {
-        // ---------------------------------------------------------------- queries and keys
-        const uint32_t boxes = a.positions ? 3 : 2;
-        int units = 0, t = 0;
+        // ---------------------------------------------------------------- loads
+        // Keys and values go round the ring in the order of their first use; an item's boxes are free again
+        // once the MMAs that read it have finished.
+        int units = 0, t = 0, tails = 0;
+        int freed = 0, freed_boxes = 0;  // items, and boxes up to them, that have been waited for
+        auto room = [&](int boxes) -> bool {  // for the boxes up to this number
+            while (ok && boxes - freed_boxes > S::kRing) {
+                ok = wait_bounded(empty(freed), (freed >> 3) & 1, abort_flag);
+                freed_boxes += freed & 1 ? 2 : kw;
+                ++freed;
+            }
+            return ok;
+        };
         while (next_unit()) {
             const int ntot = tiles_loaded();
             if (ntot == 0) continue;
             if (lane == 0) {
-                const int nx = kTiles == 2 && p.nrows > kCrTile ? 2 : 1;
+                const int nx = single() ? 1 : 2;
                 if (units > 0) ok = wait_bounded(q_empty, (units - 1) & 1, abort_flag);
                 if (ok) {
-                    mbar_arrive_expect_tx(q_full, nx * boxes * kCrBox);
+                    mbar_arrive_expect_tx(q_full, nx * kw * kCrBox);
                     for (int x = 0; x < nx; ++x) {
                         const uint32_t qd = base + 3 * kCrBox * x;
                         const int q0 = p.q0 + x * kCrTile;
@@ -570,56 +602,49 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         if (a.positions) tma_load_3d(qd + 2 * kCrBox, &tm_qr, 0, p.head, q0, q_full);
                     }
                 }
-                for (int g = 0; g < ntot && ok; ++g) {
-                    const int b = (t + g) % S::kK, use = (t + g) / S::kK;
-                    if (use > 0) ok = wait_bounded(k_empty(b), (use - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    const uint32_t kd = base + S::kOffK + b * 3 * kCrBox;
-                    const int k0 = p.k0 + (p.g0 + g) * kCrTile;
-                    mbar_arrive_expect_tx(k_full(b), boxes * kCrBox);
-                    tma_load_3d(kd, &tm_k, 0, k0, p.head, k_full(b));
-                    tma_load_3d(kd + kCrBox, &tm_k, 64, k0, p.head, k_full(b));
-                    if (a.positions) tma_load_2d(kd + 2 * kCrBox, &tm_kr, kDLatent, k0, k_full(b));
+                for (int g = 0; g < ntot && ok; ++g, ++t) {
+                    const int t0 = (p.g0 + g) * kCrTile, k0 = p.k0 + t0;
+                    if (!room(t * (kw + 2) + kw)) break;
+                    mbar_arrive_expect_tx(full(2 * t), kw * kCrBox);
+                    tma_load_3d(box(t, 0), &tm_k, 0, k0, p.head, full(2 * t));
+                    tma_load_3d(box(t, 1), &tm_k, 64, k0, p.head, full(2 * t));
+                    if (a.positions) tma_load_2d(box(t, 2), &tm_kr, kDLatent, k0, full(2 * t));
+                    if (!room((t + 1) * (kw + 2))) break;
+                    const uint32_t bar = p.nk - t0 < kCrTile ? landed(tails++) : full(2 * t + 1);
+                    mbar_arrive_expect_tx(bar, 2 * kCrBox);
+                    for (int i = 0; i < 2; ++i) {
+                        tma_load_3d(box(t, kw + i), &tm_v, 0, k0 + 64 * i, p.head, bar);
+                        tma_load_3d(box(t, kw + i) + kCrBox / 2, &tm_v, 64, k0 + 64 * i, p.head, bar);
+                    }
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
             ++units;
-            t += ntot;
         }
     } else if (w == 2) {
-        // ---------------------------------------------------------------- values
-        int t = 0, landed = 0;
+        // ---------------------------------------------------------------- tails
+        // What lies behind a run's last key is another run's, or anything: its weights are 0, but 0 x NaN is
+        // not, so those values are zeroed before PV reads them.
+        int t = 0, tails = 0;
         while (next_unit()) {
             const int ntot = tiles_loaded();
-            for (int g = 0; g < ntot && ok; ++g, ++t) {
-                const int b = t % S::kV, use = t / S::kV;
-                if (use > 0) ok = __all_sync(0xffffffffu, wait_bounded(v_empty(b), (use - 1) & 1, abort_flag));
-                if (!ok) break;
-                const uint32_t vd = base + S::kOffV + b * 2 * kCrBox;
-                const int t0 = (p.g0 + g) * kCrTile, valid = p.nk - t0;
-                // What lies behind the run's last key is another run's, or anything: its weights are 0, but
-                // 0 x NaN is not, so those rows are zeroed before PV reads them.
-                const uint32_t bar = valid < kCrTile ? v_landed : v_full(b);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, 2 * kCrBox);
-                    tma_load_3d(vd, &tm_v, 0, p.k0 + t0, p.head, bar);
-                    tma_load_3d(vd + kCrBox, &tm_v, 64, p.k0 + t0, p.head, bar);
-                }
-                if (valid < kCrTile) {
-                    ok = __all_sync(0xffffffffu, wait_bounded(v_landed, landed & 1, abort_flag));
-                    ++landed;
-                    if (!ok) break;
-                    const int chunks = (kCrTile - valid) * 8;  // 16 bytes each, of either box
-                    uint4 *rows = reinterpret_cast<uint4 *>(gbase + S::kOffV + b * 2 * kCrBox + valid * 128);
-                    for (int i = lane; i < chunks; i += 32) {
-                        rows[i] = make_uint4(0u, 0u, 0u, 0u);
-                        rows[kCrBox / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(v_full(b));
+            t += ntot;
+            const int valid = p.nk - (p.g0 + ntot - 1) * kCrTile;  // keys of the last tile
+            if (ntot == 0 || valid >= kCrTile) continue;
+            ok = __all_sync(0xffffffffu, wait_bounded(landed(tails), (tails >> 2) & 1, abort_flag));
+            if (!ok) break;
+            ++tails;
+            for (int i = 0; i < 2; ++i) {
+                const int from = min(max(valid - 64 * i, 0), 64), chunks = (64 - from) * 8;  // of 16 bytes
+                uint4 *rows = reinterpret_cast<uint4 *>(gbase + (box(t - 1, kw + i) - base) + from * 128);
+                for (int c = lane; c < chunks; c += 32) {
+                    rows[c] = make_uint4(0u, 0u, 0u, 0u);
+                    rows[kCrBox / 32 + c] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full(2 * t - 1));
         }
     } else if (w == 1) {
         // ---------------------------------------------------------------- MMAs
@@ -629,60 +654,66 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         };
         constexpr uint32_t idesc_s = idesc_bf16_major(128, kCrTile, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_major(128, kCrDh, false, true);
-        const int steps = a.positions ? 12 : 8;
-        int units = 0, t = 0;              // units with keys, and their key tiles, so far
-        int su[2] = {0, 0}, ou[2] = {0, 0};  // uses of each score buffer, units of each query tile, so far
+        int units = 0, t = 0, ou[2] = {0, 0};  // units with keys, their key tiles, units of each query tile
         while (next_unit()) {
             const int n0 = tiles_of(0), n1 = kTiles == 2 ? tiles_of(1) : 0, ntot = max(n0, n1);
             if (ntot == 0) continue;
-            // Scores of query tile x with key tile g; the key buffer goes back after the last query tile
-            // that reads it, the queries after the unit's last scores.
-            auto qk = [&](int x, int g) -> bool {
-                const int b = (t + g) % S::kK, j = kTiles == 2 ? x : (t + g) & 1;
-                if (!wait_w(k_full(b), ((t + g) / S::kK) & 1)) return false;
+            // Scores of query tile x with key tile g into buffer j (barriers i); the keys' boxes go back after the last
+            // query tile that reads them, the queries after the unit's last scores.
+            auto qk = [&](int x, int j, int i, int g) -> bool {
+                const int item = 2 * (t + g);
+                if ((x == 0 || g >= n0) && !wait_w(full(item), (item >> 3) & 1)) return false;
                 tc_fence_after();
-                const uint32_t kd = base + S::kOffK + b * 3 * kCrBox, qd = base + 3 * kCrBox * x;
-                const uint32_t cs = tmem + (kTiles == 2 ? 256u * x : 128u * j);
-                for (int k = 0; k < steps; ++k) {
-                    const uint32_t off = (k >> 2) * kCrBox + (k & 3) * 32u;
-                    mma_ss_warp(cs, smem_desc_sw128(qd + off, 16u, 1024u), smem_desc_sw128(kd + off, 16u, 1024u), idesc_s,
-                                k > 0 ? 1u : 0u);
+                for (int c = 0; c < kw; ++c) {
+                    const uint32_t kd = box(t + g, c), qd = base + (3 * x + c) * kCrBox;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss_warp(tmem + 256u * j, smem_desc_sw128(qd + 32u * k, 16u, 1024u),
+                                    smem_desc_sw128(kd + 32u * k, 16u, 1024u), idesc_s, c + k > 0 ? 1u : 0u);
                 }
-                mma_commit_warp(s_full(j));
+                mma_commit_warp(s_full(i));
                 if (x == (g < n1 ? 1 : 0)) {
-                    mma_commit_warp(k_empty(b));
+                    mma_commit_warp(empty(item));
                     if (g == ntot - 1) mma_commit_warp(q_empty);
                 }
                 return true;
             };
-            // O_x += P_x(g) V(g); the value buffer goes back after the last query tile's.
-            auto pv = [&](int x, int g) -> bool {
-                const int j = kTiles == 2 ? x : (t + g) & 1, b = (t + g) % S::kV;
+            // O_x += P(g) V(g), P in buffer j (use u of barriers i); the values' boxes go back after the last
+            // query tile's.
+            auto pv = [&](int x, int j, int i, int u, int g) -> bool {
+                const int item = 2 * (t + g) + 1;
                 if (g == 0 && ou[x] > 0 && !wait_w(o_free(x), (ou[x] - 1) & 1)) return false;
-                if (!wait_w(p_full(j), su[j] & 1) || !wait_w(v_full(b), ((t + g) / S::kV) & 1)) return false;
+                if ((x == 0 || g >= n0) && !wait_w(full(item), (item >> 3) & 1)) return false;
+                if (!wait_w(p_full(i), u & 1)) return false;
                 tc_fence_after();
-                ++su[j];
-                const uint32_t cp = tmem + (kTiles == 2 ? 256u * x : 128u * j);
-                const uint32_t co = tmem + (kTiles == 2 ? 256u * x + 128u : 256u);
-                for (int k = 0; k < kCrTile / 16; ++k) {
-                    const uint64_t bd = smem_desc_sw128(base + S::kOffV + b * 2 * kCrBox + k * 2048u, kCrBox, 1024u);
-                    mma_ts_warp(co, cp + 8u * k, bd, idesc_o, (g > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t vd = box(t + g, kw + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts_warp(tmem + 256u * x + 128u, tmem + 256u * j + 32u * c + 8u * k,
+                                    smem_desc_sw128(vd + 2048u * k, kCrBox / 2, 1024u), idesc_o, g + c + k > 0 ? 1u : 0u);
                 }
-                mma_commit_warp(pv_done(j));
-                if (x == (g < n1 ? 1 : 0)) mma_commit_warp(v_empty(b));
+                mma_commit_warp(pv_done(i));
+                if (x == (g < n1 ? 1 : 0)) mma_commit_warp(empty(item));
                 return true;
             };
             ok = wait_w(q_full, units & 1);
-            if constexpr (kTiles == 2) {
-                ok = ok && (n0 == 0 || qk(0, 0)) && (n1 == 0 || qk(1, 0));
+            if (single()) {
+                ok = ok && qk(0, 0, 2, 0);
                 for (int g = 0; g < ntot && ok; ++g) {
-                    if (g < n0) ok = pv(0, g) && (g + 1 >= n0 || qk(0, g + 1));
-                    if (ok && g < n1) ok = pv(1, g) && (g + 1 >= n1 || qk(1, g + 1));
+                    const int j = g & 1;
+                    ok = (g + 1 >= ntot || qk(0, j ^ 1, 2 + (j ^ 1), g + 1)) &&
+                         pv(0, j, 2 + j, (j ? use3 : use2) + (g >> 1), g);
                 }
             } else {
-                ok = ok && qk(0, 0);
-                for (int g = 0; g < ntot && ok; ++g) ok = (g + 1 >= ntot || qk(0, g + 1)) && pv(0, g);
+                ok = ok && (n0 == 0 || qk(0, 0, 0, 0)) && (n1 == 0 || qk(1, 1, 1, 0));
+                for (int g = 0; g < ntot && ok; ++g) {
+                    if (g < n0) ok = pv(0, 0, 0, use0 + g, g) && (g + 1 >= n0 || qk(0, 0, 0, g + 1));
+                    if (ok && g < n1) ok = pv(1, 1, 1, use1 + g, g) && (g + 1 >= n1 || qk(1, 1, 1, g + 1));
+                }
             }
+            used(n0, n1);
             if (n0 > 0) ++ou[0];
             if (n1 > 0) ++ou[1];
             ++units;
@@ -697,23 +728,23 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         const int x = warp >> 2, quad = warp & 3;
         const int r = x * kCrTile + 32 * quad + lane;  // the item's row
         const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-        const uint32_t cO = tmem + lane_base + (kTiles == 2 ? 256u * x + 128u : 256u);
-        int t = 0;  // key tiles of this query tile so far
-        auto wait_pv = [&](int n) {
-            return wait_bounded(pv_done(kTiles == 2 ? x : n & 1), (kTiles == 2 ? n : n >> 1) & 1, abort_flag);
-        };
+        const uint32_t cO = tmem + lane_base + 256u * x + 128u;
+        // the score buffer of the unit's key tile g, its barriers, and which use of them that is
+        auto buffer = [&](int g) { return single() ? g & 1 : x; };
+        auto barriers = [&](int g) { return single() ? 2 + (g & 1) : x; };
+        auto use_of = [&](int g) { return single() ? (g & 1 ? use3 : use2) + (g >> 1) : (x ? use1 : use0) + g; };
+        auto wait_pv = [&](int g) { return wait_bounded(pv_done(barriers(g)), use_of(g) & 1, abort_flag); };
         while (next_unit()) {
             const int nt = tiles_of(x);
             // (rows past the item's compute something nobody reads)
             const int see = r < p.nrows ? seen(r) : p.nk;
             float m = -INFINITY, l = 0.f;  // reference maximum (log2 units), running sum
             for (int g = 0; g < nt; ++g) {
-                const int n = t + g, j = kTiles == 2 ? x : n & 1;
-                ok = wait_bounded(s_full(j), (kTiles == 2 ? n : n >> 1) & 1, abort_flag);
+                ok = wait_bounded(s_full(barriers(g)), use_of(g) & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t cS = tmem + lane_base + (kTiles == 2 ? 256u * x : 128u * j);
+                const uint32_t cS = tmem + lane_base + 256u * buffer(g);
                 float s[kCrTile];
                 {
                     uint32_t v[4][32];
@@ -761,7 +792,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 m = mref;
                 // O is rescaled (rarely) once the previous PV has finished; the next waits for this P
                 if (g > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    ok = wait_pv(n - 1);
+                    ok = wait_pv(g - 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -778,10 +809,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(j));
+                if (lane == 0) mbar_arrive(p_full(barriers(g)));
             }
             if (!ok) break;
-            t += nt;
             // the row's result, 32 columns at a time, normalised: the whole of it, or a piece's part
             const float lse2 = l == 0.f ? -INFINITY : m + log2f(l), inv = l == 0.f ? 0.f : 1.f / l;
             const bool whole = p.row0 < 0, mine = r < p.nrows;
@@ -790,7 +820,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             Share sh{1.f, 0.f, 0.f};
             if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse, row);
             if (nt > 0) {
-                ok = wait_pv(t - 1);
+                ok = wait_pv(nt - 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -825,6 +855,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             if (mine && whole && a.lse) a.lse[row] = sh.lse;
             if (mine && !whole) part_lse[part_row] = lse2;
+            used(nt, nt);
         }
     }
     grid_dep_launch();
@@ -1016,14 +1047,14 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     const uint64_t dqn[3] = {kCrDh, (uint64_t)H, (uint64_t)total_q}, sqn[2] = {kCrDh * 2, (uint64_t)kCrDh * 2 * H};
     const uint64_t dqr[3] = {kDRope, (uint64_t)H, (uint64_t)total_q}, sqr[2] = {kDRope * 2, (uint64_t)kDRope * 2 * H};
     const uint32_t bq[3] = {64, 1, kCrTile};
-    // k nope, v [H][total_k][128]: (cols, key, h); boxes of 64 columns x 128 keys
+    // k nope, v [H][total_k][128]: (cols, key, h); boxes of 64 columns x 128 keys, or 64 values
     const uint64_t dkv[3] = {kCrDh, nk, total_k > 0 ? (uint64_t)H : 1}, skv[2] = {kCrDh * 2, (uint64_t)kCrDh * 2 * nk};
-    const uint32_t bkv[3] = {64, kCrTile, 1};
+    const uint32_t bk[3] = {64, kCrTile, 1}, bv[3] = {64, kCrTile / 2, 1};
     // RoPE keys: columns 512 .. 575 of the [total_k][576] entries
     const uint64_t de[2] = {kDEntry, nk}, se[1] = {kDEntry * 2};
     const uint32_t be[2] = {64, kCrTile};
-    if (!tmap_bf16(&tqn, q_nope, 3, dqn, sqn, bq) || !tmap_bf16(&tk, k_nope, 3, dkv, skv, bkv) ||
-        !tmap_bf16(&tv, v, 3, dkv, skv, bkv))
+    if (!tmap_bf16(&tqn, q_nope, 3, dqn, sqn, bq) || !tmap_bf16(&tk, k_nope, 3, dkv, skv, bk) ||
+        !tmap_bf16(&tv, v, 3, dkv, skv, bv))
         return MLA_ERR_CUDA;
     tqr = tqn;
     tkr = tk;
