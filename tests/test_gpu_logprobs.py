@@ -123,6 +123,14 @@ def test_the_types_lowest_and_largest_values():
         check(x[:2], tok[:2], 3, 1.0, [t[:2] for t in got])
         assert got[0][2] == 0 and got[1][2] == 0 and got[2][2] == 0
         assert got[3][2].tolist() == [5, 0, 1]
+    for dtype in TYPES.values():
+        # the lowest value and -inf together; values so large that 160 below them is not a value of the type
+        low, inf = torch.finfo(dtype).min, torch.inf
+        x = torch.full((2, 6000), -inf, dtype=dtype, device="cuda")
+        x[0, 1000:1007] = low
+        x[1, 50:53] = 6e4 if dtype == torch.float16 else 1e12
+        tok = torch.tensor([1003, 52], dtype=torch.int32, device="cuda")
+        check(x, tok, 10, 1.0, ops.token_logprobs(x, tok, top=10))
     x = torch.zeros(1, 50000, device="cuda")  # nearly certain: both terms of the entropy are small
     x[0, 33333] = 30.0
     tok = torch.tensor([33333], dtype=torch.int32, device="cuda")
