@@ -47,7 +47,7 @@ constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
 
 struct CrossHeader {
     uint32_t magic;
-    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, split_rows, reserved[5];
+    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, groups, last, reserved[4];
 };
 static_assert(sizeof(CrossHeader) == 64, "plan header is 64 bytes");
 
@@ -60,10 +60,14 @@ struct CrossPiece {
     int32_t reserved[3];
 };
 // An item that is cut: its query rows, its parts' partial rows (part p: row0 + p nrows ..), and how many
-// rows the cut items before it have.
+// groups of kCrGroup rows the cut items before it have.
+constexpr int kCrGroup = 32;
 struct CrossSplit {
     int32_t q0, nrows, row0, parts, before;
 };
+// A part's results of one head, rows row0 .. row0 + nrows of the partials: nrows log-sum-exps (log2 units),
+// and 32 runs of nrows four-column pieces (a warp's 32 rows write and read 512 bytes in a row).
+MLA_HD int64_t part_at(int row0, int nrows, int H, int head) { return (int64_t)row0 * H + (int64_t)head * nrows; }
 
 struct CrossLayout {
     size_t pieces, order, splits, seqs, item_off, part_lse, part_o, total;
@@ -175,6 +179,7 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     __shared__ __align__(16) uint32_t s_key[kCpSort];
     __shared__ int4 s_seq[kCpKeep];
     __shared__ int32_t s_off[kCpKeep];
+    __shared__ int s_last;
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     const int64_t shares = (int64_t)kCrShare * a.sms;
     const int64_t share = (cost * a.H + shares - 1) / shares;
     const int target = (int)(share > kCrMinPiece ? share : kCrMinPiece);
-    Four done{};  // pieces, cut items, their partial rows, their rows
+    Four done{};  // pieces, cut items, their partial rows, their groups of rows
     for (int i0 = 0; i0 < items; i0 += kCpThreads) {
         const int i = i0 + tid;
         int n = 0, tiles = 0;
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         int64_t row0 = -1;
         if (__syncthreads_or(n > 1) || done.v[1] > 0) {
             const int cut = n > 1;
-            const Four mine{{n, cut, cut ? (int64_t)n * p.nrows : 0, cut ? p.nrows : 0}};
+            const Four mine{{n, cut, cut ? (int64_t)n * p.nrows : 0, cut ? (p.nrows + kCrGroup - 1) / kCrGroup : 0}};
             const Four x = block_scan<false, 4>(mine, &all, s_scan);
             at = (int)(done.v[0] + x.v[0] - n);
             if (cut) {
@@ -283,13 +288,18 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
             p.g1 = (int)((int64_t)tiles * (k + 1) / n);
             p.row0 = n > 1 ? (int)(row0 + (int64_t)k * p.nrows) : -1;
             pieces[at + k] = p;
-            if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(p.g1 - p.g0, 0xFFFF)) << 16 | (uint32_t)(at + k);
+            // (one query tile takes about two thirds of two)
+            const int length = (p.g1 - p.g0) * (p.nrows > kCrTile ? 3 : 2);
+            if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(length, 0xFFFF)) << 16 | (uint32_t)(at + k);
         }
     }
     __syncthreads();
 
-    // longest first: a piece's place is the number of smaller keys (all different)
+    // Longest first: a piece's place is the number of smaller keys (all different).  Short ones (of half the
+    // longest at most), as many as the longest unit takes on every SM, come last, for all heads: they fill what the
+    // others leave.
     const int np = (int)done.v[0];
+    if (tid == 0) s_last = 0;
     if (np <= kCpSort) {
         const int whole = (np + 3) & ~3;
         if (tid < whole - np) s_key[np + tid] = 0xFFFFFFFFu;
@@ -297,15 +307,26 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         for (int i = tid; i < np; i += kCpThreads) {
             const uint32_t key = s_key[i];
             int place = 0;
+            uint32_t least = key;
+            int64_t behind = 0;  // the lengths of this piece and of those behind it
             for (int j = 0; j < whole; j += 4) {
-                const uint4 k4 = *reinterpret_cast<const uint4 *>(s_key + j);
-                place += (k4.x < key) + (k4.y < key) + (k4.z < key) + (k4.w < key);
+                const uint4 q = *reinterpret_cast<const uint4 *>(s_key + j);
+                const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    place += k4[k] < key;
+                    least = min(least, k4[k]);
+                    behind += k4[k] >= key ? 0xFFFF - (int)(k4[k] >> 16) : 0;
+                }
             }
             order[place] = i;
+            const int longest = 0xFFFF - (int)(least >> 16);
+            if (behind * a.H <= (int64_t)longest * a.sms && 2 * (0xFFFF - (int)(key >> 16)) <= longest) atomicAdd(&s_last, 1);
         }
     } else {
         for (int i = tid; i < np; i += kCpThreads) order[i] = i;
     }
+    __syncthreads();
     if (tid == 0) {
         int *counters = reinterpret_cast<int *>(a.ws + kCrCounters);
         counters[0] = counters[1] = 0;
@@ -320,7 +341,8 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         h.sms = a.sms;
         h.pieces = np;
         h.splits = (int32_t)done.v[1];
-        h.split_rows = (int32_t)done.v[3];
+        h.groups = (int32_t)done.v[3];
+        h.last = s_last;
         *reinterpret_cast<CrossHeader *>(a.ws) = h;
     }
 }
@@ -552,7 +574,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const CrossLayout L = cross_layout(a.B, a.H, a.total_q, hd->sms);
             const CrossPiece *pieces = reinterpret_cast<const CrossPiece *>(a.ws + L.pieces);
             const int32_t *order = reinterpret_cast<const int32_t *>(a.ws + L.order);
-            const int n = hd->pieces;
+            const int total = hd->pieces * a.H, n = hd->pieces - hd->last;  // (the last ones: see the plan)
             for (int i = 0; ok; ++i) {
                 const int j = i & 1;
                 if (i >= 2) ok = wait_bounded(u_empty(j), ((i >> 1) - 1) & 1, abort_flag);
@@ -566,6 +588,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     const int r = u - h0 * n;
                     d = pieces[order[r / hg]];
                     d.head = h0 + r % hg;
+                } else if (u < total) {
+                    const int r = u - n * a.H;
+                    d = pieces[order[n + r / a.H]];
+                    d.head = r % a.H;
                 }
                 slots[j] = d;
                 mbar_arrive(u_full(j));
@@ -816,7 +842,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const float lse2 = l == 0.f ? -INFINITY : m + log2f(l), inv = l == 0.f ? 0.f : 1.f / l;
             const bool whole = p.row0 < 0, mine = r < p.nrows;
             const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
-            const int64_t part_row = (int64_t)(p.row0 + r) * a.H + p.head;
+            const int64_t part = whole ? 0 : part_at(p.row0, p.nrows, a.H, p.head);
             Share sh{1.f, 0.f, 0.f};
             if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse, row);
             if (nt > 0) {
@@ -839,13 +865,12 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 if (whole) {
                     store32(a, row * kCrDh + c, o, inv * sh.mine, sh);
                 } else {
+                    float4 *dst = reinterpret_cast<float4 *>(part_o + part * kCrDh) + r;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(o[k + i]) * inv);
-                        st_global8(part_o + part_row * kCrDh + c + k, v);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        dst[(c / 4 + k) * p.nrows] =
+                            make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                                        __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
                 }
             }
             if (nt > 0) {
@@ -854,7 +879,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 if (lane == 0) mbar_arrive(o_free(x));
             }
             if (mine && whole && a.lse) a.lse[row] = sh.lse;
-            if (mine && !whole) part_lse[part_row] = lse2;
+            if (mine && !whole) part_lse[part + r] = lse2;
             used(nt, nt);
         }
     }
@@ -879,12 +904,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     }
 }
 
-// The items that were cut: a warp joins the parts of a row of one head (lane i: columns 4 i .. 4 i + 3),
-// all of them in the parts' order.
+// The items that were cut: a CTA joins the parts of up to 32 rows of one head, in the parts' order.  Lane i
+// of warp w has row i and columns 4 w .. 4 w + 3, 32 + 4 w .. and so on; the rows are then written a warp each.
 constexpr int kCmThreads = 256;
-constexpr int kCmCtasPerSm = 4;
-constexpr int kCmParts = 8;  // in flight together
-__global__ void __launch_bounds__(kCmThreads) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
+constexpr int kCmCtasPerSm = 2;
+constexpr int kCmParts = 4;  // in flight together
+__global__ void __launch_bounds__(kCmThreads, 2) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
+    __shared__ __align__(16) float s_o[kCrGroup][kCrDh + 4];
+    __shared__ float s_before[kCrGroup];
     grid_dep_wait();
     grid_dep_launch();
     const CrossHeader *hd = reinterpret_cast<const CrossHeader *>(a.ws);
@@ -893,9 +920,9 @@ __global__ void __launch_bounds__(kCmThreads) cross_merge_kernel(const __grid_co
     const CrossSplit *splits = reinterpret_cast<const CrossSplit *>(a.ws + L.splits);
     const float *part_lse = reinterpret_cast<const float *>(a.ws + L.part_lse);
     const float *part_o = reinterpret_cast<const float *>(a.ws + L.part_o);
-    const int lane = threadIdx.x & 31, n_splits = hd->splits;
-    const int64_t tasks = (int64_t)hd->split_rows * a.H, warps = (int64_t)gridDim.x * (kCmThreads / 32);
-    for (int64_t t = (int64_t)blockIdx.x * (kCmThreads / 32) + (threadIdx.x >> 5); t < tasks; t += warps) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_splits = hd->splits;
+    const int64_t tasks = (int64_t)hd->groups * a.H;
+    for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
         const int at = (int)(t / a.H), h = (int)(t - (int64_t)at * a.H);
         int lo = 0, hi = n_splits - 1;
         while (lo < hi) {
@@ -906,19 +933,26 @@ __global__ void __launch_bounds__(kCmThreads) cross_merge_kernel(const __grid_co
                 hi = mid - 1;
         }
         const CrossSplit s = splits[lo];
-        const int64_t first = (int64_t)(s.row0 + at - s.before) * a.H + h, pitch = (int64_t)s.nrows * a.H;
-        const int64_t row = (int64_t)(s.q0 + at - s.before) * a.H + h;
+        const int r0 = (at - s.before) * kCrGroup, rows = min(kCrGroup, s.nrows - r0);
+        const int64_t first = part_at(s.row0, s.nrows, a.H, h) + r0 + lane, pitch = (int64_t)s.nrows * a.H;
+        const int64_t row = (int64_t)(s.q0 + r0 + lane) * a.H + h;
+        const bool mine = lane < rows;
         float top = -INFINITY, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 < s.parts; k0 += kCmParts) {
             float l[kCmParts];
-            float4 v[kCmParts];
+            float4 v[kCmParts][4];
 #pragma unroll
             for (int k = 0; k < kCmParts; ++k) {
-                const bool is = k0 + k < s.parts;
-                l[k] = is ? part_lse[first + (k0 + k) * pitch] : -INFINITY;
-                v[k] = is ? reinterpret_cast<const float4 *>(part_o + (first + (k0 + k) * pitch) * kCrDh)[lane]
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                const bool is = mine && k0 + k < s.parts;
+                const int64_t from = first + (k0 + k) * pitch;  // (of the log-sum-exps)
+                l[k] = is ? part_lse[from] : -INFINITY;
+                const float4 *o = reinterpret_cast<const float4 *>(part_o + (from - r0 - lane) * kCrDh) + r0 + lane;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[k][c] = is ? o[(8 * c + warp) * s.nrows] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float m = top;
 #pragma unroll
@@ -926,21 +960,33 @@ __global__ void __launch_bounds__(kCmThreads) cross_merge_kernel(const __grid_co
             if (m == -INFINITY) continue;  // no key seen so far
             const float f = ex2_approx(top - m);
             sum *= f;
-            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] = make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
 #pragma unroll
             for (int k = 0; k < kCmParts; ++k) {
                 const float w = ex2_approx(l[k] - m);
                 sum += w;
-                acc = make_float4(fmaf(w, v[k].x, acc.x), fmaf(w, v[k].y, acc.y), fmaf(w, v[k].z, acc.z),
-                                  fmaf(w, v[k].w, acc.w));
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[c] = make_float4(fmaf(w, v[k][c].x, acc[c].x), fmaf(w, v[k][c].y, acc[c].y),
+                                         fmaf(w, v[k][c].z, acc[c].z), fmaf(w, v[k][c].w, acc[c].w));
             }
             top = m;
         }
-        const Share sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse, row);
+        Share sh{0.f, 0.f, 0.f};
+        if (mine) sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse, row);
         const float f = sum == 0.f ? 0.f : sh.mine / sum;
-        store4(a, row * kCrDh + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), sh.before);
-        __syncwarp();  // (lse may be before_lse itself)
-        if (a.lse && lane == 0) a.lse[row] = sh.lse;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float4 *>(&s_o[lane][4 * (8 * c + warp)]) =
+                make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
+        if (warp == 0) s_before[lane] = sh.before;
+        __syncthreads();  // (and every warp has read before_lse, which may be lse itself)
+        if (warp == 0 && mine && a.lse) a.lse[row] = sh.lse;
+        for (int i = warp; i < rows; i += kCmThreads / 32)
+            store4(a, (row + (int64_t)(i - lane) * a.H) * kCrDh + 4 * lane,
+                   *reinterpret_cast<const float4 *>(&s_o[i][4 * lane]), s_before[i]);
+        __syncthreads();
     }
 }
 
@@ -1079,6 +1125,8 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
         a.rows == kCrTile
             ? launch_pdl(cross_kernel<1>, sms, Shape<1>::kThreads, Shape<1>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a)
             : launch_pdl(cross_kernel<2>, sms, Shape<2>::kThreads, Shape<2>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a);
-    if (e == cudaSuccess) e = launch_pdl(cross_merge_kernel, kCmCtasPerSm * sms, kCmThreads, 0, (cudaStream_t)stream, a);
+    // (no item has more key tiles than all keys together: short ones are never cut)
+    if (e == cudaSuccess && total_k > kCrMinPiece * kCrTile)
+        e = launch_pdl(cross_merge_kernel, kCmCtasPerSm * sms, kCmThreads, 0, (cudaStream_t)stream, a);
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
