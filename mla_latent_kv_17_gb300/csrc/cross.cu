@@ -41,6 +41,7 @@ constexpr int kCrTile = 128;            // query rows of a tile (TMEM lanes), ke
 constexpr int kCrHeadGroup = 8;
 constexpr int kCrMinPiece = 4;          // key tiles
 constexpr int kCrShare = 3;             // pieces an SM's share is made of, at least, before items stay whole
+constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
 constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
 constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
@@ -630,6 +631,16 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
                 for (int g = 0; g < ntot && ok; ++g, ++t) {
                     const int t0 = (p.g0 + g) * kCrTile, k0 = p.k0 + t0;
+                    if (kTiles == 2 && g + kCrAhead < ntot) {  // on its way into L2
+                        const int ka = k0 + kCrAhead * kCrTile;
+                        tma_prefetch_3d(&tm_k, 0, ka, p.head);
+                        tma_prefetch_3d(&tm_k, 64, ka, p.head);
+                        if (a.positions) tma_prefetch_2d(&tm_kr, kDLatent, ka);
+                        for (int i = 0; i < 2; ++i) {
+                            tma_prefetch_3d(&tm_v, 0, ka + 64 * i, p.head);
+                            tma_prefetch_3d(&tm_v, 64, ka + 64 * i, p.head);
+                        }
+                    }
                     if (!room(t * (kw + 2) + kw)) break;
                     mbar_arrive_expect_tx(full(2 * t), kw * kCrBox);
                     tma_load_3d(box(t, 0), &tm_k, 0, k0, p.head, full(2 * t));
@@ -680,48 +691,53 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         };
         constexpr uint32_t idesc_s = idesc_bf16_major(128, kCrTile, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_major(128, kCrDh, false, true);
+        // descriptors but for their addresses: keys and queries (K-major), values (MN-major)
+        const uint64_t desc_k = smem_desc_sw128(0, 16u, 1024u), desc_v = smem_desc_sw128(0, kCrBox / 2, 1024u);
         int units = 0, t = 0, ou[2] = {0, 0};  // units with keys, their key tiles, units of each query tile
         while (next_unit()) {
             const int n0 = tiles_of(0), n1 = kTiles == 2 ? tiles_of(1) : 0, ntot = max(n0, n1);
             if (ntot == 0) continue;
-            // Scores of query tile x with key tile g into buffer j (barriers i); the keys' boxes go back after the last
-            // query tile that reads them, the queries after the unit's last scores.
+            // Waits for the keys, or the values, of key tile g (once: for the first query tile that reads them).
+            auto landed_k = [&](int x, int g) {
+                return (x == 1 && g < n0) || wait_w(full(2 * (t + g)), (2 * (t + g) >> 3) & 1);
+            };
+            auto landed_v = [&](int x, int g) {
+                return (x == 1 && g < n0) || wait_w(full(2 * (t + g) + 1), (2 * (t + g) >> 3) & 1);
+            };
+            // Scores of query tile x with key tile g into buffer j (barriers i); the keys' boxes go back after the
+            // last query tile that reads them, the queries after the unit's last scores.
             auto qk = [&](int x, int j, int i, int g) -> bool {
-                const int item = 2 * (t + g);
-                if ((x == 0 || g >= n0) && !wait_w(full(item), (item >> 3) & 1)) return false;
+                if (!landed_k(x, g)) return false;
                 tc_fence_after();
                 for (int c = 0; c < kw; ++c) {
-                    const uint32_t kd = box(t + g, c), qd = base + (3 * x + c) * kCrBox;
+                    const uint64_t kd = desc_k + (box(t + g, c) >> 4), qd = desc_k + ((base + (3 * x + c) * kCrBox) >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss_warp(tmem + 256u * j, smem_desc_sw128(qd + 32u * k, 16u, 1024u),
-                                    smem_desc_sw128(kd + 32u * k, 16u, 1024u), idesc_s, c + k > 0 ? 1u : 0u);
+                        mma_ss_warp(tmem + 256u * j, qd + 2u * k, kd + 2u * k, idesc_s, c + k > 0 ? 1u : 0u);
                 }
                 mma_commit_warp(s_full(i));
                 if (x == (g < n1 ? 1 : 0)) {
-                    mma_commit_warp(empty(item));
+                    mma_commit_warp(empty(2 * (t + g)));
                     if (g == ntot - 1) mma_commit_warp(q_empty);
                 }
                 return true;
             };
-            // O_x += P(g) V(g), P in buffer j (use u of barriers i); the values' boxes go back after the last
-            // query tile's.
+            // O_x += P(g) V(g), P in buffer j (use u of barriers i); the values' boxes go back after the last query
+            // tile's.
             auto pv = [&](int x, int j, int i, int u, int g) -> bool {
-                const int item = 2 * (t + g) + 1;
                 if (g == 0 && ou[x] > 0 && !wait_w(o_free(x), (ou[x] - 1) & 1)) return false;
-                if ((x == 0 || g >= n0) && !wait_w(full(item), (item >> 3) & 1)) return false;
-                if (!wait_w(p_full(i), u & 1)) return false;
+                if (!landed_v(x, g) || !wait_w(p_full(i), u & 1)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint32_t vd = box(t + g, kw + c);
+                    const uint64_t vd = desc_v + (box(t + g, kw + c) >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts_warp(tmem + 256u * x + 128u, tmem + 256u * j + 32u * c + 8u * k,
-                                    smem_desc_sw128(vd + 2048u * k, kCrBox / 2, 1024u), idesc_o, g + c + k > 0 ? 1u : 0u);
+                        mma_ts_warp(tmem + 256u * x + 128u, tmem + 256u * j + 32u * c + 8u * k, vd + 128u * k, idesc_o,
+                                    g + c + k > 0 ? 1u : 0u);
                 }
                 mma_commit_warp(pv_done(i));
-                if (x == (g < n1 ? 1 : 0)) mma_commit_warp(empty(item));
+                if (x == (g < n1 ? 1 : 0)) mma_commit_warp(empty(2 * (t + g) + 1));
                 return true;
             };
             ok = wait_w(q_full, units & 1);
@@ -735,10 +751,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             } else {
                 ok = ok && (n0 == 0 || qk(0, 0, 0, 0)) && (n1 == 0 || qk(1, 1, 1, 0));
                 for (int g = 0; g < ntot && ok; ++g) {
-                    if (g < n0) ok = pv(0, 0, 0, use0 + g, g) && (g + 1 >= n0 || qk(0, 0, 0, g + 1));
-                    if (ok && g < n1) ok = pv(1, 1, 1, use1 + g, g) && (g + 1 >= n1 || qk(1, 1, 1, g + 1));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int n = x ? n1 : n0;
+                        if (ok && g < n) ok = pv(x, x, x, (x ? use1 : use0) + g, g) && (g + 1 >= n || qk(x, x, x, g + 1));
+                    }
                 }
             }
+            if (!ok) break;
             used(n0, n1);
             if (n0 > 0) ++ou[0];
             if (n1 > 0) ++ou[1];
