@@ -284,14 +284,29 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         } else {
             done.v[0] += min((int64_t)kCpThreads, items - i0);
         }
-        for (int k = 0; k < n; ++k) {
-            p.g0 = (int)((int64_t)tiles * k / n);
-            p.g1 = (int)((int64_t)tiles * (k + 1) / n);
-            p.row0 = n > 1 ? (int)(row0 + (int64_t)k * p.nrows) : -1;
-            pieces[at + k] = p;
+        auto emit = [&](CrossPiece q, int at, int64_t row0, int tiles, int k, int n) {
+            q.g0 = (int)((int64_t)tiles * k / n);
+            q.g1 = (int)((int64_t)tiles * (k + 1) / n);
+            q.row0 = n > 1 ? (int)(row0 + (int64_t)k * q.nrows) : -1;
+            pieces[at + k] = q;
             // (one query tile takes about two thirds of two)
-            const int length = (p.g1 - p.g0) * (p.nrows > kCrTile ? 3 : 2);
+            const int length = (q.g1 - q.g0) * (q.nrows > kCrTile ? 3 : 2);
             if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(length, 0xFFFF)) << 16 | (uint32_t)(at + k);
+        };
+        if (n == 1) emit(p, at, row0, tiles, 0, 1);
+        // an item's pieces by its whole warp
+        for (unsigned cut = __ballot_sync(0xffffffffu, n > 1); cut; cut &= cut - 1) {
+            const int from = __ffs(cut) - 1;
+            auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, from); };
+            CrossPiece q = {};
+            q.q0 = of(p.q0);
+            q.nrows = of(p.nrows);
+            q.k0 = of(p.k0);
+            q.nk = of(p.nk);
+            q.see0 = of(p.see0);
+            const int qn = of(n), qat = of(at), qtiles = of(tiles);
+            const int64_t qrow0 = of((int)row0);
+            for (int k = tid & 31; k < qn; k += 32) emit(q, qat, qrow0, qtiles, k, qn);
         }
     }
     __syncthreads();
