@@ -115,6 +115,7 @@ constexpr int kCpThreads = 512;
 constexpr int kCpWarps = kCpThreads / 32;
 constexpr int kCpSort = 2048;  // pieces that are put in order (more of them even out by themselves)
 constexpr int kCpKeep = 1024;  // runs whose starts stay in shared memory
+constexpr int kCpFew = 8;      // pieces of an item that one thread writes
 
 // Four values a thread, scanned together: sums, or maxima.
 struct Four {
@@ -293,9 +294,10 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
             const int length = (q.g1 - q.g0) * (q.nrows > kCrTile ? 3 : 2);
             if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(length, 0xFFFF)) << 16 | (uint32_t)(at + k);
         };
-        if (n == 1) emit(p, at, row0, tiles, 0, 1);
-        // an item's pieces by its whole warp
-        for (unsigned cut = __ballot_sync(0xffffffffu, n > 1); cut; cut &= cut - 1) {
+        if (n <= kCpFew)
+            for (int k = 0; k < n; ++k) emit(p, at, row0, tiles, k, n);
+        // many pieces of an item by its whole warp
+        for (unsigned cut = __ballot_sync(0xffffffffu, n > kCpFew); cut; cut &= cut - 1) {
             const int from = __ffs(cut) - 1;
             auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, from); };
             CrossPiece q = {};
@@ -942,7 +944,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 // The items that were cut: a CTA joins the parts of up to 32 rows of one head, in the parts' order.  Lane i
 // of warp w has row i and columns 4 w .. 4 w + 3, 32 + 4 w .. and so on; the rows are then written a warp each.
 constexpr int kCmThreads = 256;
-constexpr int kCmCtasPerSm = 2;
+constexpr int kCmCtasPerSm = 6;  // (two at once; the rest even out what the rows differ by)
 constexpr int kCmParts = 4;  // in flight together
 __global__ void __launch_bounds__(kCmThreads, 2) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
     __shared__ __align__(16) float s_o[kCrGroup][kCrDh + 4];
