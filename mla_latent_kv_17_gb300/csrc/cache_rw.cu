@@ -139,7 +139,8 @@ __device__ __forceinline__ uint4 rotate_key(uint4 key, const uint64_t *turns, co
     return pack8(k);
 }
 
-// Positions of a key's pairs: one for all of them (RwArgs), or one per axis and an axis for each pair.
+// Positions of a key's pairs: one for all of them (RwArgs), or one per axis and an axis for each pair (65,536 tokens
+// with norm into records: 28 us with three axes, 25 with one; four positions to choose from per token).
 struct OnePosition {
     static constexpr bool kAxes = false;
 };

@@ -5,20 +5,26 @@
 // cross_plan_kernel: one CTA cuts the batch into items - a tile of 128 or 256 query rows of a run
 // with the key tiles (of 128) it sees - and items whose keys would keep one SM much longer than
 // the others' share into pieces, and orders the pieces by falling length.  The list is the same for
-// every head.
+// every head.  3 us (5.5 where keys are cut).
 //
 // cross_kernel: a persistent CTA per SM takes units (a piece and a head) from a counter, longest
 // pieces first, groups of eight heads in turn so that the keys and values in use stay in L2.  Per
 // unit, as in the causal prefill: S = Q K^T on tcgen05 into TMEM, online softmax with one thread per
 // query row, P as bf16 over its scores in TMEM, O += P V.  The loads and first scores of the next unit
 // run under the last softmax and the epilogue of the present one.
-//   256 rows: two query tiles share the keys and take turns on the tensor pipe.
+//   256 rows: two query tiles share the keys and take turns on the tensor pipe.  1,001 queries over 9,193 keys,
+//   causal, 128 heads: 527 us, 0.72 of the measured bf16 rate.  A key tile takes 3,650 cycles where its MMAs take
+//   2,560: the warp that issues them is the narrowest place (about 60 cycles an operation, 450 for waits and
+//   commits), then shared memory (8 KB of operands in the 64 cycles of a score operation).
 //   128 rows, for short runs: one query tile with two score buffers, more of the shared memory for keys and
-//   values, whose way from memory bounds the call.
+//   values, whose way from memory bounds the call: 64 single tokens over 256 - 2,048 keys, 16 heads: 101 us, 0.88
+//   of the copy rate.
 // Keys and values go round one ring of 16-KB boxes in the order of their first use: with a key buffer twice and
 // a value buffer once instead, the values came a load's latency late for the first of two query tiles (3,800
-// cycles a key tile).
-// The pieces of an item leave normalised partial results, which cross_merge_kernel joins.
+// cycles a key tile).  Two tiles ahead of their load they are brought into L2 where two query tiles share them
+// (545 -> 531 us; where memory bounds the call it costs 3 %).
+// The pieces of an item leave normalised partial results, which cross_merge_kernel joins (19 us for 28 parts of
+// 256 rows x 16 heads, as long as its 60 MB take at half the copy rate).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +46,9 @@ constexpr int kCrDh = 128;
 constexpr int kCrTile = 128;            // query rows of a tile (TMEM lanes), keys of a tile
 constexpr int kCrHeadGroup = 8;
 constexpr int kCrMinPiece = 4;          // key tiles
-constexpr int kCrShare = 3;             // pieces an SM's share is made of, at least, before items stay whole
+// An item longer than a third of an SM's share of the work is cut.  (4 x 256 - 512 queries over 1,024 - 8,192 keys x
+// 16 heads with 2, 3, 4, 6, 8 instead of 3: 129, 112, 129, 140, 146 us: parts cost a start, an end and their joining.)
+constexpr int kCrShare = 3;
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
 constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
@@ -79,6 +87,9 @@ struct CrossLayout {
 constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it
 constexpr size_t kCrCounters = 192;  // next unit, CTAs that are done
 
+// 256 query rows per item where the runs have more than 128 on average: two query tiles share each key tile's
+// load, which for long runs is what counts (512 queries over 8,192 keys x 76 heads with items of 128 rows: every
+// key tile loaded twice as often); short runs would leave the second tile empty and its part of shared memory unused.
 MLA_HD int cross_rows(int B, int64_t total_q) { return total_q > (int64_t)kCrTile * B ? 2 * kCrTile : kCrTile; }
 
 MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {

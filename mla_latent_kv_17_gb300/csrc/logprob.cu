@@ -12,8 +12,13 @@
 // (from L2) for the tokens that reach it.  Rows where more than kCandidates do (many equal logits) take
 // one pass for each alternative instead.
 //
-// A CTA takes a row; with few rows a cluster of up to eight CTAs shares one, its parts joined through
-// distributed shared memory.
+// A CTA takes a row after the other, the next one's first loads under the end of the present one; with few
+// rows a cluster of up to eight CTAs shares one, its parts joined through distributed shared memory.
+//
+// 4,096 rows of 131,072 bf16 logits: 167 us for the sums alone (1.07 GB, 0.95 of a copy's rate), 190 with ranks, 211
+// with 20 alternatives: issue slots are 58 % busy, DRAM 65 %.  16-bit logits are therefore compared and
+// clamped in pairs, and summed in packed fp32.  The same bytes in fp32: 177 us.  Few rows: 9 us, a chain of
+// the loads, the joins and (with several CTAs) two cluster barriers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,8 +35,10 @@ namespace {
 constexpr int kLpSms = 152;          // a GB300's; only the grid's shape depends on it
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpBatch = 8;         // 16-byte units of a thread in flight together
-constexpr int kLpCtas = 3;          // CTAs per SM
+// 16-byte units of a thread in flight together, and CTAs per SM: 4,096 rows of 131,072 without alternatives 189 us;
+// 4 and 4: 236, 12 and 2: 226, 16 and 2: 198
+constexpr int kLpBatch = 8;
+constexpr int kLpCtas = 3;
 constexpr int kLpMaxTop = 64;
 constexpr int kCandidates = 1024;   // at least kLpMaxTop units' values
 constexpr int kListed = 1024;       // batches that are read again
@@ -614,7 +621,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(LogprobArg
 
 template <typename T>
 mla_status launch_logprobs(LogprobArgs a, int64_t N, cudaStream_t stream) {
-    // CTAs per row: as many as the SMs take at once while each still has a batch of units a thread
+    // CTAs per row: as many as the SMs take at once while each thread still has a batch of units (16 rows of 131,072:
+    // 8.7 us with four CTAs each, 18 with one)
     const int64_t units = ((int64_t)a.V + T::kUnit - 1) / T::kUnit;
     int parts = 1;
     while (parts < kLpMaxCluster && N * parts * 2 <= 304 && units >= 2 * parts * kLpThreads * kLpBatch) parts *= 2;
