@@ -12,13 +12,13 @@
 // unit, as in the causal prefill: S = Q K^T on tcgen05 into TMEM, online softmax with one thread per
 // query row, P as bf16 over its scores in TMEM, O += P V.  The loads and first scores of the next unit
 // run under the last softmax and the epilogue of the present one.
-//   256 rows: two query tiles share the keys and take turns on the tensor pipe.  1,001 queries over 9,193 keys,
+//   256 rows, for many long runs: two query tiles share the keys and take turns on the tensor pipe.  1,001 queries over 9,193 keys,
 //   causal, 128 heads: 527 us, 0.72 of the measured bf16 rate.  A key tile takes 3,650 cycles where its MMAs take
 //   2,560: the warp that issues them is the narrowest place (about 60 cycles an operation, 450 for waits and
 //   commits), then shared memory (8 KB of operands in the 64 cycles of a score operation).
-//   128 rows, for short runs: one query tile with two score buffers, more of the shared memory for keys and
-//   values, whose way from memory bounds the call: 64 single tokens over 256 - 2,048 keys, 16 heads: 101 us, 0.88
-//   of the copy rate.
+//   128 rows: one query tile with two score buffers and more of the shared memory for keys and values.  8 ragged
+//   prompts of 200 - 1,024 queries over 256 - 2,048 keys, 32 heads: 117 us; 64 single tokens over 256 - 2,048 keys,
+//   16 heads: 101 us, 0.88 of the copy rate.
 // Keys and values go round one ring of 16-KB boxes in the order of their first use: with a key buffer twice and
 // a value buffer once instead, the values came a load's latency late for the first of two query tiles (3,800
 // cycles a key tile).  Two tiles ahead of their load they are brought into L2 where two query tiles share them
@@ -87,20 +87,29 @@ struct CrossLayout {
 constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it
 constexpr size_t kCrCounters = 192;  // next unit, CTAs that are done
 
-// 256 query rows per item where the runs have more than 128 on average: two query tiles share each key tile's
-// load, which for long runs is what counts (512 queries over 8,192 keys x 76 heads with items of 128 rows: every
-// key tile loaded twice as often); short runs would leave the second tile empty and its part of shared memory unused.
-MLA_HD int cross_rows(int B, int64_t total_q) { return total_q > (int64_t)kCrTile * B ? 2 * kCrTile : kCrTile; }
+// Query rows per item: 256 (two query tiles that share each key tile's load) or 128.  Two share where the keys and
+// values of all heads do not stay in L2 (192 MB and more), the runs of keys are long (1,536 on average) and no
+// more than a quarter of the tiles would be empty; else smaller items balance better and overlap their ends.
+// Measured, us with 128 and with 256 rows (runs x queries x keys x heads): 4 x 512 x 8,192 x 128 1,119 / 941,
+// 1 x 1,001 x 9,193 x 128 562 / 533, 8 x 1,024 x 2,048 x 32 290 / 254, 1 x 256 x 16,000 x 128 347 / 297; fewer bytes:
+// 2 x 2,048 x 4,096 x 16 123 / 152, 4 x 384 x 4,608 x 16 101 / 107; short keys: 4 x 512 x 1,024 x 128 154 / 181;
+// half-empty pairs: 8 x 300 x 4,000 x 64 451 / 467.
+MLA_HD int cross_rows(int B, int H, int64_t total_q, int64_t total_k) {
+    const int64_t q = total_q / B, tiles = (q + kCrTile - 1) / kCrTile, pairs = (tiles + 1) / 2;
+    const bool two = q > kCrTile && total_k / B >= 1536 && (int64_t)H * total_k * (4 * kCrDh) >= ((int64_t)192 << 20) &&
+                     8 * pairs <= 5 * tiles;
+    return two ? 2 * kCrTile : kCrTile;
+}
 
 MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {
     CrossLayout L;
-    const int rows = cross_rows(B, total_q);
+    // (room for items of either size)
     // An item of t tiles is cut into n = ceil(t / target) > 1 pieces, and the target is at least the batch's
     // cost / `cuts`: at most `cuts` items are cut, into 2 `cuts` pieces together and `cuts` + 1 each.
-    const int64_t cuts = (int64_t)kCrShare * sms / H + 1, items = total_q / rows + B;
+    const int64_t cuts = (int64_t)kCrShare * sms / H + 1, items = total_q / kCrTile + B;
     L.max_pieces = (int)(items + cuts);
     L.max_splits = (int)cuts;
-    const int64_t by_pieces = 2 * cuts * rows, by_rows = (cuts + 1) * total_q;
+    const int64_t by_pieces = 2 * cuts * 2 * kCrTile, by_rows = (cuts + 1) * total_q;
     L.max_rows = by_pieces < by_rows ? by_pieces : by_rows;
     size_t o = 256;
     L.pieces = o;
@@ -1103,7 +1112,7 @@ extern "C" mla_status mla_cross_plan(const int32_t *cu_q, const int32_t *cu_k, i
     a.total_q = (int)total_q;
     a.total_k = (int)total_k;
     a.causal = causal ? 1 : 0;
-    a.rows = cross_rows(B, total_q);
+    a.rows = cross_rows(B, H, total_q, total_k);
     a.sms = num_sms;
     a.ws = (unsigned char *)workspace;
     a.L = cross_layout(B, H, total_q, num_sms);
@@ -1161,7 +1170,7 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     a.H = H;
     a.total_q = (int)total_q;
     a.total_k = (int)total_k;
-    a.rows = cross_rows(B, total_q);
+    a.rows = cross_rows(B, H, total_q, total_k);
     a.scale_log2 = softmax_scale * kLog2e;
     a.positions = positions;
     a.before_out = before_out;

@@ -30,9 +30,9 @@ def _lib():
 class Case:
     """Packed runs; rows before, between and behind them hold NaN (q, k, entries, v)."""
 
-    def __init__(self, q_lens, k_lens, H, positions, seed, spread=1.0, pad=0, before=False):
-        g = torch.Generator().manual_seed(seed)
-        randn = lambda *s: torch.randn(*s, generator=g).to(BF)
+    def __init__(self, q_lens, k_lens, H, positions, seed, spread=1.0, pad=0, before=False, device="cpu"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        randn = lambda *s: torch.randn(*s, generator=g, device=device).to(BF)
         self.B, self.H, self.positions = len(q_lens), H, positions
         self.cu_q = np.concatenate([[pad], pad + np.cumsum(q_lens)]).astype(np.int32)
         self.cu_k = np.concatenate([[pad], pad + np.cumsum(k_lens)]).astype(np.int32)
@@ -43,9 +43,9 @@ class Case:
         self.scale = float(np.float32(1 / np.sqrt(192 if positions else 128)))
         self.before = None
         if before:
-            lse = 2 + 2 * torch.randn(self.nq, H, generator=g)
-            out = torch.randn(self.nq, H, 128, generator=g)
-            gone = torch.rand(self.nq, H, generator=g) < 0.2
+            lse = 2 + 2 * torch.randn(self.nq, H, generator=g, device=device)
+            out = torch.randn(self.nq, H, 128, generator=g, device=device)
+            gone = torch.rand(self.nq, H, generator=g, device=device) < 0.2
             lse[gone] = -torch.inf
             out[gone] = torch.nan
             self.before = (out, lse)
@@ -73,15 +73,18 @@ class Case:
         self.ws = ws
         return got
 
-    def check(self, got, causal=False):
+    def check(self, got, causal=False, heads=None):
+        """Against the definition, all heads or the given ones."""
         assert ops.status(self.ws) == 0
+        h = slice(None) if heads is None else torch.tensor(heads, device="cuda")
         num = lambda t: t.double().cpu().numpy()
-        q, k = num(self.q_nope), num(self.k_nope)
+        q, k, v = num(self.q_nope[:, h]), num(self.k_nope[h]), num(self.v[h])
         if self.positions:
-            q = np.concatenate([q, num(self.q_rope)], -1)
-            k = np.concatenate([k, np.broadcast_to(num(self.entries)[None, :, 512:], (self.H, self.nk, 64))], -1)
-        before = None if self.before is None else tuple(num(t) for t in self.before)
-        out, lse, mean, dot = prompt_ref.cross(q, k, num(self.v), self.cu_q, self.cu_k, self.scale, causal, before)
+            q = np.concatenate([q, num(self.q_rope[:, h])], -1)
+            k = np.concatenate([k, np.broadcast_to(num(self.entries)[None, :, 512:], (len(k), self.nk, 64))], -1)
+        before = None if self.before is None else tuple(num(t[:, h]) for t in self.before)
+        got = (got[0][:, h], None if got[1] is None else got[1][:, h])
+        out, lse, mean, dot = prompt_ref.cross(q, k, v, self.cu_q, self.cu_k, self.scale, causal, before)
         r = slice(self.cu_q[0], self.cu_q[-1])
         out, lse, mean, dot = out[r], lse[r], mean[r], dot[r]
         e = q.shape[-1] * U * self.scale * dot
@@ -109,6 +112,23 @@ class Case:
 def test_cross(q_lens, k_lens, H, causal, positions):
     c = Case(q_lens, k_lens, H, positions, sum(q_lens) + sum(k_lens) + H).cuda()
     c.check(c.run(causal), causal)
+
+
+# where the keys and values of all heads take 192 MB and more, a pair of query tiles shares them
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,positions,pad", [
+    ([129], [3300], True, 0), ([256], [16000], True, 0), ([400], [3400], False, 0), ([700, 300], [3500, 3100], True, 29),
+    ([1024, 0], [4000, 50], True, 0), ([1000, 24], [3301, 127], True, 0), ([200, 824], [5000, 17], False, 5),
+    ([1, 1023], [9000, 1025], True, 0), ([500, 500, 536], [0, 9000, 100], True, 0), ([385, 639], [100, 5000], True, 0)])
+def test_pairs_of_query_tiles(q_lens, k_lens, positions, pad, causal):
+    c = Case(q_lens, k_lens, 128, positions, sum(q_lens) + sum(k_lens), pad=pad, before=sum(q_lens) % 2 == 1, device="cuda").cuda()
+    got = c.run(causal)
+    assert int(c.ws.buf[24:28].view(torch.int32)) == 256  # rows per item
+    c.check(got, causal, heads=[0, 77, 127])
+    for _ in range(2):
+        again = c.run(causal, ws=c.ws)
+        r = slice(c.cu_q[0], c.cu_q[-1])
+        assert torch.equal(got[0][r], again[0][r]) and torch.equal(got[1][r], again[1][r])
 
 
 @pytest.mark.parametrize("causal", [False, True])
