@@ -413,10 +413,10 @@ struct CrossArgs {
 struct Share {
     float mine, before, lse;
 };
-__device__ __forceinline__ Share share_of(float lse, const float *before, int64_t row) {
+__device__ __forceinline__ Share share_of(float lse, bool joined, float b) {
     Share s{1.f, 0.f, lse};
-    if (before) {
-        const float b = before[row], m = fmaxf(lse, b);
+    if (joined) {
+        const float m = fmaxf(lse, b);
         if (m == -INFINITY) return s;
         const float e0 = expf(b - m), e1 = expf(lse - m), sum = e0 + e1;
         s.mine = e1 / sum;
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
             const int64_t part = whole ? 0 : part_at(p.row0, p.nrows, a.H, p.head);
             Share sh{1.f, 0.f, 0.f};
-            if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse, row);
+            if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse != nullptr, a.before_lse ? a.before_lse[row] : 0.f);
             if (nt > 0) {
                 ok = wait_pv(nt - 1);
                 ok = __all_sync(0xffffffffu, ok);
@@ -981,19 +981,15 @@ __global__ void __launch_bounds__(kCmThreads, 2) cross_merge_kernel(const __grid
     const int64_t tasks = (int64_t)hd->groups * a.H;
     for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
         const int at = (int)(t / a.H), h = (int)(t - (int64_t)at * a.H);
-        int lo = 0, hi = n_splits - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (splits[mid].before <= at)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
+        int lo = -1;  // the last cut item that starts at or before group `at`, 32 of them looked at together
+        for (int i = lane; i - lane < n_splits; i += 32)
+            lo += __popc(__ballot_sync(0xffffffffu, i < n_splits && splits[i].before <= at));
         const CrossSplit s = splits[lo];
         const int r0 = (at - s.before) * kCrGroup, rows = min(kCrGroup, s.nrows - r0);
         const int64_t first = part_at(s.row0, s.nrows, a.H, h) + r0 + lane, pitch = (int64_t)s.nrows * a.H;
         const int64_t row = (int64_t)(s.q0 + r0 + lane) * a.H + h;
         const bool mine = lane < rows;
+        const float before = mine && a.before_lse ? a.before_lse[row] : -INFINITY;
         float top = -INFINITY, sum = 0.f;
         float4 acc[4];
 #pragma unroll
@@ -1031,7 +1027,7 @@ __global__ void __launch_bounds__(kCmThreads, 2) cross_merge_kernel(const __grid
             top = m;
         }
         Share sh{0.f, 0.f, 0.f};
-        if (mine) sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse, row);
+        if (mine) sh = share_of(sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2, a.before_lse != nullptr, before);
         const float f = sum == 0.f ? 0.f : sh.mine / sum;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
