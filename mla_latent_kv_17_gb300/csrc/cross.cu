@@ -23,8 +23,8 @@
 // a value buffer once instead, the values came a load's latency late for the first of two query tiles (3,800
 // cycles a key tile).  Two tiles ahead of their load they are brought into L2 where two query tiles share them
 // (545 -> 531 us; where memory bounds the call it costs 3 %).
-// The pieces of an item leave normalised partial results, which cross_merge_kernel joins (19 us for 28 parts of
-// 256 rows x 16 heads, as long as its 60 MB take at half the copy rate).
+// The pieces of an item leave normalised partial results, which cross_merge_kernel joins (18 us by itself for 9 items
+// of 128 rows in 26 parts x 16 heads, 40 MB: a chain of loads per 32 rows).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,7 +47,8 @@ constexpr int kCrTile = 128;            // query rows of a tile (TMEM lanes), ke
 constexpr int kCrHeadGroup = 8;
 constexpr int kCrMinPiece = 4;          // key tiles
 // An item longer than a third of an SM's share of the work is cut.  (4 x 256 - 512 queries over 1,024 - 8,192 keys x
-// 16 heads with 2, 3, 4, 6, 8 instead of 3: 129, 112, 129, 140, 146 us: parts cost a start, an end and their joining.)
+// 16 heads with 2, 3, 4, 5: 110, 101, 104, 102 us; 2 x 2,048 causal queries over 4,096 x 16: 124, 123, 132, 144: parts
+// cost a start, an end and their joining.)
 constexpr int kCrShare = 3;
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
