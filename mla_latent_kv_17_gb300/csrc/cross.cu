@@ -50,6 +50,7 @@ constexpr int kCrMinPiece = 4;          // key tiles
 // 16 heads with 2, 3, 4, 5: 110, 101, 104, 102 us; 2 x 2,048 causal queries over 4,096 x 16: 124, 123, 132, 144: parts
 // cost a start, an end and their joining.)
 constexpr int kCrShare = 3;
+constexpr int kCrJoin = 8;              // what the joining of parts costs, in key tiles of 128 rows
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
 constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     __shared__ __align__(16) uint32_t s_key[kCpSort];
     __shared__ int4 s_seq[kCpKeep];
     __shared__ int32_t s_off[kCpKeep];
-    __shared__ int s_last;
+    __shared__ int s_last, s_longest;
+    if (threadIdx.x == 0) s_longest = 0;
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
@@ -252,7 +254,8 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
             for (int j = 0; j < tiles; ++j)
                 c += kCrItemCost + key_tiles(seen_by(min(nq, (j + 1) * a.rows), nq, nk, 1));
         }
-        const Four x = block_scan<false, 2>(Four{{tiles, c, 0, 0}}, &all, s_scan);
+        const Four x = block_scan<false, 2>(Four{{tiles, c, 0, 0}}, &all, s_scan);  // (a barrier: s_longest is set)
+        if (tiles > 0) atomicMax(&s_longest, kCrItemCost + key_tiles(nk));
         if (b < a.B) {
             seqs[b] = make_int4(qs, nq, ks, nk);
             item_off[b] = (int32_t)(items + x.v[0] - tiles);
@@ -262,10 +265,18 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     }
     __syncthreads();
 
-    // the items, and those of more than a part of an SM's share in pieces
+    // The items, and those of more than a part of an SM's share in pieces - where that pays: whole ones, longest
+    // first, end within as many rounds of the longest as there are, and within the SM's share and the longest;
+    // pieces end about half a piece after the share, and are joined.  (Us whole and in pieces: 1,024 queries x 2,048
+    // keys x 19 heads 29 / 41, 256 x 8,192 x 128 causal 135 / 181; 512 x 6,000 and 3,000 and 1,000 x 32 146 / 117.)
     const int64_t shares = (int64_t)kCrShare * a.sms;
     const int64_t share = (cost * a.H + shares - 1) / shares;
-    const int target = (int)(share > kCrMinPiece ? share : kCrMinPiece);
+    int target = (int)(share > kCrMinPiece ? share : kCrMinPiece);
+    {
+        const uint32_t rounds = ((uint32_t)items * a.H + a.sms - 1) / a.sms;  // (fits: see the shapes that are taken)
+        const float longest = s_longest, mean = (float)cost * a.H / a.sms;
+        if (fminf(rounds * longest, mean + longest) <= mean + 0.5f * target + (float)(kCrJoin * kCrTile) / a.rows) target = INT32_MAX;
+    }
     Four done{};  // pieces, cut items, their partial rows, their groups of rows
     for (int i0 = 0; i0 < items; i0 += kCpThreads) {
         const int i = i0 + tid;

@@ -312,3 +312,64 @@ def test_empty_and_refusals():
     for bad in ((c.d_cu[0][:-1], c.d_cu[1]), (c.d_cu[0].long(), c.d_cu[1]), (c.d_cu[0].cpu(), c.d_cu[1])):
         with pytest.raises(ValueError):
             ops.plan_cross(c.ws, *bad, c.nk)
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H,causal", [([1024], [1024], 19, False), ([1024], [2048], 19, False),
+                                                    ([256], [8192], 128, True), ([128] * 9, [640] * 9, 16, True)])
+def test_items_that_fill_the_sms_stay_whole(q_lens, k_lens, H, causal):
+    c = Case(q_lens, k_lens, H, True, 9 + H, device="cuda").cuda()
+    got = c.run(causal)
+    assert int(c.ws.buf[36:40].view(torch.int32)) == 0  # cut items
+    c.check(got, causal, heads=[0, H // 2, H - 1])
+
+
+@pytest.mark.parametrize("sms", [1, 7, 76, 1000])
+def test_plans_for_other_numbers_of_sms(sms):
+    c = Case([130, 1, 300], [6000, 9000, 700], 4, True, 40, before=True).cuda()
+    ws = ops.CrossWorkspace(c.B, c.H, c.nq, num_sms=sms)
+    c.check(c.run(True, ws=ws), True)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B", [511, 513, 1025, 3000])
+def test_many_runs(B, causal):
+    g = np.random.default_rng(B)
+    q_lens, k_lens = g.integers(0, 4, B), g.integers(0, 90, B)
+    q_lens[B // 2], k_lens[B // 3], k_lens[B // 2] = 300, 3000, 5000
+    c = Case(q_lens, k_lens, 2, True, B, pad=3).cuda()
+    c.check(c.run(causal), causal)
+
+
+def test_far_keys_and_far_queries():
+    # keys, values, queries and results whose places pass 2^31 elements: the last head's, and the last rows'
+    c = Case([3, 130], [139_000, 1300], 128, True, 41, device="cuda").cuda()
+    assert c.k_nope.numel() > 2 ** 31
+    c.check(c.run(True), True, heads=[0, 127])
+    del c
+    c = Case([131_500, 130], [40, 200], 128, False, 42, device="cuda").cuda()
+    assert c.q_nope.numel() > 2 ** 31
+    got = c.run(True)
+    assert ops.status(c.ws) == 0
+    last = Case([130], [200], 128, False, 43, device="cuda").cuda()  # the last run by itself
+    last.q_nope, last.k_nope = c.q_nope[-130:].contiguous(), c.k_nope[:, -200:].contiguous()
+    last.v = c.v[:, -200:].contiguous()
+    want = last.run(True)
+    last.check(want, True, heads=[0, 127])
+    assert torch.equal(got[0][-130:], want[0]) and torch.equal(got[1][-130:], want[1])
+    assert bool((got[1][:100] == -torch.inf).all()) and bool((got[0][:100] == 0).all())  # they see no key
+
+
+def test_two_graphs_share_a_workspace():
+    a = Case([5, 300], [4000, 900], 4, True, 44).cuda()
+    b = Case([300, 5], [30, 5000], 4, True, 45).cuda()
+    a.run()
+    ws = a.ws
+    b.run(ws=ws)
+    graphs, got = [], []
+    for c, causal in ((a, False), (b, True)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(c.run(causal, ws=ws))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        graphs[i].replay()
+        (a, b)[i].check(got[i], causal=i == 1)
