@@ -49,8 +49,9 @@ constexpr int kCrMinPiece = 4;          // key tiles
 // An item longer than a third of an SM's share of the work is cut.  (4 x 256 - 512 queries over 1,024 - 8,192 keys x
 // 16 heads with 2, 3, 4, 5: 110, 101, 104, 102 us; 2 x 2,048 causal queries over 4,096 x 16: 124, 123, 132, 144: parts
 // cost a start, an end and their joining.)
-constexpr int kCrShare = 3;
+constexpr int kCrShare = 3, kCrShareRest = 2;  // (at most kCrShare: see the layout)
 constexpr int kCrJoin = 8;              // what the joining of parts costs, in key tiles of 128 rows
+constexpr float kCrAlike = 1.2f;        // items are much alike: the longest is at most this much longer than they are on average
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
 constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
@@ -58,7 +59,9 @@ constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
 
 struct CrossHeader {
     uint32_t magic;
-    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, groups, last, reserved[4];
+    int32_t B, H, total_q, total_k, causal, rows, sms, pieces, splits, groups, last;
+    int32_t whole, items;  // heads whose items stay whole, and those (pieces: of the other heads)
+    int32_t reserved[2];
 };
 static_assert(sizeof(CrossHeader) == 64, "plan header is 64 bytes");
 
@@ -76,14 +79,15 @@ constexpr int kCrGroup = 32;
 struct CrossSplit {
     int32_t q0, nrows, row0, parts, before;
 };
-// A part's results of one head, rows row0 .. row0 + nrows of the partials: nrows log-sum-exps (log2 units),
-// and 32 runs of nrows four-column pieces (a warp's 32 rows write and read 512 bytes in a row).
-MLA_HD int64_t part_at(int row0, int nrows, int H, int head) { return (int64_t)row0 * H + (int64_t)head * nrows; }
+// A part's results of one of the `heads` heads with cut items, rows row0 .. row0 + nrows of the partials: nrows
+// log-sum-exps (log2 units), and 32 runs of nrows four-column pieces (a warp's 32 rows write and read 512 bytes in
+// a row).
+MLA_HD int64_t part_at(int row0, int nrows, int heads, int head) { return (int64_t)row0 * heads + (int64_t)head * nrows; }
 
 struct CrossLayout {
     size_t pieces, order, splits, seqs, item_off, part_lse, part_o, total;
     int max_pieces, max_splits;
-    int64_t max_rows;
+    int64_t max_parts;  // rows of partial results, of all heads
 };
 
 constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it
@@ -106,13 +110,12 @@ MLA_HD int cross_rows(int B, int H, int64_t total_q, int64_t total_k) {
 MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {
     CrossLayout L;
     // (room for items of either size)
-    // An item of t tiles is cut into n = ceil(t / target) > 1 pieces, and the target is at least the batch's
-    // cost / `cuts`: at most `cuts` items are cut, into 2 `cuts` pieces together and `cuts` + 1 each.
-    const int64_t cuts = (int64_t)kCrShare * sms / H + 1, items = total_q / kCrTile + B;
-    L.max_pieces = (int)(items + cuts);
-    L.max_splits = (int)cuts;
-    const int64_t by_pieces = 2 * cuts * 2 * kCrTile, by_rows = (cuts + 1) * total_q;
-    L.max_rows = by_pieces < by_rows ? by_pieces : by_rows;
+    // An item of t tiles of a head is cut into n = ceil(t / target) > 1 pieces, and the target is at least the h
+    // heads' cost / `cuts`: cuts / h items are cut at most, into 2 cuts / h pieces together and cuts / h + 1 each.
+    const int64_t cuts = (int64_t)kCrShare * sms, items = total_q / kCrTile + B;
+    L.max_pieces = (int)(2 * items + 4 + cuts);  // whole ones, then the others
+    L.max_splits = (int)(items < cuts ? items : cuts);
+    L.max_parts = (cuts + H) * (total_q < 4 * kCrTile ? total_q : 4 * kCrTile);
     size_t o = 256;
     L.pieces = o;
     o = align_up(o + sizeof(CrossPiece) * (size_t)L.max_pieces, 256);
@@ -125,9 +128,9 @@ MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {
     L.item_off = o;
     o = align_up(o + sizeof(int32_t) * (size_t)(B + 1), 256);
     L.part_lse = o;
-    o = align_up(o + sizeof(float) * (size_t)L.max_rows * H, 256);
+    o = align_up(o + sizeof(float) * (size_t)L.max_parts, 256);
     L.part_o = o;
-    o = align_up(o + sizeof(float) * (size_t)L.max_rows * H * kCrDh, 256);
+    o = align_up(o + sizeof(float) * (size_t)L.max_parts * kCrDh, 256);
     L.total = o;
     return L;
 }
@@ -265,18 +268,33 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     }
     __syncthreads();
 
-    // The items, and those of more than a part of an SM's share in pieces - where that pays: whole ones, longest
-    // first, end within as many rounds of the longest as there are, and within the SM's share and the longest;
-    // pieces end about half a piece after the share, and are joined.  (Us whole and in pieces: 1,024 queries x 2,048
-    // keys x 19 heads 29 / 41, 256 x 8,192 x 128 causal 135 / 181; 512 x 6,000 and 3,000 and 1,000 x 32 146 / 117.)
-    const int64_t shares = (int64_t)kCrShare * a.sms;
-    const int64_t share = (cost * a.H + shares - 1) / shares;
-    int target = (int)(share > kCrMinPiece ? share : kCrMinPiece);
-    {
-        const uint32_t rounds = ((uint32_t)items * a.H + a.sms - 1) / a.sms;  // (fits: see the shapes that are taken)
+    // Items of more than a third of an SM's share are cut, where that pays: whole ones, longest first, end within
+    // as many rounds of the longest as there are, and within the share and the longest; pieces end about half a
+    // piece after the share, and are joined.  (Us whole and in pieces: 1,024 queries x 2,048 keys x 19 heads 29 / 41,
+    // 256 x 8,192 x 128 causal 135 / 181; 512 x 6,000 and 3,000 and 1,000 x 32 146 / 117.)
+    // Where the items are much alike, those of the first heads stay whole, as many units as fill all SMs equally
+    // often, and the other heads' are cut, more than half of an SM's share of them.  (Us before and so: 5 x 512 x
+    // 3,000 x 32 heads 189 / 139, 512 x 4,096 x 40 74 / 62, 1,001 x 9,193 x 128 causal 532 / 497; by thirds 142, 62,
+    // 502.  Where the longest is 1.8 times the mean, 30 x 1 x 50 - 8,750 x 16, 193 / 243: the last whole ones are long.)
+    int whole = a.H, target = INT32_MAX;
+    if (items > 0) {
+        const uint32_t units = (uint32_t)items * a.H, rounds = (units + a.sms - 1) / a.sms;  // (fits: see the shapes)
         const float longest = s_longest, mean = (float)cost * a.H / a.sms;
-        if (fminf(rounds * longest, mean + longest) <= mean + 0.5f * target + (float)(kCrJoin * kCrTile) / a.rows) target = INT32_MAX;
+        const bool alike = longest * items <= kCrAlike * cost;
+        const int some = alike ? (int)((rounds - 1) * a.sms / (uint32_t)items) : 0;
+        const int64_t shares = (int64_t)(some > 0 ? kCrShareRest : kCrShare) * a.sms;
+        const int64_t share = (cost * (a.H - some) + shares - 1) / shares;
+        const int least = (int)(share > kCrMinPiece ? share : kCrMinPiece);
+        if (fminf(rounds * longest, mean + longest) > mean + 0.5f * least + (float)(kCrJoin * kCrTile) / a.rows) {
+            whole = some;
+            target = least;
+        }
     }
+    const int cut_heads = a.H - whole, cut_at = whole > 0 ? (int)(items + 3) & ~3 : 0;  // and their pieces' place
+    auto key_of = [&](const CrossPiece &q, int i) {  // (one query tile takes about two thirds of two)
+        const int length = (q.g1 - q.g0) * (q.nrows > kCrTile ? 3 : 2);
+        return (uint32_t)(0xFFFF - min(length, 0xFFFF)) << 16 | (uint32_t)i;
+    };
     Four done{};  // pieces, cut items, their partial rows, their groups of rows
     for (int i0 = 0; i0 < items; i0 += kCpThreads) {
         const int i = i0 + tid;
@@ -301,6 +319,14 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
             tiles = key_tiles(seen_by(r0 + p.nrows, s.y, s.w, a.causal));
             n = tiles > target ? (tiles + target - 1) / target : 1;
         }
+        if (whole > 0 && i < items) {
+            CrossPiece q = p;
+            q.g1 = tiles;
+            q.row0 = -1;
+            pieces[i] = q;
+            if (i < kCpSort) s_key[i] = key_of(q, i);
+        }
+        if (cut_heads == 0) continue;
         int at = i;  // (nothing cut: each item is a piece)
         int64_t row0 = -1;
         if (__syncthreads_or(n > 1) || done.v[1] > 0) {
@@ -321,10 +347,8 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
             q.g0 = (int)((int64_t)tiles * k / n);
             q.g1 = (int)((int64_t)tiles * (k + 1) / n);
             q.row0 = n > 1 ? (int)(row0 + (int64_t)k * q.nrows) : -1;
-            pieces[at + k] = q;
-            // (one query tile takes about two thirds of two)
-            const int length = (q.g1 - q.g0) * (q.nrows > kCrTile ? 3 : 2);
-            if (at + k < kCpSort) s_key[at + k] = (uint32_t)(0xFFFF - min(length, 0xFFFF)) << 16 | (uint32_t)(at + k);
+            pieces[cut_at + at + k] = q;
+            if (cut_at + at + k < kCpSort) s_key[cut_at + at + k] = key_of(q, at + k);
         };
         if (n <= kCpFew)
             for (int k = 0; k < n; ++k) emit(p, at, row0, tiles, k, n);
@@ -350,17 +374,21 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     // others leave.
     const int np = (int)done.v[0];
     if (tid == 0) s_last = 0;
-    if (np <= kCpSort) {
-        const int whole = (np + 3) & ~3;
-        if (tid < whole - np) s_key[np + tid] = 0xFFFFFFFFu;
+    auto sort = [&](int from, int n, int heads, bool last) {
+        const int rounded = (n + 3) & ~3;
+        if (from + rounded > kCpSort) {
+            for (int i = tid; i < n; i += kCpThreads) order[from + i] = from + i;
+            return;
+        }
+        if (tid < rounded - n) s_key[from + n + tid] = 0xFFFFFFFFu;
         __syncthreads();
-        for (int i = tid; i < np; i += kCpThreads) {
-            const uint32_t key = s_key[i];
+        for (int i = tid; i < n; i += kCpThreads) {
+            const uint32_t key = s_key[from + i];
             int place = 0;
             uint32_t least = key;
             int64_t behind = 0;  // the lengths of this piece and of those behind it
-            for (int j = 0; j < whole; j += 4) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(s_key + j);
+            for (int j = 0; j < rounded; j += 4) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(s_key + from + j);
                 const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -369,13 +397,15 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
                     behind += k4[k] >= key ? 0xFFFF - (int)(k4[k] >> 16) : 0;
                 }
             }
-            order[place] = i;
+            order[from + place] = from + i;
             const int longest = 0xFFFF - (int)(least >> 16);
-            if (behind * a.H <= (int64_t)longest * a.sms && 2 * (0xFFFF - (int)(key >> 16)) <= longest) atomicAdd(&s_last, 1);
+            if (last && behind * heads <= (int64_t)longest * a.sms && 2 * (0xFFFF - (int)(key >> 16)) <= longest)
+                atomicAdd(&s_last, 1);
         }
-    } else {
-        for (int i = tid; i < np; i += kCpThreads) order[i] = i;
-    }
+    };
+    __syncthreads();
+    if (whole > 0) sort(0, (int)items, whole, cut_heads == 0);
+    if (cut_heads > 0) sort(cut_at, np, cut_heads, true);
     __syncthreads();
     if (tid == 0) {
         int *counters = reinterpret_cast<int *>(a.ws + kCrCounters);
@@ -393,6 +423,8 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         h.splits = (int32_t)done.v[1];
         h.groups = (int32_t)done.v[3];
         h.last = s_last;
+        h.whole = whole;
+        h.items = whole > 0 ? (int32_t)items : 0;
         *reinterpret_cast<CrossHeader *>(a.ws) = h;
     }
 }
@@ -624,7 +656,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const CrossLayout L = cross_layout(a.B, a.H, a.total_q, hd->sms);
             const CrossPiece *pieces = reinterpret_cast<const CrossPiece *>(a.ws + L.pieces);
             const int32_t *order = reinterpret_cast<const int32_t *>(a.ws + L.order);
-            const int total = hd->pieces * a.H, n = hd->pieces - hd->last;  // (the last ones: see the plan)
+            // whole items of the first heads, then the other heads' pieces; the last list's last ones for all its heads
+            const int first = hd->items * hd->whole, cut_heads = a.H - hd->whole;
+            const int total = first + hd->pieces * cut_heads;
             for (int i = 0; ok; ++i) {
                 const int j = i & 1;
                 if (i >= 2) ok = wait_bounded(u_empty(j), ((i >> 1) - 1) & 1, abort_flag);
@@ -632,16 +666,24 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 const int u = atomicAdd(&counters[0], 1);
                 CrossPiece d;
                 d.head = -1;
-                if (u < n * a.H) {
-                    // a group of heads: each piece for all of them, in the pieces' order
-                    const int h0 = u / (kCrHeadGroup * n) * kCrHeadGroup, hg = min(kCrHeadGroup, a.H - h0);
-                    const int r = u - h0 * n;
-                    d = pieces[order[r / hg]];
-                    d.head = h0 + r % hg;
-                } else if (u < total) {
-                    const int r = u - n * a.H;
-                    d = pieces[order[n + r / a.H]];
-                    d.head = r % a.H;
+                if (u < total) {
+                    const bool cut = u >= first;
+                    int r = cut ? u - first : u;
+                    const int from = cut && hd->whole > 0 ? (hd->items + 3) & ~3 : 0, heads = cut ? cut_heads : hd->whole;
+                    const int n = (cut ? hd->pieces : hd->items) - (cut || cut_heads == 0 ? hd->last : 0);
+                    int head;
+                    if (r < n * heads) {
+                        // a group of heads: each piece for all of them, in the pieces' order
+                        const int h0 = r / (kCrHeadGroup * n) * kCrHeadGroup, hg = min(kCrHeadGroup, heads - h0);
+                        r -= h0 * n;
+                        d = pieces[order[from + r / hg]];
+                        head = h0 + r % hg;
+                    } else {
+                        r -= n * heads;
+                        d = pieces[order[from + n + r / heads]];
+                        head = r % heads;
+                    }
+                    d.head = (cut ? hd->whole : 0) + head;
                 }
                 slots[j] = d;
                 mbar_arrive(u_full(j));
@@ -911,7 +953,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const float lse2 = l == 0.f ? -INFINITY : m + log2f(l), inv = l == 0.f ? 0.f : 1.f / l;
             const bool whole = p.row0 < 0, mine = r < p.nrows;
             const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
-            const int64_t part = whole ? 0 : part_at(p.row0, p.nrows, a.H, p.head);
+            const int64_t part = whole ? 0 : part_at(p.row0, p.nrows, a.H - hd->whole, p.head - hd->whole);
             Share sh{1.f, 0.f, 0.f};
             if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse != nullptr, a.before_lse ? a.before_lse[row] : 0.f);
             if (nt > 0) {
@@ -990,16 +1032,17 @@ __global__ void __launch_bounds__(kCmThreads, 2) cross_merge_kernel(const __grid
     const float *part_lse = reinterpret_cast<const float *>(a.ws + L.part_lse);
     const float *part_o = reinterpret_cast<const float *>(a.ws + L.part_o);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_splits = hd->splits;
-    const int64_t tasks = (int64_t)hd->groups * a.H;
+    const int heads = a.H - hd->whole;
+    const int64_t tasks = (int64_t)hd->groups * heads;
     for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
-        const int at = (int)(t / a.H), h = (int)(t - (int64_t)at * a.H);
+        const int at = (int)(t / heads), h = (int)(t - (int64_t)at * heads);  // (of the heads with cut items)
         int lo = -1;  // the last cut item that starts at or before group `at`, 32 of them looked at together
         for (int i = lane; i - lane < n_splits; i += 32)
             lo += __popc(__ballot_sync(0xffffffffu, i < n_splits && splits[i].before <= at));
         const CrossSplit s = splits[lo];
         const int r0 = (at - s.before) * kCrGroup, rows = min(kCrGroup, s.nrows - r0);
-        const int64_t first = part_at(s.row0, s.nrows, a.H, h) + r0 + lane, pitch = (int64_t)s.nrows * a.H;
-        const int64_t row = (int64_t)(s.q0 + r0 + lane) * a.H + h;
+        const int64_t first = part_at(s.row0, s.nrows, heads, h) + r0 + lane, pitch = (int64_t)s.nrows * heads;
+        const int64_t row = (int64_t)(s.q0 + r0 + lane) * a.H + hd->whole + h;
         const bool mine = lane < rows;
         const float before = mine && a.before_lse ? a.before_lse[row] : -INFINITY;
         float top = -INFINITY, sum = 0.f;

@@ -373,3 +373,19 @@ def test_two_graphs_share_a_workspace():
     for i in (0, 1, 1, 0, 1, 0, 0):
         graphs[i].replay()
         (a, b)[i].check(got[i], causal=i == 1)
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H,causal,sms,pays", [
+    ([512] * 5, [3000] * 5, 32, False, 0, True), ([1001], [9193], 128, True, 0, True), ([512], [4096], 40, True, 0, True),
+    ([130, 129], [2000, 2000], 16, False, 7, True), ([300], [5000], 3, True, 2, True),
+    # 11 units of 24 + 2 key tiles: three rounds on 4 SMs end at 78, in pieces they would at 71.5 + 5 + 8
+    ([1], [3000], 11, True, 4, False)])
+def test_the_first_heads_stay_whole(q_lens, k_lens, H, causal, sms, pays):
+    c = Case(q_lens, k_lens, H, True, 50 + H, before=H < 100, device="cuda").cuda()
+    ws = ops.CrossWorkspace(c.B, H, c.nq, num_sms=sms)
+    got = c.run(causal, ws=ws)
+    whole, cut = int(ws.buf[48:52].view(torch.int32)), int(ws.buf[36:40].view(torch.int32))
+    assert 0 < whole < H and cut > 0 if pays else whole == H and cut == 0
+    c.check(got, causal, heads=sorted({0, whole - 1, min(whole, H - 1), H - 1}))
+    again = c.run(causal, ws=ws)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
