@@ -50,7 +50,7 @@ constexpr int kCrMinPiece = 4;          // key tiles
 // 16 heads with 2, 3, 4, 5: 110, 101, 104, 102 us; 2 x 2,048 causal queries over 4,096 x 16: 124, 123, 132, 144: parts
 // cost a start, an end and their joining.)
 constexpr int kCrShare = 3, kCrShareRest = 2;  // (at most kCrShare: see the layout)
-constexpr int kCrJoin = 8;              // what the joining of parts costs, in key tiles of 128 rows
+constexpr int kCrJoin = 8;              // what the joining of parts costs, in key tiles
 constexpr float kCrAlike = 1.2f;        // items are much alike: the longest is at most this much longer than they are on average
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     // Items of more than a third of an SM's share are cut, where that pays: whole ones, longest first, end within
     // as many rounds of the longest as there are, and within the share and the longest; pieces end about half a
     // piece after the share, and are joined.  (Us whole and in pieces: 1,024 queries x 2,048 keys x 19 heads 29 / 41,
-    // 256 x 8,192 x 128 causal 135 / 181; 512 x 6,000 and 3,000 and 1,000 x 32 146 / 117.)
+    // 256 x 8,192 x 128 causal 135 / 181, 256 x 32,000 x 128 490 / 538; 512 x 6,000 and 3,000 and 1,000 x 32 146 / 117.)
     // Where the items are much alike, those of the first heads stay whole, as many units as fill all SMs equally
     // often, and the other heads' are cut, more than half of an SM's share of them.  (Us before and so: 5 x 512 x
     // 3,000 x 32 heads 189 / 139, 512 x 4,096 x 40 74 / 62, 1,001 x 9,193 x 128 causal 532 / 497; by thirds 142, 62,
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         const int64_t shares = (int64_t)(some > 0 ? kCrShareRest : kCrShare) * a.sms;
         const int64_t share = (cost * (a.H - some) + shares - 1) / shares;
         const int least = (int)(share > kCrMinPiece ? share : kCrMinPiece);
-        if (fminf(rounds * longest, mean + longest) > mean + 0.5f * least + (float)(kCrJoin * kCrTile) / a.rows) {
+        if (fminf(rounds * longest, mean + longest) > mean + 0.5f * least + kCrJoin) {
             whole = some;
             target = least;
         }
