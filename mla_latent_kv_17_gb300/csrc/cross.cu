@@ -3,9 +3,9 @@
 // (mla_cross_attention).
 //
 // cross_plan_kernel: one CTA cuts the batch into items - a tile of 128 or 256 query rows of a run
-// with the key tiles (of 128) it sees - and items whose keys would keep one SM much longer than
-// the others' share into pieces, and orders the pieces by falling length.  The list is the same for
-// every head.  3 us (5.5 where keys are cut).
+// with the key tiles (of 128) it sees - and, where whole items would leave SMs idle at the end, the
+// longer ones into pieces: those of all heads, or of the last ones.  Items and pieces are ordered by
+// falling length; the lists are the same for all their heads.  3 us (5 - 7 where keys are cut).
 //
 // cross_kernel: a persistent CTA per SM takes units (a piece and a head) from a counter, longest
 // pieces first, groups of eight heads in turn so that the keys and values in use stay in L2.  Per
@@ -13,9 +13,10 @@
 // query row, P as bf16 over its scores in TMEM, O += P V.  The loads and first scores of the next unit
 // run under the last softmax and the epilogue of the present one.
 //   256 rows, for many long runs: two query tiles share the keys and take turns on the tensor pipe.  1,001 queries over 9,193 keys,
-//   causal, 128 heads: 527 us, 0.72 of the measured bf16 rate.  A key tile takes 3,650 cycles where its MMAs take
-//   2,560: the warp that issues them is the narrowest place (about 60 cycles an operation, 450 for waits and
-//   commits), then shared memory (8 KB of operands in the 64 cycles of a score operation).
+//   causal, 128 heads: 497 us with plan and joining, 0.76 of the measured bf16 rate (466 us, 0.82, by itself).  A key
+//   tile takes 3,650 cycles where its MMAs take 2,560: the warp that issues them is the narrowest place (about 60
+//   cycles an operation, and 120 a wait, even where there is nothing to wait for), then shared memory (8 KB of
+//   operands in the 64 cycles of a score operation).
 //   128 rows: one query tile with two score buffers and more of the shared memory for keys and values.  8 ragged
 //   prompts of 200 - 1,024 queries over 256 - 2,048 keys, 32 heads: 117 us; 64 single tokens over 256 - 2,048 keys,
 //   16 heads: 101 us, 0.88 of the copy rate.
