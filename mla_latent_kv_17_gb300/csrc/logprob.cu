@@ -368,53 +368,16 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(LogprobArg
         // the largest and the second largest of the stripe's batches, and where the largest one is
         float top = -INFINITY, second = -INFINITY;
         int top_at = u0 + tid;
+        bool here = true;  // the batch is in v, or on its way
         for (int u = u0 + tid; u < u1; u += kLpBatch * kLpThreads) {
-            if (u != u0 + tid) load_batch(row, u, u1, v);
+            if (!here) load_batch(row, u, u1, v);
+            here = false;
             const float most = T::most(v, kLpBatch);
+            // A whole batch is read while the one before it is worked on, each unit as soon as its place is free.
+            const int un = u + kLpBatch * kLpThreads;
+            const bool roll = un >= row.whole_begin() && un + (kLpBatch - 1) * kLpThreads < min(u1, row.whole_end());
+            const uint4 *from = row.at(un);
             if (most == -INFINITY) continue;  // all masked
-            second = fmaxf(second, fminf(top, most));
-            if (most > top) {
-                top = most;
-                top_at = u;
-            }
-            const float d = fmaxf((t.m - top) * c, -200.f), g = ptx::ex2_approx(d);
-            // two chains of each sum
-            uint64_t s2[2] = {pair(t.s * g, 0.f), 0}, w2[2] = {pair(g * (t.w + d * t.s), 0.f), 0};
-            t.m = top;
-            const uint64_t neg_m = pair(-top, -top);
-            // 2^-160 is 0 in fp32.  (Rounded down, so that it stays below the maximum however large that is; at the
-            // bottom of the range, where nothing does, masked tokens are told apart below.)
-            const typename T::Low low = T::low_of(__fadd_rd(top, span));
-            const bool bottom = top < -1e37f;
-#pragma unroll
-            for (int q = 0; q < kLpBatch; ++q) {
-                if (bottom) break;
-                uint64_t x[E / 2];
-                T::pairs(v[q], low, x);
-#pragma unroll
-                for (int i = 0; i < E / 2; ++i) {
-                    const uint64_t y = mul2(add2(x[i], neg_m), c2);
-                    const float2 e = halves(y);
-                    const uint64_t p = pair(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
-                    s2[i & 1] = add2(s2[i & 1], p);
-                    w2[i & 1] = fma2(p, y, w2[i & 1]);
-                }
-            }
-            const float2 ss = halves(add2(s2[0], s2[1])), ww = halves(add2(w2[0], w2[1]));
-            t.s = ss.x + ss.y;
-            t.w = ww.x + ww.y;
-            if (bottom) {
-                for (int q = 0; q < kLpBatch; ++q) {
-                    float f[E];
-                    T::unpack(v[q], f);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float y = fmaxf((f[i] - top) * c, -200.f), e = ptx::ex2_approx(y);
-                        t.s += e;
-                        t.w = fmaf(e, y, t.w);
-                    }
-                }
-            }
             if (most >= mine) {
                 float ahead = 0.f;
                 if (u > own) {
@@ -443,6 +406,51 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(LogprobArg
                 }
                 t.ahead += (int)ahead;
             }
+            second = fmaxf(second, fminf(top, most));
+            if (most > top) {
+                top = most;
+                top_at = u;
+            }
+            const float d = fmaxf((t.m - top) * c, -200.f), g = ptx::ex2_approx(d);
+            // two chains of each sum
+            uint64_t s2[2] = {pair(t.s * g, 0.f), 0}, w2[2] = {pair(g * (t.w + d * t.s), 0.f), 0};
+            t.m = top;
+            const uint64_t neg_m = pair(-top, -top);
+            // 2^-160 is 0 in fp32.  (Rounded down, so that it stays below the maximum however large that is; at the
+            // bottom of the range, where nothing does, masked tokens are told apart below.)
+            const typename T::Low low = T::low_of(__fadd_rd(top, span));
+            const bool bottom = top < -1e37f;
+#pragma unroll
+            for (int q = 0; q < kLpBatch; ++q) {
+                if (bottom) break;
+                uint64_t x[E / 2];
+                T::pairs(v[q], low, x);
+                if (roll) v[q] = from[q * kLpThreads];
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    const uint64_t y = mul2(add2(x[i], neg_m), c2);
+                    const float2 e = halves(y);
+                    const uint64_t p = pair(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
+                    s2[i & 1] = add2(s2[i & 1], p);
+                    w2[i & 1] = fma2(p, y, w2[i & 1]);
+                }
+            }
+            const float2 ss = halves(add2(s2[0], s2[1])), ww = halves(add2(w2[0], w2[1]));
+            t.s = ss.x + ss.y;
+            t.w = ww.x + ww.y;
+            if (bottom) {
+                for (int q = 0; q < kLpBatch; ++q) {
+                    float f[E];
+                    T::unpack(v[q], f);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const float y = fmaxf((f[i] - top) * c, -200.f), e = ptx::ex2_approx(y);
+                        t.s += e;
+                        t.w = fmaf(e, y, t.w);
+                    }
+                }
+            }
+            here = roll && !bottom;
         }
         if (n + rows_at_once < a.N) {
             const Row<T> next = row_of(n + rows_at_once);
