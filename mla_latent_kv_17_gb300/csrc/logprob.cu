@@ -15,10 +15,11 @@
 // A CTA takes a row after the other, the next one's first loads under the end of the present one; with few
 // rows a cluster of up to eight CTAs shares one, its parts joined through distributed shared memory.
 //
-// 4,096 rows of 131,072 bf16 logits: 167 us for the sums alone (1.07 GB, 0.95 of a copy's rate), 190 with ranks, 211
-// with 20 alternatives: issue slots are 58 % busy, DRAM 65 %.  16-bit logits are therefore compared and
-// clamped in pairs, and summed in packed fp32.  The same bytes in fp32: 177 us.  Few rows: 9 us, a chain of
-// the loads, the joins and (with several CTAs) two cluster barriers.
+// 4,096 rows of 131,072 bf16 logits: 157 us for the sums alone (1.07 GB, a copy's rate), 179 with ranks of random
+// tokens (160 where all are the best), 195 with the best alternative too, 203 with 20: issue slots are 60 % busy, and a
+// row's end is a chain.  16-bit logits are therefore compared and clamped in pairs, and summed in packed fp32, and a
+// batch is read while the one before is worked on (211 -> 201 us).  The same bytes in fp32: 180 us.  Few rows: 9 us, a
+// chain of the loads, the joins and (with several CTAs) two cluster barriers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
