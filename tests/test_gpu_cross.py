@@ -389,3 +389,23 @@ def test_the_first_heads_stay_whole(q_lens, k_lens, H, causal, sms, pays):
     c.check(got, causal, heads=sorted({0, whole - 1, min(whole, H - 1), H - 1}))
     again = c.run(causal, ws=ws)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_more_pieces_than_are_put_in_order(causal):
+    c = Case([1] * 24, [48_000 + 16 * i for i in range(24)], 1, False, 51, device="cuda").cuda()
+    ws = ops.CrossWorkspace(c.B, c.H, c.nq, num_sms=2000)
+    got = c.run(causal, ws=ws)
+    assert int(ws.buf[32:36].view(torch.int32)) > 2048  # pieces
+    c.check(got, causal)
+
+
+def test_no_queries_in_any_run():
+    c = Case([0, 0], [300, 5], 2, True, 52).cuda()
+    ws = ops.CrossWorkspace(2, 2, 7)  # seven rows that no run has
+    ops.plan_cross(ws, *c.d_cu, c.nk)
+    q = torch.full((7, 2, 192), torch.nan, dtype=BF, device="cuda")
+    out, lse = torch.full((7, 2, 128), 5.0, device="cuda"), torch.full((7, 2), 5.0, device="cuda")
+    ops.cross_attention(ws, q[..., :128].contiguous(), q[..., 128:].contiguous(), c.entries, c.k_nope, c.v, c.scale, out=out,
+                        lse=lse)
+    assert ops.status(ws) == 0 and bool((out == 5).all()) and bool((lse == 5).all())
