@@ -417,7 +417,7 @@ mla_status mla_verify_draft(const float *target, const float *draft, const int32
  * out = 0 and lse = -inf (or the earlier part's result).  Rows of out and lse outside every run stay
  * as they were, and rows of q, entries, k_nope and v outside every run may hold anything; values
  * inside the runs must be finite.  Scores and softmax in fp32, probabilities rounded to bf16 for their
- * product with the values, fp32 accumulation; a call's result depends on its sizes alone.
+ * product with the values, fp32 accumulation; a call's result depends on its runs, its shape and num_sms alone.
  * The plan reads cu_q and cu_k on the device; it serves any number of calls (layers) until they
  * change, one call at a time, and holds the work list, partial results and the status word, which
  * mla_decode_status reads: runs that fall or lie outside are moved up or in and recorded as
