@@ -52,6 +52,8 @@ constexpr int kCrMinPiece = 4;          // key tiles
 // cost a start, an end and their joining.)
 constexpr int kCrShare = 3, kCrShareRest = 2;  // (at most kCrShare: see the layout)
 constexpr int kCrJoin = 8;              // what the joining of parts costs, in key tiles
+constexpr int kCrSms = 152;             // a GB300's (for the choice of the items' size alone)
+constexpr float kCrPair = 1.77f;        // what a key tile takes with two query tiles, against one (3,600 cycles against 2,040)
 constexpr float kCrAlike = 1.2f;        // items are much alike: the longest is at most this much longer than they are on average
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
@@ -94,18 +96,28 @@ struct CrossLayout {
 constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it
 constexpr size_t kCrCounters = 192;  // next unit, CTAs that are done
 
-// Query rows per item: 256 (two query tiles that share each key tile's load) or 128.  Two share where the keys and
-// values of all heads do not stay in L2 (192 MB and more), the runs of keys are long (1,536 on average) and no
-// more than a quarter of the tiles would be empty; else smaller items balance better and overlap their ends.
+// Query rows per item: 256 (two query tiles that share each key tile's load) or 128.  Two share, where no more than
+// a quarter of the tiles would be empty and the runs of keys are long (1,536 on average), if the keys and values of
+// all heads do not stay in L2 (192 MB and more), or if their units, which are fewer and shorter per row, would end
+// sooner: judged for runs of average length, and only where keys are three times the queries, since a causal run's
+// items differ much where they are not.  Else smaller items balance better and overlap their ends.
 // Measured, us with 128 and with 256 rows (runs x queries x keys x heads): 4 x 512 x 8,192 x 128 1,119 / 941,
-// 1 x 1,001 x 9,193 x 128 562 / 533, 8 x 1,024 x 2,048 x 32 290 / 254, 1 x 256 x 16,000 x 128 347 / 297; fewer bytes:
-// 2 x 2,048 x 4,096 x 16 123 / 152, 4 x 384 x 4,608 x 16 101 / 107; short keys: 4 x 512 x 1,024 x 128 154 / 181;
-// half-empty pairs: 8 x 300 x 4,000 x 64 451 / 467.
+// 8 x 1,024 x 2,048 x 32 290 / 254, 1 x 256 x 16,000 x 128 347 / 297; sooner: 2 x 2,048 x 16,384 x 8 305 / 234,
+// 9 x 256 x 2,000 x 16 73 / 54, 2 x 1,024 x 6,000 x 32 209 / 187, 1 x 2,048 x 8,192 x 16 causal 134 / 126; not sooner:
+// 1 x 512 x 4,096 x 40 61 / 88, 1 x 1,024 x 4,000 x 16 43 / 65; causal, keys twice the queries: 2 x 2,048 x 4,096 x 16
+// 123 / 152; short keys: 4 x 512 x 1,024 x 128 154 / 181; half-empty pairs: 8 x 300 x 4,000 x 64 451 / 467.
+// When this many units of this length would end, in key tiles: whole ones in rounds, or cut (see the plan).
+MLA_HD float cross_end(int64_t units, float length) {
+    const float rounds = (float)((units + kCrSms - 1) / kCrSms) * length, cut = 1.1f * units * length / kCrSms + kCrJoin;
+    return rounds < cut ? rounds : cut;
+}
 MLA_HD int cross_rows(int B, int H, int64_t total_q, int64_t total_k) {
-    const int64_t q = total_q / B, tiles = (q + kCrTile - 1) / kCrTile, pairs = (tiles + 1) / 2;
-    const bool two = q > kCrTile && total_k / B >= 1536 && (int64_t)H * total_k * (4 * kCrDh) >= ((int64_t)192 << 20) &&
-                     8 * pairs <= 5 * tiles;
-    return two ? 2 * kCrTile : kCrTile;
+    const int64_t q = total_q / B, k = total_k / B, tiles = (q + kCrTile - 1) / kCrTile, pairs = (tiles + 1) / 2;
+    if (tiles < 2 || 8 * pairs > 5 * tiles || k < 1536) return kCrTile;
+    const bool far = (int64_t)H * total_k * (4 * kCrDh) >= ((int64_t)192 << 20);
+    const float length = (float)k / kCrTile + kCrItemCost;
+    const bool sooner = k >= 3 * q && 1.06f * kCrPair * cross_end(pairs * B * H, length) <= cross_end(tiles * B * H, length);
+    return far || sooner ? 2 * kCrTile : kCrTile;
 }
 
 MLA_HD CrossLayout cross_layout(int B, int H, int64_t total_q, int sms) {

@@ -409,3 +409,12 @@ def test_no_queries_in_any_run():
     ops.cross_attention(ws, q[..., :128].contiguous(), q[..., 128:].contiguous(), c.entries, c.k_nope, c.v, c.scale, out=out,
                         lse=lse)
     assert ops.status(ws) == 0 and bool((out == 5).all()) and bool((lse == 5).all())
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H,causal", [([256] * 9, [2000] * 9, 16, False), ([2048], [8192], 16, True),
+                                                    ([512, 700, 300, 536], [3000, 2400, 3600, 3000], 16, True)])
+def test_pairs_of_query_tiles_that_end_sooner(q_lens, k_lens, H, causal):
+    c = Case(q_lens, k_lens, H, True, 53 + H, before=causal, device="cuda").cuda()
+    got = c.run(causal)
+    assert int(c.ws.buf[24:28].view(torch.int32)) == 256  # rows per item
+    c.check(got, causal, heads=[0, H // 2, H - 1])
