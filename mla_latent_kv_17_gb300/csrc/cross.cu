@@ -494,20 +494,8 @@ __device__ __forceinline__ void st_global8(void *p, const uint32_t (&v)[8]) {
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
-// 32 values of the result's row from element `at` on: f times o, and the earlier part's share.
-__device__ __forceinline__ void store32(const CrossArgs &a, int64_t at, const uint32_t (&o)[32], float f, const Share &s) {
-    float y[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * f;
-    if (s.before != 0.f) {  // (what has no weight may hold anything)
-#pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-            float v[8];
-            ld_global8(a.before_out + at + c, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[c + i] = fmaf(v[i], s.before, y[c + i]);
-        }
-    }
+// 32 values of the result's row from element `at` on.
+__device__ __forceinline__ void store32(const CrossArgs &a, int64_t at, const float (&y)[32]) {
     if (a.out) {
 #pragma unroll
         for (int c = 0; c < 32; c += 8) {
@@ -526,7 +514,7 @@ __device__ __forceinline__ void store32(const CrossArgs &a, int64_t at, const ui
         }
     }
 }
-// The same for four values, scaled already.
+// Four values, scaled already, and the earlier part's share.
 __device__ __forceinline__ void store4(const CrossArgs &a, int64_t at, float4 o, float before) {
     if (before != 0.f) {
         const float4 b = *reinterpret_cast<const float4 *>(a.before_out + at);
@@ -545,7 +533,9 @@ __device__ __forceinline__ bool plan_fits(const CrossArgs &a, const CrossHeader 
            cross_layout(a.B, a.H, a.total_q, hd->sms).total <= a.ws_bytes;
 }
 
-template <int kTiles>
+// kJoined: with an earlier part's result.  (A kernel of its own: without, 8 x 3,384 queries x 38 keys x 32 heads take
+// 155 us instead of 161 - 165.)
+template <int kTiles, bool kJoined>
 __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     cross_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qr,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
@@ -889,6 +879,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             // (rows past the item's compute something nobody reads)
             const int see = r < p.nrows ? seen(r) : p.nk;
             float m = -INFINITY, l = 0.f;  // reference maximum (log2 units), running sum
+            const bool whole = p.row0 < 0, mine = r < p.nrows;
+            const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
+            const float before = kJoined && whole && mine ? a.before_lse[row] : -INFINITY;
             for (int g = 0; g < nt; ++g) {
                 ok = wait_bounded(s_full(barriers(g)), use_of(g) & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -964,20 +957,16 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             if (!ok) break;
             // the row's result, 32 columns at a time, normalised: the whole of it, or a piece's part
             const float lse2 = l == 0.f ? -INFINITY : m + log2f(l), inv = l == 0.f ? 0.f : 1.f / l;
-            const bool whole = p.row0 < 0, mine = r < p.nrows;
-            const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
             const int64_t part = whole ? 0 : part_at(p.row0, p.nrows, a.H - hd->whole, p.head - hd->whole);
             Share sh{1.f, 0.f, 0.f};
-            if (whole && mine) sh = share_of(lse2 * kLn2, a.before_lse != nullptr, a.before_lse ? a.before_lse[row] : 0.f);
-            if (nt > 0) {
-                ok = wait_pv(nt - 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+            if (whole && mine) sh = share_of(lse2 * kLn2, kJoined, before);
+            auto finished = [&]() -> bool {  // the unit's last PV
+                if (nt == 0) return true;
+                ok = __all_sync(0xffffffffu, wait_pv(nt - 1));
                 tc_fence_after();
-            }
-#pragma unroll 1
-            for (int c = 0; c < kCrDh; c += 32) {
-                uint32_t o[32];
+                return ok;
+            };
+            auto output = [&](int c, uint32_t (&o)[32]) {
                 if (nt > 0) {
                     tmem_ld32(cO + c, o);
                     tmem_wait_ld();
@@ -985,18 +974,61 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
-                if (!mine) continue;
-                if (whole) {
-                    store32(a, row * kCrDh + c, o, inv * sh.mine, sh);
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(part_o + part * kCrDh) + r;
+            };
+            if (kJoined && kTiles == 1 && whole) {
+                // the earlier part's row is on its way while PV finishes (what has no weight may hold anything; 8 x 1,750
+                // queries x 13 keys x 64 heads 374 -> 318 us)
+                float e[kCrDh];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        dst[(c / 4 + k) * p.nrows] =
-                            make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                                        __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+                for (int i = 0; i < kCrDh; ++i) e[i] = 0.f;
+                if (sh.before != 0.f) {
+#pragma unroll
+                    for (int i = 0; i < kCrDh; i += 8)
+                        ld_global8(a.before_out + row * kCrDh + i, *reinterpret_cast<float(*)[8]>(e + i));
+                }
+                if (finished()) {
+#pragma unroll
+                    for (int c = 0; c < kCrDh; c += 32) {
+                        uint32_t o[32];
+                        output(c, o);
+                        float y[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            y[i] = fmaf(e[c + i], sh.before, __uint_as_float(o[i]) * (inv * sh.mine));
+                        if (mine) store32(a, row * kCrDh + c, y);
+                    }
+                }
+            } else if (finished()) {
+#pragma unroll 1
+                for (int c = 0; c < kCrDh; c += 32) {
+                    uint32_t o[32];
+                    output(c, o);
+                    if (!mine) continue;
+                    if (whole) {
+                        float y[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * (inv * sh.mine);
+                        if (kJoined && sh.before != 0.f) {  // (their registers leave no room for the whole row)
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8) {
+                                float e[8];
+                                ld_global8(a.before_out + row * kCrDh + c + k, e);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[k + i] = fmaf(e[i], sh.before, y[k + i]);
+                            }
+                        }
+                        store32(a, row * kCrDh + c, y);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(part_o + part * kCrDh) + r;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[(c / 4 + k) * p.nrows] =
+                                make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                                            __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+                    }
                 }
             }
+            if (!ok) break;
             if (nt > 0) {
                 tc_fence_before();
                 __syncwarp();
@@ -1116,6 +1148,10 @@ bool tmap_bf16(CUtensorMap *m, const void *p, int rank, const uint64_t *d, const
     return tmap_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rank, d, s, b);
 }
 
+template <typename K>
+bool grant(K kernel, uint32_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
 // SMs of the current device (0: none), its cross kernels' shared memory granted.
 int cross_device() {
     static int sms[64] = {};
@@ -1123,10 +1159,8 @@ int cross_device() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if (sms[dev] > 0) return sms[dev];
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(cross_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<1>::kSmem) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(cross_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<2>::kSmem) !=
-            cudaSuccess) {
+        !grant(cross_kernel<1, false>, Shape<1>::kSmem) || !grant(cross_kernel<1, true>, Shape<1>::kSmem) ||
+        !grant(cross_kernel<2, false>, Shape<2>::kSmem) || !grant(cross_kernel<2, true>, Shape<2>::kSmem)) {
         cudaGetLastError();
         return 0;
     }
@@ -1243,10 +1277,12 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     a.out = out_dtype == MLA_OUT_FP32 ? (float *)out : nullptr;
     a.out16 = out_dtype == MLA_OUT_BF16 ? (uint16_t *)out : nullptr;
     a.lse = lse;
-    cudaError_t e =
-        a.rows == kCrTile
-            ? launch_pdl(cross_kernel<1>, sms, Shape<1>::kThreads, Shape<1>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a)
-            : launch_pdl(cross_kernel<2>, sms, Shape<2>::kThreads, Shape<2>::kSmem, (cudaStream_t)stream, tqn, tqr, tk, tkr, tv, a);
+    const auto one = before_out ? cross_kernel<1, true> : cross_kernel<1, false>;
+    const auto two = before_out ? cross_kernel<2, true> : cross_kernel<2, false>;
+    cudaError_t e = a.rows == kCrTile ? launch_pdl(one, sms, Shape<1>::kThreads, Shape<1>::kSmem, (cudaStream_t)stream, tqn,
+                                                   tqr, tk, tkr, tv, a)
+                                      : launch_pdl(two, sms, Shape<2>::kThreads, Shape<2>::kSmem, (cudaStream_t)stream, tqn,
+                                                   tqr, tk, tkr, tv, a);
     // (no item has more key tiles than all keys together: short ones are never cut)
     if (e == cudaSuccess && total_k > kCrMinPiece * kCrTile)
         e = launch_pdl(cross_merge_kernel, kCmCtasPerSm * sms, kCmThreads, 0, (cudaStream_t)stream, a);

@@ -418,3 +418,15 @@ def test_pairs_of_query_tiles_that_end_sooner(q_lens, k_lens, H, causal):
     got = c.run(causal)
     assert int(c.ws.buf[24:28].view(torch.int32)) == 256  # rows per item
     c.check(got, causal, heads=[0, H // 2, H - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("q,k,H", [(600, 13, 40), (257, 130, 64), (130, 1, 128)])
+def test_joined_many_queries_few_keys(q, k, H, dtype):
+    c = Case([q, 1, q, 0, q + 7, q], [k, k, 0, k, k + 1, k], H, True, 54 + q, before=True, device="cuda").cuda()
+    got = c.run(out_dtype=dtype)
+    c.check(got, heads=[0, H // 2, H - 1])
+    if dtype == torch.float32:  # in place
+        want, (out, lse) = got, c.before
+        got = c.run(out=out, lse=lse)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
