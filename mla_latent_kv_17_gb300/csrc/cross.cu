@@ -18,7 +18,7 @@
 //   cycles an operation, and 120 a wait, even where there is nothing to wait for), then shared memory (8 KB of
 //   operands in the 64 cycles of a score operation).
 //   128 rows: one query tile with two score buffers and more of the shared memory for keys and values.  8 ragged
-//   prompts of 200 - 1,024 queries over 256 - 2,048 keys, 32 heads: 117 us; 64 single tokens over 256 - 2,048 keys,
+//   prompts of 200 - 1,024 queries over 256 - 2,048 keys, 32 heads: 116 us; 64 single tokens over 256 - 2,048 keys,
 //   16 heads: 101 us, 0.88 of the copy rate.
 // Keys and values go round one ring of 16-KB boxes in the order of their first use: with a key buffer twice and
 // a value buffer once instead, the values came a load's latency late for the first of two query tiles (3,800
