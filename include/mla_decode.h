@@ -421,7 +421,8 @@ mla_status mla_verify_draft(const float *target, const float *draft, const int32
  * The plan reads cu_q and cu_k on the device; it serves any number of calls (layers) until they
  * change, one call at a time, and holds the work list, partial results and the status word, which
  * mla_decode_status reads: runs that fall or lie outside are moved up or in and recorded as
- * MLA_ERR_INDEX.  After MLA_ERR_TIMEOUT the plan has to be made again.  num_sms as for
+ * MLA_ERR_INDEX.  The workspace may hold anything before its first plan, which sets the status word to MLA_OK
+ * before it records; later plans keep an error that has not been read.  After MLA_ERR_TIMEOUT the plan has to be made again.  num_sms as for
  * mla_decode_plan, the same in the first two calls.  1 <= B <= 2^20, total_q <= 2^24, 1 <= H <= 128;
  * workspace and inputs 16-byte aligned, out and before_out 32-byte. */
 size_t mla_cross_workspace_size(int B, int H, int64_t total_q, int num_sms);

@@ -59,6 +59,8 @@ constexpr int kCrAhead = 2;             // key tiles between the prefetch into L
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
 constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
 constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
+// Beside the status word once a plan has been made: memory without them may hold anything where that word is.
+constexpr uint32_t kCrossMarkY = 0x58535441u, kCrossMarkZ = 0x9E3779B9u, kCrossMarkW = 0xC2B2AE35u;
 
 struct CrossHeader {
     uint32_t magic;
@@ -93,7 +95,7 @@ struct CrossLayout {
     int64_t max_parts;  // rows of partial results, of all heads
 };
 
-constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it
+constexpr size_t kCrStatus = 128;    // device status word, where mla_decode_status looks for it, and three marks
 constexpr size_t kCrCounters = 192;  // next unit, CTAs that are done
 
 // Query rows per item: 256 (two query tiles that share each key tile's load) or 128.  Two share, where no more than
@@ -230,7 +232,9 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
     CrossPiece *pieces = reinterpret_cast<CrossPiece *>(a.ws + a.L.pieces);
     CrossSplit *splits = reinterpret_cast<CrossSplit *>(a.ws + a.L.splits);
     int32_t *order = reinterpret_cast<int32_t *>(a.ws + a.L.order);
-    int *status = reinterpret_cast<int *>(a.ws + kCrStatus);
+    uint4 *status = reinterpret_cast<uint4 *>(a.ws + kCrStatus);
+    const uint4 state = *status;  // (looked at by one thread, at the end)
+    bool fell = false;            // some run does not lie as it should
 
     // the runs: starts that fall or lie outside are moved up or in (and recorded), so that runs never
     // overlap and the items fit their places
@@ -247,9 +251,10 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
             ks = min(max(r[2], 0), a.total_k);
             ke = min(max(r[3], 0), a.total_k);
             bad = r[0] != qs || r[1] != qe || r[2] != ks || r[3] != ke || qs > qe || ks > ke;
-            if (bad) record_error(status, MLA_ERR_INDEX);
         }
-        if (__syncthreads_or(bad) || upto.v[1] > 0 || upto.v[3] > 0) {
+        bad = __syncthreads_or(bad);
+        fell |= bad;
+        if (bad || upto.v[1] > 0 || upto.v[3] > 0) {
             // a run starts no earlier than the largest start before it, and ends no earlier
             const Four x = block_scan<true, 4>(Four{{qs, max(qs, qe), ks, max(ks, ke)}}, &all, s_scan);
             qs = (int)max(upto.v[1], x.v[0]);
@@ -439,6 +444,11 @@ __global__ void __launch_bounds__(kCpThreads) cross_plan_kernel(const __grid_con
         h.whole = whole;
         h.items = whole > 0 ? (int32_t)items : 0;
         *reinterpret_cast<CrossHeader *>(a.ws) = h;
+        // The first plan in this memory sets its status word up; a later one keeps an error that nobody has read yet.
+        if (state.y != kCrossMarkY || state.z != kCrossMarkZ || state.w != kCrossMarkW)
+            *status = make_uint4(fell ? MLA_ERR_INDEX : MLA_OK, kCrossMarkY, kCrossMarkZ, kCrossMarkW);
+        else if (fell)
+            record_error(reinterpret_cast<int *>(status), MLA_ERR_INDEX);
     }
 }
 

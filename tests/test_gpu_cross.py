@@ -430,3 +430,28 @@ def test_joined_many_queries_few_keys(q, k, H, dtype):
         want, (out, lse) = got, c.before
         got = c.run(out=out, lse=lse)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_workspace_of_any_content():
+    # the first plan in a workspace sets its status word up, whatever the memory held; later ones keep an unread error
+    c = Case([5, 200], [3000, 129], 3, True, 60).cuda()
+    want = c.run(True)
+    c.check(want, True)
+    bad = torch.tensor([0, 150, 40], dtype=torch.int32, device="cuda")
+    call = lambda ws: ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale)
+    for fill in (0xFF, 0x01, 0x7F):
+        ws = ops.CrossWorkspace(c.B, c.H, c.nq)
+        ws.buf.fill_(fill)
+        got = c.run(True, ws=ws)
+        assert ops.status(ws) == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        ws.buf.fill_(fill)
+        ops.plan_cross(ws, bad, c.d_cu[1], c.nk, causal=True)
+        call(ws)
+        got = c.run(True, ws=ws)  # another plan, and its call, before anybody asks
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert ops.status(ws) == 5 and ops.status(ws) == 0
+        c.run(True, ws=ws)
+        assert ops.status(ws) == 0
+        ops.plan_cross(ws, bad, c.d_cu[1], c.nk, causal=True)
+        assert ops.status(ws) == 5
