@@ -126,6 +126,10 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _stream_of(ws, stream):
+    return ctypes.c_void_p(ws._on_stream(stream, torch.cuda.current_device()))
+
+
 def workspace_size(B: int, H: int, num_sms: int = 0) -> int:
     n = lib().mla_decode_workspace_size(int(B), int(H), int(num_sms))
     if n == 0:
@@ -133,7 +137,35 @@ def workspace_size(B: int, H: int, num_sms: int = 0) -> int:
     return int(n)
 
 
-class Workspace:
+class _Memory:
+    """A workspace's device memory, made (and its header zeroed) on the then current stream.  What calls
+    on any other stream do with it comes after that, and after the work of that stream before it, which
+    the memory may have served; and it is not handed out again before they are done.  (In a captured
+    graph streams are ordered by the capture alone.)"""
+
+    def _made(self):
+        """To be called once self.buf is made."""
+        dev = self.buf.get_device()
+        with _on(dev):
+            self._event = None if torch.cuda.is_current_stream_capturing() else torch.cuda.current_stream().record_event()
+        self._known = {_raw(None, dev)}  # streams whose calls come after the making
+
+    def _on_stream(self, stream, dev) -> int:
+        """The handle of the stream that a call of this workspace goes to, as _raw()."""
+        raw = _raw(stream, dev)
+        if raw not in self._known:
+            if stream is None:
+                stream = torch.cuda.current_stream(dev)
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if self._event is not None and not capturing:  # (no event of one can be waited for in the other)
+                stream.wait_event(self._event)
+                self.buf.record_stream(stream)
+                self._known.add(raw)
+        return raw
+
+
+class Workspace(_Memory):
     """Device workspace holding a plan, the split-KV partials and the status word."""
 
     def __init__(self, B: int, H: int, num_sms: int = 0, device=None):
@@ -141,6 +173,7 @@ class Workspace:
         self.nbytes = workspace_size(B, H, num_sms)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8,
                                device=device or torch.device("cuda", torch.cuda.current_device()))
+        self._made()
         self.topk = None
 
     def ptr(self):
@@ -168,7 +201,7 @@ def plan(ws: Workspace, seq_lens=None, topk: int = 0, num_sms: int = 0, stream=N
     if seq_lens is not None:
         _i32(seq_lens, "seq_lens")
     st = lib().mla_decode_plan(_ptr(seq_lens), ws.B, ws.H, int(topk), _kv_code(kv_dtype), int(num_sms),
-                               ws.ptr(), ws.nbytes, _stream(stream))
+                               ws.ptr(), ws.nbytes, _stream_of(ws, stream))
     _check("mla_decode_plan", st)
     ws.topk = int(topk)
     return ws
@@ -212,7 +245,7 @@ def decode(ws: Workspace, q_nope, q_rope, cache, block_table, seq_lens, softmax_
     out, lse = _outputs(B, H, q_nope.device, out, lse)
     st = lib().mla_decode(ws.ptr(), ws.nbytes, _ptr(q_nope), _ptr(q_rope), _ptr(cache), kv,
                           cache.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-                          B, H, float(softmax_scale), _ptr(out), _ptr(lse), _stream(stream))
+                          B, H, float(softmax_scale), _ptr(out), _ptr(lse), _stream_of(ws, stream))
     _check("mla_decode", st)
     return out, lse
 
@@ -373,7 +406,7 @@ def decode_sparse(ws: Workspace, q_nope, q_rope, cache, block_table, seq_lens, i
     st = lib().mla_decode_sparse(ws.ptr(), ws.nbytes, _ptr(q_nope), _ptr(q_rope), _ptr(cache),
                                  cache.shape[0], _ptr(block_table), block_table.shape[1],
                                  _ptr(seq_lens), _ptr(indices), indices.shape[1], B, H,
-                                 float(softmax_scale), _ptr(out), _ptr(lse), _stream(stream))
+                                 float(softmax_scale), _ptr(out), _ptr(lse), _stream_of(ws, stream))
     _check("mla_decode_sparse", st)
     return out, lse
 
@@ -419,7 +452,7 @@ def inject_stall(enable: bool) -> None:
 
 def status(ws: Workspace, stream=None) -> int:
     """Synchronise and return (and clear) the device-side status code of the workspace."""
-    return int(lib().mla_decode_status(ws.ptr(), ws.nbytes, _stream(stream)))
+    return int(lib().mla_decode_status(ws.ptr(), ws.nbytes, _stream_of(ws, stream)))
 
 
 # ---- several tokens per request: rotary positions, cache write and read, verification ----
@@ -731,7 +764,7 @@ def cache_read(cache, block_table, requests, positions, entries=None, device_sta
     return entries
 
 
-class TreeWorkspace:
+class TreeWorkspace(_Memory):
     """Device workspace of a tree attention over B requests of T drafted tokens and H heads: its
     plan, split-KV partials and status word (status() reads it)."""
 
@@ -746,6 +779,7 @@ class TreeWorkspace:
                 raise MlaError("mla_decode_tree_workspace_size", 1, "invalid arguments")
             self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
             self.buf[:256].zero_()  # no plan yet, no error
+            self._made()
 
     def ptr(self):
         return _ptr(self.buf)
@@ -760,7 +794,7 @@ def plan_tree(ws: TreeWorkspace, seq_lens, tree_lens=None, num_sms: int = 0, str
         _ints(tree_lens, (ws.B,), "tree_lens")
     with _on(dev):
         st = lib().mla_decode_tree_plan(seq_lens.data_ptr(), _at(tree_lens), ws.B, ws.T, ws.H, _kv_code(kv_dtype),
-                                        num_sms, ws.buf.data_ptr(), ws.nbytes, _raw(stream, dev))
+                                        num_sms, ws.buf.data_ptr(), ws.nbytes, ws._on_stream(stream, dev))
     if st:
         _check("mla_decode_tree_plan", st)
     return ws
@@ -806,7 +840,7 @@ def decode_tree(ws: TreeWorkspace, q_nope, q_rope, cache, block_table, seq_lens,
             ws.buf.data_ptr(), ws.nbytes, q_nope.data_ptr(), q_rope.data_ptr(), cache.data_ptr(), kind,
             cache.shape[0], block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), _at(tree_lens),
             tree_mask.data_ptr(), B, T, H, softmax_scale, out.data_ptr(), 1 if out_dtype == torch.bfloat16 else 0,
-            _at(lse), _raw(stream, dev))
+            _at(lse), ws._on_stream(stream, dev))
     if st:
         _check("mla_decode_tree", st)
     return out, lse
@@ -849,7 +883,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
     return num, depths, nxt
 
 
-class CrossWorkspace:
+class CrossWorkspace(_Memory):
     """Device workspace of a cross attention of B query runs of H heads, total_q query rows in all: its
     plan, partial results and status word (status() reads it)."""
 
@@ -865,6 +899,7 @@ class CrossWorkspace:
                 raise MlaError("mla_cross_workspace_size", 1, "invalid arguments")
             self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
             self.buf[:256].zero_()  # no plan yet, no error
+            self._made()
 
     def ptr(self):
         return _ptr(self.buf)
@@ -879,7 +914,7 @@ def plan_cross(ws: CrossWorkspace, cu_q, cu_k, total_k: int, causal: bool = Fals
     _ints(cu_k, (ws.B + 1,), "cu_k")
     with _on(dev):
         st = lib().mla_cross_plan(cu_q.data_ptr(), cu_k.data_ptr(), ws.B, ws.H, ws.total_q, total_k, 1 if causal else 0,
-                                  ws.num_sms, ws.buf.data_ptr(), ws.nbytes, _raw(stream, dev))
+                                  ws.num_sms, ws.buf.data_ptr(), ws.nbytes, ws._on_stream(stream, dev))
     if st:
         _check("mla_cross_plan", st)
     ws.total_k = total_k
@@ -927,7 +962,7 @@ def cross_attention(ws: CrossWorkspace, q_nope, q_rope, entries, k_nope, v, soft
         st = lib().mla_cross_attention(
             ws.buf.data_ptr(), ws.nbytes, q_nope.data_ptr(), _at(q_rope), _at(entries), k_nope.data_ptr(), v.data_ptr(),
             ws.B, H, Nq, Nk, softmax_scale, _at(before_out), _at(before_lse), out.data_ptr(),
-            1 if out_dtype == bf16 else 0, _at(lse), _raw(stream, dev))
+            1 if out_dtype == bf16 else 0, _at(lse), ws._on_stream(stream, dev))
     if st:
         _check("mla_cross_attention", st)
     return out, lse
