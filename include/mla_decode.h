@@ -110,8 +110,9 @@ mla_status mla_decode_status(void *workspace, size_t ws_bytes, void *stream);
 const char *mla_status_string(mla_status status);
 
 /* Limit, in SM clock cycles, of every pipeline wait inside the decode kernel, for the
- * mla_decode / mla_decode_sparse / mla_decode_static calls made after it in this process
- * (0 restores the default, about two seconds).  A wait that runs out records
+ * mla_decode / mla_decode_sparse / mla_decode_static / mla_decode_tree calls made after it in this
+ * process, and of mla_cross_attention's, which wait up to 8,000 cycles more for each 128 keys of
+ * total_k (0 restores the default, about two seconds).  A wait that runs out records
  * MLA_ERR_TIMEOUT in the status word; the kernel then stops issuing work, gives copies and
  * tensor-core operations already in flight a bounded time to land, releases its tensor
  * memory and returns, so the device and the workspace stay usable (the call's out and lse

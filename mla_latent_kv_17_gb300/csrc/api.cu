@@ -339,7 +339,7 @@ bool tree_shape_ok(int B, int T, int H) {
     return B >= 1 && T >= 1 && H >= 1 && T <= kMaxDrafted && H <= kMaxHeads && B <= (1 << 20) / row_tiles(T, H);
 }
 
-// Limit of one pipeline wait in the decode kernel (SM clock cycles), for calls made from now on.
+// Limit of one pipeline wait in the decode and the cross kernel (SM clock cycles), for calls made from now on.
 std::atomic<long long> g_wait_cycles{kDefaultWaitCycles};
 // Injected stall for tests of the timeout path (mla_decode_inject_stall).
 std::atomic<int> g_stall_test{0};
@@ -414,6 +414,9 @@ mla_status run_decode(const DecodeArgs &a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+long long wait_limit() { return g_wait_cycles.load(); }
+
 }  // namespace mla
 
 using namespace mla;

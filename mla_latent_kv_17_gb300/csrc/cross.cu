@@ -34,6 +34,7 @@
 
 #include "common.cuh"
 #include "f32x2.cuh"
+#include "launch.h"
 #include "mla_decode.h"
 #include "sm103_ptx.cuh"
 #include "tc_util.cuh"
@@ -57,6 +58,9 @@ constexpr float kCrPair = 1.77f;        // what a key tile takes with two query 
 constexpr float kCrAlike = 1.2f;        // items are much alike: the longest is at most this much longer than they are on average
 constexpr int kCrAhead = 2;             // key tiles between the prefetch into L2 and the load
 constexpr int kCrItemCost = 2;          // an item's start and end, in key tiles
+// A role may wait as long as another one's unit takes, 3,600 cycles a key tile, so the limit of a wait grows with the
+// keys: by twice that, and a little.
+constexpr long long kCrWaitPerTile = 8000;
 constexpr float kCrRescale = 8.f;       // the reference maximum moves when exceeded by 2^8
 constexpr uint32_t kCrossMagic = 0x4D4C4158u;  // "MLAX"
 // Beside the status word once a plan has been made: memory without them may hold anything where that word is.
@@ -470,6 +474,7 @@ struct CrossArgs {
     int B, H, total_q, total_k, rows;
     float scale_log2;
     int positions;
+    long long wait_cycles;  // limit of a wait
     const float *before_out, *before_lse;
     float *out;       // one of the two
     uint16_t *out16;
@@ -616,6 +621,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     if (!match && threadIdx.x == 0) record_error(status, MLA_ERR_WORKSPACE);
     const int step = hd->causal ? 1 : 0;
     bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, abort_flag, a.wait_cycles); };
 
     // The next unit's piece, from its slot (the whole warp); false: there is none, or a wait ran out.
     int taken = 0;
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     auto next_unit = [&]() -> bool {
         if (!ok) return false;
         const int j = taken & 1;
-        ok = __all_sync(0xffffffffu, wait_bounded(u_full(j), (taken >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, wait(u_full(j), (taken >> 1) & 1));
         if (!ok) return false;
         p = slots[j];
         __syncwarp();
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int total = first + hd->pieces * cut_heads;
             for (int i = 0; ok; ++i) {
                 const int j = i & 1;
-                if (i >= 2) ok = wait_bounded(u_empty(j), ((i >> 1) - 1) & 1, abort_flag);
+                if (i >= 2) ok = wait(u_empty(j), ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 const int u = atomicAdd(&counters[0], 1);
                 CrossPiece d;
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         int freed = 0, freed_boxes = 0;  // items, and boxes up to them, that have been waited for
         auto room = [&](int boxes) -> bool {  // for the boxes up to this number
             while (ok && boxes - freed_boxes > S::kRing) {
-                ok = wait_bounded(empty(freed), (freed >> 3) & 1, abort_flag);
+                ok = wait(empty(freed), (freed >> 3) & 1);
                 freed_boxes += freed & 1 ? 2 : kw;
                 ++freed;
             }
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             if (ntot == 0) continue;
             if (lane == 0) {
                 const int nx = single() ? 1 : 2;
-                if (units > 0) ok = wait_bounded(q_empty, (units - 1) & 1, abort_flag);
+                if (units > 0) ok = wait(q_empty, (units - 1) & 1);
                 if (ok) {
                     mbar_arrive_expect_tx(q_full, nx * kw * kCrBox);
                     for (int x = 0; x < nx; ++x) {
@@ -772,7 +778,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             t += ntot;
             const int valid = p.nk - (p.g0 + ntot - 1) * kCrTile;  // keys of the last tile
             if (ntot == 0 || valid >= kCrTile) continue;
-            ok = __all_sync(0xffffffffu, wait_bounded(landed(tails), (tails >> 2) & 1, abort_flag));
+            ok = __all_sync(0xffffffffu, wait(landed(tails), (tails >> 2) & 1));
             if (!ok) break;
             ++tails;
             for (int i = 0; i < 2; ++i) {
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         // ---------------------------------------------------------------- MMAs
         // the whole warp runs the issue loop (its waits made warp-uniform); one elected lane issues
         auto wait_w = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_quick(bar, parity, abort_flag));
+            return __all_sync(0xffffffffu, wait_quick(bar, parity, abort_flag, a.wait_cycles));
         };
         constexpr uint32_t idesc_s = idesc_bf16_major(128, kCrTile, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_major(128, kCrDh, false, true);
@@ -883,7 +889,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         auto buffer = [&](int g) { return single() ? g & 1 : x; };
         auto barriers = [&](int g) { return single() ? 2 + (g & 1) : x; };
         auto use_of = [&](int g) { return single() ? (g & 1 ? use3 : use2) + (g >> 1) : (x ? use1 : use0) + g; };
-        auto wait_pv = [&](int g) { return wait_bounded(pv_done(barriers(g)), use_of(g) & 1, abort_flag); };
+        auto wait_pv = [&](int g) { return wait(pv_done(barriers(g)), use_of(g) & 1); };
         while (next_unit()) {
             const int nt = tiles_of(x);
             // (rows past the item's compute something nobody reads)
@@ -893,7 +899,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
             const float before = kJoined && whole && mine ? a.before_lse[row] : -INFINITY;
             for (int g = 0; g < nt; ++g) {
-                ok = wait_bounded(s_full(barriers(g)), use_of(g) & 1, abort_flag);
+                ok = wait(s_full(barriers(g)), use_of(g) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -1282,6 +1288,7 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     a.rows = cross_rows(B, H, total_q, total_k);
     a.scale_log2 = softmax_scale * kLog2e;
     a.positions = positions;
+    a.wait_cycles = wait_limit() + kCrWaitPerTile * ((total_k + kCrTile - 1) / kCrTile);
     a.before_out = before_out;
     a.before_lse = before_lse;
     a.out = out_dtype == MLA_OUT_FP32 ? (float *)out : nullptr;

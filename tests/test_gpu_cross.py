@@ -455,3 +455,19 @@ def test_a_workspace_of_any_content():
         assert ops.status(ws) == 0
         ops.plan_cross(ws, bad, c.d_cu[1], c.nk, causal=True)
         assert ops.status(ws) == 5
+
+
+@pytest.mark.parametrize("q,k,H,rows", [(19456, 16384, 1, 128), (4864, 65536, 8, 256)])
+def test_waits_for_long_units_have_longer_limits(q, k, H, rows):
+    # one role waits for as long as another one's unit takes: 128 key tiles of some 2,000 cycles, 512 of 3,600, while
+    # the limit by itself is 50,000
+    c = Case([q], [k], H, False, 61, device="cuda").cuda()
+    want = c.run()
+    assert int(c.ws.buf[24:28].view(torch.int32)) == rows and int(c.ws.buf[36:40].view(torch.int32)) == 0  # none is cut
+    ops.set_wait_limit(50_000)
+    try:
+        got = c.run(ws=c.ws)
+        assert ops.status(c.ws) == 0
+    finally:
+        ops.set_wait_limit(0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
