@@ -121,8 +121,8 @@ const char *mla_status_string(mla_status status);
  * MLA_ERR_INVALID_ARG for a negative limit. */
 mla_status mla_decode_set_wait_limit(int64_t cycles);
 
-/* Test hook for the timeout path: while enabled (enable != 0), every decode call made
- * afterwards in this process has its tensor-core issuer wait, before it issues anything,
+/* Test hook for the timeout path: while enabled (enable != 0), every decode call and every
+ * mla_cross_attention made afterwards in this process has its tensor-core issuer wait, before it issues anything,
  * on a barrier that nothing ever completes.  That wait runs out after the wait limit
  * above, the call records MLA_ERR_TIMEOUT and winds down as described there, and the
  * device stays usable.  It exists so that tests can make a wait run out on purpose without

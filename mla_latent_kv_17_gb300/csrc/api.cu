@@ -416,6 +416,7 @@ mla_status run_decode(const DecodeArgs &a, cudaStream_t stream) {
 }  // namespace
 
 long long wait_limit() { return g_wait_cycles.load(); }
+bool stall_wanted() { return g_stall_test.load() != 0; }
 
 }  // namespace mla
 

@@ -477,6 +477,7 @@ struct CrossArgs {
     float scale_log2;
     int positions;
     long long wait_cycles;  // limit of a wait
+    int stall;              // tests: the MMA warp first waits for a barrier that nothing completes
     const float *before_out, *before_lse;
     float *out;       // one of the two
     uint16_t *out16;
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     auto o_free = [&](int x) { return bars + 256u + 8u * x; };
     auto u_full = [&](int j) { return bars + 272u + 8u * j; };
     auto u_empty = [&](int j) { return bars + 288u + 8u * j; };
-    const uint32_t q_full = bars + 304, q_empty = bars + 312;
+    const uint32_t q_full = bars + 304, q_empty = bars + 312, never = bars + 432;
     CrossPiece *slots = reinterpret_cast<CrossPiece *>(gbase + S::kOffBar + 320);  // two of 48 bytes
     int *abort_flag = reinterpret_cast<int *>(gbase + S::kOffBar + 416);
     volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(gbase + S::kOffBar + 424);
@@ -604,6 +605,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             mbar_init(q_full, 1);
             mbar_init(q_empty, 1);
+            mbar_init(never, 1);
             *abort_flag = 0;
             fence_mbar_init();
         }
@@ -806,6 +808,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         // descriptors but for their addresses: keys and queries (K-major), values (MN-major)
         const uint64_t desc_k = smem_desc_sw128(0, 16u, 1024u), desc_v = smem_desc_sw128(0, kCrBox / 2, 1024u);
         int units = 0, t = 0, ou[2] = {0, 0};  // units with keys, their key tiles, units of each query tile
+        if (a.stall) ok = wait_w(never, 0);
         while (next_unit()) {
             const int n0 = tiles_of(0), n1 = kTiles == 2 ? tiles_of(1) : 0, ntot = max(n0, n1);
             if (ntot == 0) continue;
@@ -1291,6 +1294,7 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     a.scale_log2 = softmax_scale * kLog2e;
     a.positions = positions;
     a.wait_cycles = wait_limit() + kCrWaitPerTile * ((total_k + kCrTile - 1) / kCrTile);
+    a.stall = stall_wanted();
     a.before_out = before_out;
     a.before_lse = before_lse;
     a.out = out_dtype == MLA_OUT_FP32 ? (float *)out : nullptr;

@@ -12,7 +12,9 @@ cudaError_t launch_decode_sm103(const DecodeArgs &a, int num_clusters, cudaStrea
 // Clusters of that kernel that fit on the current device at once (0 if unknown).
 int sm103_max_units();
 
-// Limit of a pipeline wait, in SM clock cycles (mla_decode_set_wait_limit).
+// Limit of a pipeline wait, in SM clock cycles (mla_decode_set_wait_limit), and whether tests want one to run out
+// (mla_decode_inject_stall).
 long long wait_limit();
+bool stall_wanted();
 
 }  // namespace mla

@@ -445,7 +445,7 @@ def set_wait_limit(cycles: int = 0) -> None:
 
 
 def inject_stall(enable: bool) -> None:
-    """Test hook: while enabled, decode calls make their MMA issuer wait on a barrier that
+    """Test hook: while enabled, decode and cross_attention calls make their MMA issuer wait on a barrier that
     nothing completes, so that the wait runs out (MLA_ERR_TIMEOUT) without any fault."""
     _check("mla_decode_inject_stall", lib().mla_decode_inject_stall(1 if enable else 0))
 

@@ -471,3 +471,40 @@ def test_waits_for_long_units_have_longer_limits(q, k, H, rows):
     finally:
         ops.set_wait_limit(0)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H,causal,before,kind", [
+    ([5, 200], [3000, 129], 3, True, False, "cut"), ([70, 1], [100, 0], 2, False, True, "whole"),
+    ([1001], [3400], 128, True, False, "pairs"), ([512], [16384], 128, False, True, "pairs")])
+def test_a_wait_that_runs_out(q_lens, k_lens, H, causal, before, kind):
+    # the MMA warps wait for a barrier that nothing completes: the call is recorded, its kernels return and write inside
+    # their arrays, and the plan has to be made again
+    c = Case(q_lens, k_lens, H, True, 62, before=before, device="cuda").cuda()
+    want = c.run(causal)
+    assert ops.status(c.ws) == 0
+    assert (int(c.ws.buf[24:28].view(torch.int32)) == 256) == (kind == "pairs")
+    assert kind != "cut" or int(c.ws.buf[36:40].view(torch.int32)) > 0
+    ws = ops.CrossWorkspace(c.B, H, c.nq)
+    g = [Guarded(ws.nbytes), Guarded(c.nq * H * 512), Guarded(c.nq * H * 4)]
+    ws.buf = g[0].inner
+    out, lse = g[1].inner.view(torch.float32).view(c.nq, H, 128), g[2].inner.view(torch.float32).view(c.nq, H)
+    ops.plan_cross(ws, *c.d_cu, c.nk, causal=causal)
+    call = lambda: ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale, before=c.before, out=out, lse=lse)
+    ops.set_wait_limit(2_000_000)  # about a millisecond
+    ops.inject_stall(True)
+    try:
+        call()
+        assert ops.status(ws) == 6
+    finally:
+        ops.inject_stall(False)
+        ops.set_wait_limit(0)
+    out.fill_(5)
+    lse.fill_(5)
+    call()  # without a new plan: refused, and nothing written
+    assert ops.status(ws) == 3
+    assert bool((out == 5).all()) and bool((lse == 5).all())
+    for _ in range(2):
+        got = c.run(causal, ws=ws, out=out, lse=lse)
+        assert ops.status(ws) == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for b in g:
+        b.check("after a wait that ran out")
