@@ -111,8 +111,8 @@ const char *mla_status_string(mla_status status);
 
 /* Limit, in SM clock cycles, of every pipeline wait inside the decode kernel, for the
  * mla_decode / mla_decode_sparse / mla_decode_static / mla_decode_tree calls made after it in this
- * process, and of mla_cross_attention's, which wait up to 8,000 cycles more for each 128 keys of
- * total_k (0 restores the default, about two seconds).  A wait that runs out records
+ * process; and of those waits of mla_cross_attention that may last as long as one of its pieces of
+ * work, which wait up to 8,000 cycles more for each 128 keys of total_k (0 restores the default, about two seconds).  A wait that runs out records
  * MLA_ERR_TIMEOUT in the status word; the kernel then stops issuing work, gives copies and
  * tensor-core operations already in flight a bounded time to land, releases its tensor
  * memory and returns, so the device and the workspace stay usable (the call's out and lse

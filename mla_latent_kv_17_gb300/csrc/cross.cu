@@ -476,7 +476,7 @@ struct CrossArgs {
     int B, H, total_q, total_k, rows;
     float scale_log2;
     int positions;
-    long long wait_cycles;  // limit of a wait
+    long long wait_cycles;  // limit of a wait that may last as long as a unit
     int stall;              // tests: the MMA warp first waits for a barrier that nothing completes
     const float *before_out, *before_lse;
     float *out;       // one of the two
@@ -625,7 +625,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     if (!match && threadIdx.x == 0) record_error(status, MLA_ERR_WORKSPACE);
     const int step = hd->causal ? 1 : 0;
     bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, abort_flag, a.wait_cycles); };
+    // For the next unit, a slot for it, a unit's last values, and as the second of two query tiles, which has no rows in some
+    // units, for its first scores, a role may wait as long as a unit takes.  (All waits with a limit that is no constant:
+    // 1 % of short units.)
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, abort_flag); };
+    auto wait_long = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, abort_flag, a.wait_cycles); };
 
     // The next unit's piece, from its slot (the whole warp); false: there is none, or a wait ran out.
     int taken = 0;
@@ -633,7 +637,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     auto next_unit = [&]() -> bool {
         if (!ok) return false;
         const int j = taken & 1;
-        ok = __all_sync(0xffffffffu, wait(u_full(j), (taken >> 1) & 1));
+        ok = __all_sync(0xffffffffu, wait_long(u_full(j), (taken >> 1) & 1));
         if (!ok) return false;
         p = slots[j];
         __syncwarp();
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int total = first + hd->pieces * cut_heads;
             for (int i = 0; ok; ++i) {
                 const int j = i & 1;
-                if (i >= 2) ok = wait(u_empty(j), ((i >> 1) - 1) & 1);
+                if (i >= 2) ok = wait_long(u_empty(j), ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 const int u = atomicAdd(&counters[0], 1);
                 CrossPiece d;
@@ -782,7 +786,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             t += ntot;
             const int valid = p.nk - (p.g0 + ntot - 1) * kCrTile;  // keys of the last tile
             if (ntot == 0 || valid >= kCrTile) continue;
-            ok = __all_sync(0xffffffffu, wait(landed(tails), (tails >> 2) & 1));
+            ok = __all_sync(0xffffffffu, wait_long(landed(tails), (tails >> 2) & 1));
             if (!ok) break;
             ++tails;
             for (int i = 0; i < 2; ++i) {
@@ -801,14 +805,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         // ---------------------------------------------------------------- MMAs
         // the whole warp runs the issue loop (its waits made warp-uniform); one elected lane issues
         auto wait_w = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_quick(bar, parity, abort_flag, a.wait_cycles));
+            return __all_sync(0xffffffffu, wait_quick(bar, parity, abort_flag));
         };
         constexpr uint32_t idesc_s = idesc_bf16_major(128, kCrTile, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_major(128, kCrDh, false, true);
         // descriptors but for their addresses: keys and queries (K-major), values (MN-major)
         const uint64_t desc_k = smem_desc_sw128(0, 16u, 1024u), desc_v = smem_desc_sw128(0, kCrBox / 2, 1024u);
         int units = 0, t = 0, ou[2] = {0, 0};  // units with keys, their key tiles, units of each query tile
-        if (a.stall) ok = wait_w(never, 0);
+        if (a.stall) ok = __all_sync(0xffffffffu, wait_long(never, 0));
         while (next_unit()) {
             const int n0 = tiles_of(0), n1 = kTiles == 2 ? tiles_of(1) : 0, ntot = max(n0, n1);
             if (ntot == 0) continue;
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int64_t row = (int64_t)(p.q0 + r) * a.H + p.head;
             const float before = kJoined && whole && mine ? a.before_lse[row] : -INFINITY;
             for (int g = 0; g < nt; ++g) {
-                ok = wait(s_full(barriers(g)), use_of(g) & 1);
+                ok = kTiles == 2 ? wait_long(s_full(barriers(g)), use_of(g) & 1) : wait(s_full(barriers(g)), use_of(g) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();

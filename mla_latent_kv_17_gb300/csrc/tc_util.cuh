@@ -33,8 +33,8 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int 
 }
 // The same with the first probe inline, for an issuing thread whose barriers have mostly
 // completed already (one try_wait then, no call and no clock read).
-__device__ __forceinline__ bool wait_quick(uint32_t bar, uint32_t parity, int *abort_flag, long long limit = kWaitCycles) {
-    return ptx::mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag, limit);
+__device__ __forceinline__ bool wait_quick(uint32_t bar, uint32_t parity, int *abort_flag) {
+    return ptx::mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag);
 }
 
 // Gives copies or MMAs still in flight a bounded time to land before the CTA leaves.

@@ -439,8 +439,8 @@ def decode_static(q_nope, q_rope, cache, block_table, seq_lens, softmax_scale: f
 
 
 def set_wait_limit(cycles: int = 0) -> None:
-    """Limit of every pipeline wait of the decode kernel, and of cross_attention's (more there for many
-    keys), in SM clock cycles, for later calls (0 restores the default of about two seconds)."""
+    """Limit of every pipeline wait of the decode kernel, and of cross_attention's long ones (more there
+    for many keys), in SM clock cycles, for later calls (0 restores the default of about two seconds)."""
     _check("mla_decode_set_wait_limit", lib().mla_decode_set_wait_limit(int(cycles)))
 
 
