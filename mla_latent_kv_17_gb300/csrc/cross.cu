@@ -10,10 +10,14 @@
 // cross_kernel: a persistent CTA per SM takes units (a piece and a head) from a counter, longest
 // pieces first, groups of eight heads in turn so that the keys and values in use stay in L2.  Per
 // unit, as in the causal prefill: S = Q K^T on tcgen05 into TMEM, online softmax with one thread per
-// query row, P as bf16 over its scores in TMEM, O += P V.  The loads and first scores of the next unit
-// run under the last softmax and the epilogue of the present one.
+// query row, P as bf16 over its scores in TMEM, O += P V.  The loads of the next unit run under the last
+// tiles of the present one, its first scores under the epilogue.
+//   P is rounded to bf16 because the MMA takes both operands in one type and the values are bf16 (fp16 would not hold
+// them; P in two bf16 parts would double PV).  That is up to 2^-8 of each weight: with the result's own rounding to
+// bf16 the error is 0.0022 - 0.0023 of the result (rms) where fp32 weights would give 0.0017.  The sum of weights is
+// taken before the rounding, in fp32.
 //   256 rows, for many long runs: two query tiles share the keys and take turns on the tensor pipe.  1,001 queries over 9,193 keys,
-//   causal, 128 heads: 497 us with plan and joining, 0.76 of the measured bf16 rate (466 us, 0.82, by itself).  A key
+//   causal, 128 heads: 490 - 500 us with plan and joining, 0.75 of the measured bf16 rate (466 us, 0.80, by itself).  A key
 //   tile takes 3,650 cycles where its MMAs take 2,560: the warp that issues them is the narrowest place (about 60
 //   cycles an operation, and 120 a wait, even where there is nothing to wait for), then shared memory (8 KB of
 //   operands in the 64 cycles of a score operation).
@@ -111,7 +115,11 @@ constexpr size_t kCrCounters = 192;  // next unit, CTAs that are done
 // 8 x 1,024 x 2,048 x 32 290 / 254, 1 x 256 x 16,000 x 128 347 / 297; sooner: 2 x 2,048 x 16,384 x 8 305 / 234,
 // 9 x 256 x 2,000 x 16 73 / 54, 2 x 1,024 x 6,000 x 32 209 / 187, 1 x 2,048 x 8,192 x 16 causal 134 / 126; not sooner:
 // 1 x 512 x 4,096 x 40 61 / 88, 1 x 1,024 x 4,000 x 16 43 / 65; causal, keys twice the queries: 2 x 2,048 x 4,096 x 16
-// 123 / 152; short keys: 4 x 512 x 1,024 x 128 154 / 181; half-empty pairs: 8 x 300 x 4,000 x 64 451 / 467.
+// 123 / 152; half-empty pairs: 8 x 300 x 4,000 x 64 451 / 467; short keys: 4 x 512 x 1,024 x 128 154 / 156,
+// 8 x 1,024 x 1,024 x 32 152 / 147, 8 x 1,024 x 500 x 32 97 / 101, 8 x 1,024 x 200 x 32 68 / 73, 8 x 3,384 x 38 x 32
+// 161 / 148, joined 8 x 1,750 x 13 x 64 277 / 297.  Where the average hides much, the other size may be better: 8 ragged
+// causal runs of 200 - 1,024 queries over 1,024 - 2,048 keys x 32 heads 142 / 154 (256 rows, by the 192 MB), over
+// 1,024 - 8,192 473 / 450.
 // When this many units of this length would end, in key tiles: whole ones in rounds, or cut (see the plan).
 MLA_HD float cross_end(int64_t units, float length) {
     const float rounds = (float)((units + kCrSms - 1) / kCrSms) * length, cut = 1.1f * units * length / kCrSms + kCrJoin;
@@ -551,8 +559,8 @@ __device__ __forceinline__ bool plan_fits(const CrossArgs &a, const CrossHeader 
            cross_layout(a.B, a.H, a.total_q, hd->sms).total <= a.ws_bytes;
 }
 
-// kJoined: with an earlier part's result.  (A kernel of its own: without, 8 x 3,384 queries x 38 keys x 32 heads take
-// 155 us instead of 161 - 165.)
+// kJoined: with an earlier part's result.  (A kernel of its own: in one kernel for both, calls without an earlier part
+// took 4 - 6 % longer where units are short; 8 x 3,384 queries x 38 keys x 32 heads take 161 us.)
 template <int kTiles, bool kJoined>
 __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     cross_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qr,
@@ -1002,7 +1010,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             };
             if (kJoined && kTiles == 1 && whole) {
                 // the earlier part's row is on its way while PV finishes (what has no weight may hold anything; 8 x 1,750
-                // queries x 13 keys x 64 heads 374 -> 318 us)
+                // queries x 13 keys x 64 heads 374 -> 318 us in fp32 without positions; in bf16 272, with positions 277)
                 float e[kCrDh];
 #pragma unroll
                 for (int i = 0; i < kCrDh; ++i) e[i] = 0.f;

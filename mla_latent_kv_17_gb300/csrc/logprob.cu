@@ -15,11 +15,12 @@
 // A CTA takes a row after the other, the next one's first loads under the end of the present one; with few
 // rows a cluster of up to eight CTAs shares one, its parts joined through distributed shared memory.
 //
-// 4,096 rows of 131,072 bf16 logits: 157 us for the sums alone (1.07 GB, a copy's rate), 179 with ranks of random
-// tokens (160 where all are the best), 195 with the best alternative too, 203 with 20: issue slots are 60 % busy, and a
-// row's end is a chain.  16-bit logits are therefore compared and clamped in pairs, and summed in packed fp32, and a
-// batch is read while the one before is worked on (211 -> 201 us).  The same bytes in fp32: 180 us.  Few rows: 9 us, a
-// chain of the loads, the joins and (with several CTAs) two cluster barriers.
+// 4,096 rows of 131,072 bf16 logits: 155 us for the sums alone (1.07 GB, a copy's rate), 176 with ranks of random
+// tokens (159 where all are the best), 193 with the best alternative too, 201 with 20: issue slots are 60 % busy, and a
+// row's end is a chain.  16-bit logits are therefore compared in pairs (bf16 ones clamped in pairs, too), and summed in
+// packed fp32, and a batch is read while the one before is worked on (211 -> 201 us).  fp16, whose values are clamped one
+// by one, as its range does not hold every limit: 186 us with ranks, 210 with 20 alternatives.  The same bytes in fp32:
+// 159 and 177.  Few rows: 9 us, a chain of the loads, the joins and (with several CTAs) two cluster barriers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,14 +37,15 @@ namespace {
 constexpr int kLpSms = 152;          // a GB300's; only the grid's shape depends on it
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-// 16-byte units of a thread in flight together, and CTAs per SM: 4,096 rows of 131,072 without alternatives 189 us;
-// 4 and 4: 236, 12 and 2: 226, 16 and 2: 198
+// 16-byte units of a thread in flight together, and CTAs per SM: 4,096 rows of 131,072 without and with 20 alternatives
+// 176 and 201 us; 4 and 4: 184 and 213, 12 and 2: 203 and 258, 16 and 2: 187 and 243
 constexpr int kLpBatch = 8;
 constexpr int kLpCtas = 3;
 constexpr int kLpMaxTop = 64;
 constexpr int kCandidates = 1024;   // at least kLpMaxTop units' values
 constexpr int kListed = 1024;       // batches that are read again
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpShared = 2;        // CTAs per SM up to which rows are shared (see launch_logprobs)
 constexpr unsigned kFull = 0xffffffffu;
 
 struct LogprobArgs {
@@ -630,11 +632,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(LogprobArg
 
 template <typename T>
 mla_status launch_logprobs(LogprobArgs a, int64_t N, cudaStream_t stream) {
-    // CTAs per row: as many as the SMs take at once while each thread still has a batch of units (16 rows of 131,072:
-    // 8.7 us with four CTAs each, 18 with one)
+    // CTAs per row: twice as many while all rows' come to two per SM at most and each thread still has a batch of units.
+    // Rows of 131,072 bf16 logits with 5 alternatives, us with 1, 2, 4 and 8 CTAs a row (* what the rule takes): 1 row 11.6,
+    // 9.9, 8.7, 8.2*; 16 rows 11.9, 10.3, 9.1, 8.8*; 40 rows 12.0, 10.6, 10.0*, with three per SM 10.5; 100 rows 12.2, 13.0*,
+    // with three per SM 12.7 for 4; 152 rows 15.4, 17.5*.  (Two a row cost 1 - 2 us where every SM has a row of its own.)
     const int64_t units = ((int64_t)a.V + T::kUnit - 1) / T::kUnit;
     int parts = 1;
-    while (parts < kLpMaxCluster && N * parts * 2 <= 304 && units >= 2 * parts * kLpThreads * kLpBatch) parts *= 2;
+    while (parts < kLpMaxCluster && N * parts * 2 <= kLpShared * kLpSms && units >= 2 * parts * kLpThreads * kLpBatch) parts *= 2;
     const int64_t rows = N * parts <= kLpSms * kLpCtas ? N : kLpSms * kLpCtas / parts;  // at once
     a.parts = parts;
     a.N = N;

@@ -885,7 +885,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniforms, parents=None
 
 class CrossWorkspace(_Memory):
     """Device workspace of a cross attention of B query runs of H heads, total_q query rows in all: its
-    plan, partial results and status word (status() reads it)."""
+    plan, partial results (up to 147 MiB on 152 SMs) and status word (status() reads it)."""
 
     def __init__(self, B: int, H: int, total_q: int, num_sms: int = 0, device=None):
         self.B, self.H, self.total_q, self.num_sms = int(B), int(H), int(total_q), int(num_sms)
