@@ -424,7 +424,8 @@ mla_status mla_verify_draft(const float *target, const float *draft, const int32
  * mla_decode_status reads: runs that fall or lie outside are moved up or in and recorded as
  * MLA_ERR_INDEX.  The workspace may hold anything before its first plan, which sets the status word up;
  * later plans keep an error that has not been read.  After MLA_ERR_TIMEOUT the plan has to be made
- * again.  num_sms as for mla_decode_plan, the same in the first two calls.  The workspace has room for
+ * again.  num_sms as for mla_decode_plan (the SMs that the attention runs on; joining its cut pieces
+ * takes all), the same in the first two calls.  The workspace has room for
  * partial results whatever the keys are, (3 num_sms + H) x min(total_q, 512) x 516 bytes (152 SMs: 15 MiB
  * for 64 queries x 16 heads, 119 MiB for 512 and more, 147 MiB for those of 128 heads), and for the
  * plan's lists.  1 <= B <= 2^20, total_q <= 2^24, total_k < 2^31 - 128, 1 <= H <= 128; workspace and

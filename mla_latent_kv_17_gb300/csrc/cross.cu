@@ -698,7 +698,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 const int j = i & 1;
                 if (i >= 2) ok = wait_long(u_empty(j), ((i >> 1) - 1) & 1);
                 if (!ok) break;
-                const int u = atomicAdd(&counters[0], 1);
+                // (a CTA beyond the SMs that the plan is for takes none)
+                const int u = (int)blockIdx.x < hd->sms ? atomicAdd(&counters[0], 1) : total;
                 CrossPiece d;
                 d.head = -1;
                 if (u < total) {

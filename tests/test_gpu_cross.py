@@ -508,3 +508,24 @@ def test_a_wait_that_runs_out(q_lens, k_lens, H, causal, before, kind):
         assert ops.status(ws) == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     for b in g:
         b.check("after a wait that ran out")
+
+
+def test_the_plan_says_how_many_sms_may_be_used():
+    # 320 units of one length take 3 rounds of 152 SMs, and 40 of 8
+    c = Case([2560], [1024], 16, True, 63, device="cuda").cuda()
+    want = c.run()
+
+    def took(sms):
+        ws = ops.CrossWorkspace(c.B, c.H, c.nq, num_sms=sms)
+        c.check(c.run(ws=ws), heads=[0, 15])
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        times = []
+        for _ in range(3):
+            a.record()
+            ops.cross_attention(ws, c.q_nope, c.q_rope, c.entries, c.k_nope, c.v, c.scale, out=want[0], lse=want[1])
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    assert took(8) > 4 * took(0)
