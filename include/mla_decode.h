@@ -112,18 +112,18 @@ const char *mla_status_string(mla_status status);
 /* Limit, in SM clock cycles, of every pipeline wait inside the decode kernel, for the
  * mla_decode / mla_decode_sparse / mla_decode_static / mla_decode_tree calls made after it in this
  * process; and of those waits of mla_cross_attention that may last as long as one of its pieces of
- * work, which wait up to 8,000 cycles more for each 128 keys of total_k (0 restores the default, about two seconds).  A wait that runs out records
- * MLA_ERR_TIMEOUT in the status word; the kernel then stops issuing work, gives copies and
- * tensor-core operations already in flight a bounded time to land, releases its tensor
- * memory and returns, so the device and the workspace stay usable (the call's out and lse
- * are then undefined).  The default is far above any healthy wait; a tiny limit makes
+ * work, which wait up to 8,000 cycles more for each 128 keys of total_k (its others have the default).
+ * 0 restores the default, about two seconds.  A wait that runs out records MLA_ERR_TIMEOUT in the
+ * status word; the kernel then stops issuing work, gives copies and tensor-core operations already
+ * in flight a bounded time to land, releases its tensor memory and returns, so the device and the
+ * workspace stay usable (the call's out and lse are then undefined).  The default is far above any healthy wait; a tiny limit makes
  * waits run out on purpose, which is how the timeout path is tested.  Returns
  * MLA_ERR_INVALID_ARG for a negative limit. */
 mla_status mla_decode_set_wait_limit(int64_t cycles);
 
 /* Test hook for the timeout path: while enabled (enable != 0), every decode call and every
- * mla_cross_attention made afterwards in this process has its tensor-core issuer wait, before it issues anything,
- * on a barrier that nothing ever completes.  That wait runs out after the wait limit
+ * mla_cross_attention made afterwards in this process has its tensor-core issuer wait, before it
+ * issues anything, on a barrier that nothing ever completes.  That wait runs out after the wait limit
  * above, the call records MLA_ERR_TIMEOUT and winds down as described there, and the
  * device stays usable.  It exists so that tests can make a wait run out on purpose without
  * any fault; production code leaves it disabled (the default). */

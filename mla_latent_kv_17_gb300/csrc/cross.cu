@@ -1306,7 +1306,8 @@ extern "C" mla_status mla_cross_attention(void *workspace, size_t ws_bytes, cons
     a.rows = cross_rows(B, H, total_q, total_k);
     a.scale_log2 = softmax_scale * kLog2e;
     a.positions = positions;
-    a.wait_cycles = wait_limit() + kCrWaitPerTile * ((total_k + kCrTile - 1) / kCrTile);
+    const long long more = kCrWaitPerTile * ((total_k + kCrTile - 1) / kCrTile), limit = wait_limit();
+    a.wait_cycles = limit < INT64_MAX - more ? limit + more : INT64_MAX;
     a.stall = stall_wanted();
     a.before_out = before_out;
     a.before_lse = before_lse;

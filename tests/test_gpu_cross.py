@@ -529,3 +529,12 @@ def test_the_plan_says_how_many_sms_may_be_used():
         return min(times)
 
     assert took(8) > 4 * took(0)
+
+
+def test_the_largest_limit_of_a_wait():
+    c = Case([5, 200], [3000, 129], 3, True, 64).cuda()
+    ops.set_wait_limit(2 ** 63 - 1)
+    try:
+        c.check(c.run())
+    finally:
+        ops.set_wait_limit(0)
